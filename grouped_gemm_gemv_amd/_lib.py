@@ -35,6 +35,8 @@ EXPORTED = [
     "moe_ffn_gate_up", "moe_ffn_gate_up_gather", "moe_ffn_down", "moe_grouped_ffn", "moe_combine",
     "moe_forward", "moe_ffn_gate_up_fp8", "moe_ffn_down_fp8", "moe_forward_fp8", "moe_pack_blocked16",
     "moe_forward_noalloc",
+    "moe_backward_query", "moe_saved8_carve", "moe_ffn_gate_up_save8", "moe_saved8_unpack", "moe_combine_backward",
+    "moe_permute_backward", "moe_route_backward", "moe_grouped_ffn_backward", "moe_forward_save8", "moe_backward",
 ]
 
 
@@ -62,6 +64,17 @@ class MoeForwardViews(ctypes.Structure):
                 ("h", c_ptr), ("y_perm", c_ptr)]
 
 
+class MoeBackwardSizes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in ("saved8_bytes", "route_ws_bytes", "ffn_ws_bytes", "backward_ws_bytes")]
+
+
+SAVED8_ARRAYS = ["gate", "up", "gate_exp", "up_exp"]
+
+
+class MoeSaved8(ctypes.Structure):
+    _fields_ = [(n, c_ptr) for n in SAVED8_ARRAYS]
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn: str, status: int, msg: str):
         super().__init__(f"{fn} failed: {msg}")
@@ -76,6 +89,7 @@ def _declare(lib):
     P = ctypes.POINTER
     S = P(MoeShape)
     D = P(MoeDispatch)
+    V = P(MoeSaved8)
     lib.moe_status_string.argtypes = [ctypes.c_int]
     lib.moe_status_string.restype = ctypes.c_char_p
     sig = {
@@ -98,6 +112,16 @@ def _declare(lib):
         "moe_pack_blocked16": [c_ptr, c_ptr, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, c_ptr],
         "moe_forward_noalloc": [S, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr,
                                 P(MoeForwardViews), c_ptr],
+        "moe_backward_query": [S, P(MoeBackwardSizes)],
+        "moe_saved8_carve": [S, c_ptr, ctypes.c_size_t, V],
+        "moe_ffn_gate_up_save8": [S, c_ptr, c_ptr, c_ptr, D, ctypes.c_int, c_ptr, V, c_ptr],
+        "moe_saved8_unpack": [S, V, D, c_ptr, c_ptr, c_ptr],
+        "moe_combine_backward": [S, c_ptr, c_ptr, c_ptr, D, c_ptr, c_ptr, c_ptr],
+        "moe_permute_backward": [S, c_ptr, D, c_ptr, c_ptr],
+        "moe_route_backward": [S] + [c_ptr] * 9 + [ctypes.c_size_t, c_ptr],
+        "moe_grouped_ffn_backward": [S] + [c_ptr] * 6 + [D, V] + [c_ptr] * 6 + [ctypes.c_size_t, c_ptr],
+        "moe_forward_save8": [S] + [c_ptr] * 9 + [D, V, c_ptr, ctypes.c_size_t, c_ptr],
+        "moe_backward": [S] + [c_ptr] * 7 + [D, V] + [c_ptr] * 9 + [ctypes.c_size_t, c_ptr],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)

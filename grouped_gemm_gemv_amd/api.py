@@ -14,7 +14,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import MoeDispatch, MoeForwardViews, MoeShape, MoeSizes, check, lib
+from ._lib import (MoeBackwardSizes, MoeDispatch, MoeForwardViews, MoeSaved8, MoeShape, MoeSizes, check, lib)
 
 _DT = {torch.float32: _lib.MOE_F32, torch.bfloat16: _lib.MOE_BF16}
 _TORCH_DT = {v: k for k, v in _DT.items()}
@@ -246,3 +246,182 @@ def moe_forward_noalloc(shape: Shape, x, w_router, bias, topk_ids, topk_w, w_gat
         ctypes.byref(shape.c()), _p(x), _p(w_router), _p(bias), _p(topk_ids), _p(topk_w), _p(w_gate), _p(w_up),
         _p(w_down), _p(out), ctypes.byref(v), _stream(stream)))
     return v
+
+
+# ---- backward pass ----
+
+
+def _in(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype, device) -> Optional[int]:
+    """Device address of a tensor that must have this shape and type, contiguous on `device`; None stays None."""
+    if t is None:
+        return None
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {list(shape)} of {dtype}, got {list(t.shape)} of {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return _p(t)
+
+
+def _disp(disp: Dispatch, shape: Shape, device):
+    """The C dispatch of a Dispatch that was made for this shape (its storage order and tile height aside)."""
+    mine, other = disp.shape, shape
+    if (mine.T, mine.E, mine.k, mine.capacity) != (other.T, other.E, other.k, other.capacity):
+        raise ValueError(f"disp was made for {mine}")
+    if disp.buf.device != device:
+        raise ValueError(f"disp is on {disp.buf.device}, expected {device}")
+    return ctypes.byref(disp.c)
+
+
+def _weights(shape: Shape, prefix: str, gate, up, down, device):
+    s = shape
+    return (_in(gate, prefix + "_gate", (s.E, s.F, s.d), s.dtype, device),
+            _in(up, prefix + "_up", (s.E, s.F, s.d), s.dtype, device),
+            _in(down, prefix + "_down", (s.E, s.d, s.F), s.dtype, device))
+
+
+def _ws(ws: torch.Tensor, device):
+    if ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, expected {device}")
+    return _p(ws), ws.numel() * ws.element_size()
+
+
+def _call(name: str, device, stream, *args):
+    """One entry point on the tensors' device, on `stream` or that device's current stream."""
+    if device.type != "cuda":
+        raise ValueError("libmoe takes device tensors")
+    with torch.cuda.device(device):
+        s = stream if stream is not None else torch.cuda.current_stream(device)
+        check(name, getattr(lib(), name)(*args, s.cuda_stream))
+
+
+def backward_query(shape: Shape) -> MoeBackwardSizes:
+    """Bytes of the 8-bit projections and of the backward calls' workspaces (moe_backward_query)."""
+    out = MoeBackwardSizes()
+    check("moe_backward_query", lib().moe_backward_query(ctypes.byref(shape.c()), ctypes.byref(out)))
+    return out
+
+
+def backward_workspace_size(shape: Shape) -> int:
+    """Bytes of workspace moe_backward needs; enough for every other backward call."""
+    return backward_query(shape).backward_ws_bytes
+
+
+class Saved8:
+    """Device buffer of a layer's two projections in 8 bits (moe_saved8_t), with tensor views."""
+
+    def __init__(self, shape: Shape, device="cuda"):
+        self.shape = shape
+        n = backward_query(shape).saved8_bytes
+        self.buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
+        base = (self.buf.data_ptr() + 255) // 256 * 256
+        self.c = MoeSaved8()
+        check("moe_saved8_carve", lib().moe_saved8_carve(ctypes.byref(shape.c()), base, n, ctypes.byref(self.c)))
+
+    def arrays(self) -> dict:
+        """gate, up [R, F] int8 codes; gate_exp, up_exp [R, F / 16] uint8 exponents."""
+        R, F = query(self.shape).rows, self.shape.F
+
+        def view(ptr, cols, dtype):
+            off = ptr - self.buf.data_ptr()
+            return self.buf[off:off + R * cols].view(dtype).view(R, cols)
+
+        return {"gate": view(self.c.gate, F, torch.int8), "up": view(self.c.up, F, torch.int8),
+                "gate_exp": view(self.c.gate_exp, F // 16, torch.uint8),
+                "up_exp": view(self.c.up_exp, F // 16, torch.uint8)}
+
+
+def _saved(saved: Saved8, shape: Shape, device):
+    mine, other = saved.shape, shape
+    if (mine.T, mine.E, mine.k, mine.F, mine.capacity) != (other.T, other.E, other.k, other.F, other.capacity):
+        raise ValueError(f"saved was made for {mine}")
+    if saved.buf.device != device:
+        raise ValueError(f"saved is on {saved.buf.device}, expected {device}")
+    return ctypes.byref(saved.c)
+
+
+def moe_ffn_gate_up_save8(shape: Shape, x, w_gate, w_up, disp: Dispatch, pass_idx: int, h, saved: Saved8,
+                          stream=None):
+    """Gate+up over a pass (x [T, d] read through the dispatch) that also keeps both projections in 8 bits."""
+    s, dev = shape, x.device
+    wg, wu, _ = _weights(s, "w", w_gate, w_up, None, dev)
+    _call("moe_ffn_gate_up_save8", dev, stream, ctypes.byref(s.c()), _in(x, "x", (s.T, s.d), s.dtype, dev), wg, wu,
+          _disp(disp, s, dev), pass_idx, _in(h, "h", (query(s).rows, s.F), s.dtype, dev), _saved(saved, s, dev))
+
+
+def moe_saved8_unpack(shape: Shape, saved: Saved8, disp: Dispatch, gate, up, stream=None):
+    """The values the codes stand for, in bf16 (gate, up [R, F]); rows without a token are left as they are."""
+    s, dev = shape, gate.device
+    R = query(s).rows
+    _call("moe_saved8_unpack", dev, stream, ctypes.byref(s.c()), _saved(saved, s, dev), _disp(disp, s, dev),
+          _in(gate, "gate", (R, s.F), torch.bfloat16, dev), _in(up, "up", (R, s.F), torch.bfloat16, dev))
+
+
+def moe_combine_backward(shape: Shape, dout, y_perm, topk_w, disp: Dispatch, dy_perm, dtopk_w, stream=None):
+    """Gradient of moe_combine: dy_perm [R, d] and dtopk_w [T, k] (fp32)."""
+    s, dev = shape, dout.device
+    R = query(s).rows
+    _call("moe_combine_backward", dev, stream, ctypes.byref(s.c()), _in(dout, "dout", (s.T, s.d), s.dtype, dev),
+          _in(y_perm, "y_perm", (R, s.d), s.dtype, dev), _in(topk_w, "topk_w", (s.T, s.k), torch.float32, dev),
+          _disp(disp, s, dev), _in(dy_perm, "dy_perm", (R, s.d), s.dtype, dev),
+          _in(dtopk_w, "dtopk_w", (s.T, s.k), torch.float32, dev))
+
+
+def moe_permute_backward(shape: Shape, dx_perm, disp: Dispatch, dx, stream=None):
+    """Gradient of moe_permute's gather: dx [T, d] from dx_perm [R, d]."""
+    s, dev = shape, dx_perm.device
+    _call("moe_permute_backward", dev, stream, ctypes.byref(s.c()),
+          _in(dx_perm, "dx_perm", (query(s).rows, s.d), s.dtype, dev), _disp(disp, s, dev),
+          _in(dx, "dx", (s.T, s.d), s.dtype, dev))
+
+
+def moe_route_backward(shape: Shape, x, w_router, topk_ids, topk_w, dtopk_w, dx, dw_router, dbias, ws, stream=None):
+    """Gradient of moe_route from the routing weights' gradient; dbias may be None."""
+    s, dev = shape, x.device
+    tk = (s.T, s.k)
+    _call("moe_route_backward", dev, stream, ctypes.byref(s.c()), _in(x, "x", (s.T, s.d), s.dtype, dev),
+          _in(w_router, "w_router", (s.E, s.d), s.dtype, dev), _in(topk_ids, "topk_ids", tk, torch.int32, dev),
+          _in(topk_w, "topk_w", tk, torch.float32, dev), _in(dtopk_w, "dtopk_w", tk, torch.float32, dev),
+          _in(dx, "dx", (s.T, s.d), s.dtype, dev), _in(dw_router, "dw_router", (s.E, s.d), s.dtype, dev),
+          _in(dbias, "dbias", (s.E,), torch.float32, dev), *_ws(ws, dev))
+
+
+def moe_grouped_ffn_backward(shape: Shape, x, dout, topk_w, w_gate, w_up, w_down, disp: Dispatch, saved: Saved8,
+                             dx_perm, dtopk_w, dw_gate, dw_up, dw_down, ws, stream=None):
+    """Gradient of the experts' products from the 8-bit projections.  dw_gate and dw_up (both or neither) and
+    dw_down may be None: not computed."""
+    s, dev = shape, x.device
+    tk = (s.T, s.k)
+    _call("moe_grouped_ffn_backward", dev, stream, ctypes.byref(s.c()), _in(x, "x", (s.T, s.d), s.dtype, dev),
+          _in(dout, "dout", (s.T, s.d), s.dtype, dev), _in(topk_w, "topk_w", tk, torch.float32, dev),
+          *_weights(s, "w", w_gate, w_up, w_down, dev), _disp(disp, s, dev), _saved(saved, s, dev),
+          _in(dx_perm, "dx_perm", (query(s).rows, s.d), s.dtype, dev),
+          _in(dtopk_w, "dtopk_w", tk, torch.float32, dev), *_weights(s, "dw", dw_gate, dw_up, dw_down, dev),
+          *_ws(ws, dev))
+
+
+def moe_forward_save8(shape: Shape, x, w_router, bias, topk_ids, topk_w, w_gate, w_up, w_down, out, disp: Dispatch,
+                      saved: Saved8, ws, stream=None):
+    """The whole layer for training.  topk_ids and topk_w [T, k] are written where w_router is given, else read;
+    disp and saved receive what moe_backward needs."""
+    s, dev = shape, x.device
+    tk = (s.T, s.k)
+    _call("moe_forward_save8", dev, stream, ctypes.byref(s.c()), _in(x, "x", (s.T, s.d), s.dtype, dev),
+          _in(w_router, "w_router", (s.E, s.d), s.dtype, dev), _in(bias, "bias", (s.E,), torch.float32, dev),
+          _in(topk_ids, "topk_ids", tk, torch.int32, dev), _in(topk_w, "topk_w", tk, torch.float32, dev),
+          *_weights(s, "w", w_gate, w_up, w_down, dev), _in(out, "out", (s.T, s.d), s.dtype, dev),
+          _disp(disp, s, dev), _saved(saved, s, dev), *_ws(ws, dev))
+
+
+def moe_backward(shape: Shape, x, w_router, topk_ids, topk_w, w_gate, w_up, w_down, disp: Dispatch, saved: Saved8,
+                 dout, dx, dtopk_w, dw_router, dbias, dw_gate, dw_up, dw_down, ws, stream=None):
+    """The whole layer's backward pass after moe_forward_save8.  w_router None: the routing was the caller's, and
+    dw_router and dbias are None too."""
+    s, dev = shape, x.device
+    tk = (s.T, s.k)
+    _call("moe_backward", dev, stream, ctypes.byref(s.c()), _in(x, "x", (s.T, s.d), s.dtype, dev),
+          _in(w_router, "w_router", (s.E, s.d), s.dtype, dev), _in(topk_ids, "topk_ids", tk, torch.int32, dev),
+          _in(topk_w, "topk_w", tk, torch.float32, dev), *_weights(s, "w", w_gate, w_up, w_down, dev),
+          _disp(disp, s, dev), _saved(saved, s, dev), _in(dout, "dout", (s.T, s.d), s.dtype, dev),
+          _in(dx, "dx", (s.T, s.d), s.dtype, dev), _in(dtopk_w, "dtopk_w", tk, torch.float32, dev),
+          _in(dw_router, "dw_router", (s.E, s.d), s.dtype, dev), _in(dbias, "dbias", (s.E,), torch.float32, dev),
+          *_weights(s, "dw", dw_gate, dw_up, dw_down, dev), *_ws(ws, dev))

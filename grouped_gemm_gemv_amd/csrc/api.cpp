@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "launch.hpp"
 #include "moe.h"
@@ -384,8 +385,15 @@ constexpr int kWideMaxRows = 160;
 // from row r of x_perm.
 moe_status_t enqueue_gate_up(const moe_shape_t& s, const void* x_perm, const void* wg, const void* wu,
                              const moe_dispatch_t& d, int pass, void* h, hipStream_t st,
-                             const void* x_src = nullptr, const float* sg = nullptr, const float* su = nullptr) {
+                             const void* x_src = nullptr, const float* sg = nullptr, const float* su = nullptr,
+                             const moe_saved8_t* saved = nullptr) {
   moe::GemmArgs a = gemm_args(s, d, pass, true);
+  if (saved != nullptr) {
+    a.save_gate = saved->gate;
+    a.save_up = saved->up;
+    a.save_gate_exp = saved->gate_exp;
+    a.save_up_exp = saved->up_exp;
+  }
   a.s0 = sg;
   a.s1 = su;
   const int64_t mean = mean_rows(s);
@@ -434,6 +442,40 @@ moe_status_t enqueue_down(const moe_shape_t& s, const void* h, const void* wd, c
                                                 s.d, static_cast<char*>(y) + (size_t)r0 * s.d * elt_bytes(s), st));
 }
 
+// The layer's steps on validated arguments.  w_router null: ids and w are the
+// caller's routing; saved not null: the gate+up GEMM also keeps its projections.
+moe_status_t enqueue_layer(const moe_shape_t& s, const Plan& p, const void* x, const void* w_router, const float* bias,
+                           int32_t* ids, float* w, const void* w_gate, const void* w_up, const void* w_down,
+                           const float* s_gate, const float* s_up, const float* s_down, void* out,
+                           const moe_dispatch_t& disp, void* h, void* y, void* perm_ws, const moe_saved8_t* saved,
+                           hipStream_t stream) {
+  moe_status_t st;
+  if (w_router != nullptr && s.T <= moe::kRouteDispatchTokens && s.E <= 64) {
+    // a decode batch: routing and dispatch in one workgroup
+    if (moe::launch_route_dispatch(s.dtype, x, w_router, bias, s.T, s.d, s.E, s.k, ids, w,
+                                   small_dispatch_args(s, p, ids, disp), stream) != hipSuccess)
+      return MOE_ERR_HIP;
+  } else {
+    if (w_router != nullptr &&
+        moe::launch_route(s.dtype, x, w_router, bias, s.T, s.d, s.E, s.k, ids, w, stream) != hipSuccess)
+      return MOE_ERR_HIP;
+    if ((st = enqueue_permute(s, p, x, ids, disp, nullptr, perm_ws, stream)) != MOE_OK) return st;
+  }
+  // capacity mode: both passes in each launch (the overflow tiles of an expert
+  // run next to its first-pass tiles and find its weights in L2)
+  const int ps = s.capacity > 0 ? kBothPasses : 0;
+  if ((st = enqueue_gate_up(s, nullptr, w_gate, w_up, disp, ps, h, stream, x, s_gate, s_up, saved)) != MOE_OK)
+    return st;
+  const bool split = split_down(s, disp.tile_rows);
+  if (fused_down_combine(s, disp.tile_rows))  // a decode batch: the combine inside the down GEMM
+    return enqueue_down(s, h, w_down, disp, ps, y, stream, s_down, true, out, w);
+  if ((st = enqueue_down(s, h, w_down, disp, ps, y, stream, s_down, !split)) != MOE_OK) return st;
+  if (split)  // y formed from the two K ranges inside the combine
+    return hip_status(moe::launch_combine_split(s.dtype, disp.kpart, (size_t)p.R * s.d, w, disp.row_of, s.T, s.k, s.d,
+                                                y, out, stream));
+  return hip_status(moe::launch_combine(s.dtype, y, w, disp.row_of, s.T, s.k, s.d, out, stream));
+}
+
 // The whole layer; s_gate/s_up/s_down non-null: the weights are E4M3 codes.
 moe_status_t forward_impl(const moe_shape_t* s, const void* x, const void* w_router, const float* bias,
                           const int32_t* topk_ids_in, const float* topk_w_in, const void* w_gate, const void* w_up,
@@ -462,32 +504,169 @@ moe_status_t forward_impl(const moe_shape_t* s, const void* x, const void* w_rou
     v.topk_w = reinterpret_cast<float*>(ws + p.ws_w);
   }
   if (views_out != nullptr) *views_out = v;
-  if (topk_ids_in == nullptr && s->T <= moe::kRouteDispatchTokens && s->E <= 64) {
-    // a decode batch: routing and dispatch in one workgroup
-    if (moe::launch_route_dispatch(s->dtype, x, w_router, bias, s->T, s->d, s->E, s->k, v.topk_ids, v.topk_w,
-                                   small_dispatch_args(*s, p, v.topk_ids, v.disp), stream) != hipSuccess)
-      return MOE_ERR_HIP;
-  } else {
-    if (topk_ids_in == nullptr &&
-        moe::launch_route(s->dtype, x, w_router, bias, s->T, s->d, s->E, s->k, v.topk_ids, v.topk_w, stream) !=
-            hipSuccess)
-      return MOE_ERR_HIP;
-    if ((st = enqueue_permute(*s, p, x, v.topk_ids, v.disp, nullptr, ws + p.ws_perm, stream)) != MOE_OK) return st;
+  return enqueue_layer(*s, p, x, topk_ids_in == nullptr ? w_router : nullptr, bias, v.topk_ids, v.topk_w, w_gate, w_up,
+                       w_down, s_gate, s_up, s_down, out, v.disp, v.h, v.y_perm, ws + p.ws_perm, nullptr, stream);
+}
+
+// ---- backward pass ----
+
+// Workspace of the backward calls (byte offsets).  The router's part comes
+// first, so moe_route_backward needs only that; the experts' part starts at
+// `ffn`; dx_perm, which only the whole backward pass keeps here, is last.
+struct BackPlan {
+  size_t saved_bytes, saved_up, saved_gate_exp, saved_up_exp;
+  int ranges, range_steps;  // token ranges of the router's weight gradient, K steps each
+  size_t dz, dense_hi, dense_lo, part, route_ws;
+  int mean, dot_ld;
+  size_t x_perm, dout_perm, dg, du, hw, wrow, dot, ffn_ws;  // from the start of the experts' part
+  size_t dx_perm, backward_ws;
+};
+
+BackPlan back_plan(const moe_shape_t& s) {
+  BackPlan b{};
+  const size_t R = (size_t)row_space(s), Tk = (size_t)s.T * s.k, eb = elt_bytes(s);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes);
+    return at;
+  };
+  take(R * s.F);  // gate codes
+  b.saved_up = take(R * s.F);
+  b.saved_gate_exp = take(R * (s.F / 16));
+  b.saved_up_exp = take(R * (s.F / 16));
+  b.saved_bytes = o;
+  // Token ranges of the router's weight gradient: two workgroups for each
+  // compute unit, but at least 8 K steps each.
+  const int64_t steps = ceil_div(s.T, 64 / (int64_t)eb);
+  const int64_t tiles = ceil_div(s.d, moe::kRouteGradCols[s.dtype]) * ceil_div(s.E, 64);
+  const int64_t want = std::min(ceil_div(2 * kComputeUnits, tiles), std::max<int64_t>(1, steps / 8));
+  b.range_steps = (int)ceil_div(steps, want);
+  b.ranges = (int)ceil_div(steps, b.range_steps);
+  o = 0;
+  b.dz = take(4 * Tk);
+  b.dense_hi = take((size_t)steps * s.E * 64);
+  b.dense_lo = s.dtype == MOE_BF16 ? take((size_t)steps * s.E * 64) : 0;
+  b.part = take(4 * (size_t)b.ranges * s.E * s.d);
+  b.route_ws = o;
+  b.mean = (int)mean_rows(s);
+  b.dot_ld = moe::dgrad_dot_ld(s.dtype, b.mean, s.F);
+  o = 0;
+  b.x_perm = take(R * s.d * eb);
+  b.dout_perm = take(R * s.d * eb);
+  b.dg = take(R * s.F * eb);
+  b.du = take(R * s.F * eb);
+  b.hw = take(R * s.F * eb);
+  b.wrow = take(4 * R);
+  b.dot = take(4 * R * b.dot_ld);
+  b.ffn_ws = o;
+  o = b.route_ws + b.ffn_ws;
+  b.dx_perm = take(R * s.d * eb);
+  b.backward_ws = o;
+  return b;
+}
+
+bool aligned(std::initializer_list<const void*> ptrs, size_t to) {
+  for (const void* p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p) % to != 0) return false;
+  return true;
+}
+
+moe_status_t check_saved(const moe_saved8_t* v) {
+  if (v == nullptr || !v->gate || !v->up || !v->gate_exp || !v->up_exp) return MOE_ERR_NULL_PTR;
+  return aligned({v->gate, v->up, v->gate_exp, v->up_exp}, 16) ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+
+moe::GradRows grad_rows(const moe_shape_t& s, const moe_dispatch_t& d) {
+  return moe::GradRows{d.counts, d.offsets, d.spill_offsets, s.E, s.capacity};
+}
+
+// The experts' gradients: rows into expert order, the two data gradients, then
+// every weight gradient in one launch, and the routing weights' gradient.
+moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const void* x, const void* dout,
+                                  const float* topk_w, const void* w_gate, const void* w_up, const void* w_down,
+                                  const moe_dispatch_t& d, const moe_saved8_t& saved, void* dx_perm, float* dtopk_w,
+                                  void* dw_gate, void* dw_up, void* dw_down, char* ws, hipStream_t st) {
+  const int Tk = s.T * s.k;
+  const int64_t row_bytes = (int64_t)s.d * elt_bytes(s);
+  float* wrow = reinterpret_cast<float*>(ws + b.wrow);
+  if (moe::launch_gather_backward(x, dout, topk_w, d.row_of, Tk, s.k, row_bytes, ws + b.x_perm, ws + b.dout_perm, wrow,
+                                  st) != hipSuccess)
+    return MOE_ERR_HIP;
+  const int BM = moe::dgrad_tile_rows(s.dtype, b.mean);
+  const int64_t tiles = pass_max_tiles(s, BM, 0) + pass_max_tiles(s, BM, 1);
+  moe::DgradArgs a{};
+  a.rows = grad_rows(s, d);
+  a.blocked16 = s.weight_layout == MOE_LAYOUT_BLOCKED16 ? 1 : 0;
+  a.a0 = ws + b.dout_perm;
+  a.b0 = w_down;
+  a.K = s.d;
+  a.N = s.F;
+  a.wrow = wrow;
+  a.g8 = saved.gate;
+  a.u8 = saved.up;
+  a.gx = saved.gate_exp;
+  a.ux = saved.up_exp;
+  a.dg = ws + b.dg;
+  a.du = ws + b.du;
+  a.hw = dw_down != nullptr ? ws + b.hw : nullptr;
+  a.dot = reinterpret_cast<float*>(ws + b.dot);
+  a.dot_ld = b.dot_ld;
+  if (moe::launch_dgrad(s.dtype, true, b.mean, a, tiles, st) != hipSuccess) return MOE_ERR_HIP;
+  a.a0 = ws + b.dg;
+  a.a1 = ws + b.du;
+  a.b0 = w_gate;
+  a.b1 = w_up;
+  a.K = s.F;
+  a.N = s.d;
+  a.out = dx_perm;
+  if (moe::launch_dgrad(s.dtype, false, b.mean, a, tiles, st) != hipSuccess) return MOE_ERR_HIP;
+  moe::WgradArgs g{};
+  g.rows = a.rows;
+  g.blocked16 = a.blocked16;
+  auto add = [&](const void* P, const void* Q, void* out, int M, int N) {
+    g.P[g.n] = P;
+    g.Q[g.n] = Q;
+    g.out[g.n] = out;
+    g.M[g.n] = M;
+    g.N[g.n] = N;
+    ++g.n;
+  };
+  if (dw_down != nullptr) add(ws + b.dout_perm, ws + b.hw, dw_down, s.d, s.F);
+  if (dw_gate != nullptr) {
+    add(ws + b.dg, ws + b.x_perm, dw_gate, s.F, s.d);
+    add(ws + b.du, ws + b.x_perm, dw_up, s.F, s.d);
   }
-  // capacity mode: both passes in each launch (the overflow tiles of an expert
-  // run next to its first-pass tiles and find its weights in L2)
-  const int ps = s->capacity > 0 ? kBothPasses : 0;
-  if ((st = enqueue_gate_up(*s, nullptr, w_gate, w_up, v.disp, ps, v.h, stream, x, s_gate, s_up)) != MOE_OK)
-    return st;
-  const bool split = split_down(*s, v.disp.tile_rows);
-  if (fused_down_combine(*s, v.disp.tile_rows))  // a decode batch: the combine inside the down GEMM
-    return enqueue_down(*s, v.h, w_down, v.disp, ps, v.y_perm, stream, s_down, true, out, v.topk_w);
-  if ((st = enqueue_down(*s, v.h, w_down, v.disp, ps, v.y_perm, stream, s_down, !split)) != MOE_OK) return st;
-  if (split)  // y formed from the two K ranges inside the combine
-    return hip_status(moe::launch_combine_split(s->dtype, v.disp.kpart, (size_t)p.R * s->d, v.topk_w,
-                                                v.disp.row_of, s->T, s->k, s->d, v.y_perm, out, stream));
+  if (g.n > 0 && moe::launch_wgrad(s.dtype, b.mean, g, st) != hipSuccess) return MOE_ERR_HIP;
+  return hip_status(moe::launch_dot_finish(a.dot, a.dot_ld, d.row_of, Tk, dtopk_w, st));
+}
+
+// The router's gradient; with row_of set, dx also takes the sum of dx_perm's rows.
+moe_status_t enqueue_route_backward(const moe_shape_t& s, const BackPlan& b, const void* x, const void* w_router,
+                                    const int32_t* ids, const float* w, const float* dw, const void* dx_perm,
+                                    const int32_t* row_of, void* dx, void* dw_router, float* dbias, char* ws,
+                                    hipStream_t st) {
+  float* dz = reinterpret_cast<float*>(ws + b.dz);
+  char* lo = s.dtype == MOE_BF16 ? ws + b.dense_lo : nullptr;
+  if (moe::launch_route_dz(s.dtype, ids, w, dw, s.T, s.k, s.E, dz, ws + b.dense_hi, lo, st) != hipSuccess)
+    return MOE_ERR_HIP;
+  moe::RouteWgradArgs a{};
+  a.dz_hi = ws + b.dense_hi;
+  a.dz_lo = lo;
+  a.x = x;
+  a.part = reinterpret_cast<float*>(ws + b.part);
+  a.T = s.T;
+  a.E = s.E;
+  a.d = s.d;
+  a.steps = b.range_steps;
+  if ((s.dtype == MOE_BF16 ? moe::launch_route_wgrad_bf16(a, b.ranges, st)
+                           : moe::launch_route_wgrad_f32(a, b.ranges, st)) != hipSuccess)
+    return MOE_ERR_HIP;
+  if (moe::launch_token_backward(s.dtype, dx_perm, row_of, dz, ids, w_router, s.T, s.k, s.d, s.E, dx, st) !=
+      hipSuccess)
+    return MOE_ERR_HIP;
   return hip_status(
-      moe::launch_combine(s->dtype, v.y_perm, v.topk_w, v.disp.row_of, s->T, s->k, s->d, out, stream));
+      moe::launch_route_finish(s.dtype, a.part, b.ranges, ids, dz, s.T, s.k, s.E, s.d, dw_router, dbias, st));
 }
 
 }  // namespace
@@ -697,6 +876,166 @@ moe_status_t moe_forward_fp8(const moe_shape_t* s, const void* x, const void* w_
   if (!s_gate || !s_up || !s_down) return MOE_ERR_NULL_PTR;
   return forward_impl(s, x, w_router, bias, topk_ids_in, topk_w_in, w_gate, w_up, w_down, s_gate, s_up, s_down,
                       out, workspace, ws_bytes, views_out, stream);
+}
+
+moe_status_t moe_backward_query(const moe_shape_t* s, moe_backward_sizes_t* out) {
+  moe_status_t st = validate(s);
+  if (st != MOE_OK) return st;
+  if (out == nullptr) return MOE_ERR_NULL_PTR;
+  const BackPlan b = back_plan(*s);
+  out->saved8_bytes = b.saved_bytes;
+  out->route_ws_bytes = b.route_ws;
+  out->ffn_ws_bytes = b.ffn_ws;
+  out->backward_ws_bytes = b.backward_ws;
+  return MOE_OK;
+}
+
+moe_status_t moe_saved8_carve(const moe_shape_t* s, void* base, size_t bytes, moe_saved8_t* saved) {
+  moe_status_t st = validate(s);
+  if (st != MOE_OK) return st;
+  if (base == nullptr || saved == nullptr) return MOE_ERR_NULL_PTR;
+  const BackPlan b = back_plan(*s);
+  if (bytes < b.saved_bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned({base}, kAlign)) return MOE_ERR_INVALID_ARG;
+  char* p = static_cast<char*>(base);
+  saved->gate = reinterpret_cast<int8_t*>(p);
+  saved->up = reinterpret_cast<int8_t*>(p + b.saved_up);
+  saved->gate_exp = reinterpret_cast<uint8_t*>(p + b.saved_gate_exp);
+  saved->up_exp = reinterpret_cast<uint8_t*>(p + b.saved_up_exp);
+  return MOE_OK;
+}
+
+moe_status_t moe_ffn_gate_up_save8(const moe_shape_t* s, const void* x, const void* w_gate, const void* w_up,
+                                   const moe_dispatch_t* disp, int pass, void* h, const moe_saved8_t* saved,
+                                   hipStream_t stream) {
+  moe_status_t st = validate(s);
+  if (st != MOE_OK) return st;
+  if ((st = validate_gather(*s)) != MOE_OK) return st;
+  if (!x || !w_gate || !w_up || !h) return MOE_ERR_NULL_PTR;
+  if (pass < 0 || pass > kBothPasses) return MOE_ERR_INVALID_ARG;
+  const Plan p = make_plan(*s);
+  if ((st = check_dispatch(*s, p, disp)) != MOE_OK) return st;
+  if ((st = check_saved(saved)) != MOE_OK) return st;
+  if (!aligned({x, w_gate, w_up, h}, 16)) return MOE_ERR_INVALID_ARG;
+  return enqueue_gate_up(*s, nullptr, w_gate, w_up, *disp, pass, h, stream, x, nullptr, nullptr, saved);
+}
+
+moe_status_t moe_saved8_unpack(const moe_shape_t* s, const moe_saved8_t* saved, const moe_dispatch_t* disp,
+                               void* gate, void* up, hipStream_t stream) {
+  moe_status_t st = validate(s);
+  if (st != MOE_OK) return st;
+  if (!gate || !up || !disp || !disp->token_of) return MOE_ERR_NULL_PTR;
+  if ((st = check_saved(saved)) != MOE_OK) return st;
+  if (!aligned({gate, up}, 16)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_saved8_unpack(saved->gate, saved->up, saved->gate_exp, saved->up_exp, disp->token_of,
+                                              row_space(*s), s->F, gate, up, stream));
+}
+
+moe_status_t moe_combine_backward(const moe_shape_t* s, const void* dout, const void* y_perm, const float* topk_w,
+                                  const moe_dispatch_t* disp, void* dy_perm, float* dtopk_w, hipStream_t stream) {
+  moe_status_t st = validate(s);
+  if (st != MOE_OK) return st;
+  if (!dout || !y_perm || !topk_w || !dy_perm || !dtopk_w || !disp || !disp->row_of) return MOE_ERR_NULL_PTR;
+  if (!aligned({dout, y_perm, dy_perm}, 16) || !aligned({topk_w, dtopk_w}, 4)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_combine_backward(s->dtype, dout, y_perm, topk_w, disp->row_of, s->T, s->k, s->d,
+                                                 dy_perm, dtopk_w, stream));
+}
+
+moe_status_t moe_permute_backward(const moe_shape_t* s, const void* dx_perm, const moe_dispatch_t* disp, void* dx,
+                                  hipStream_t stream) {
+  moe_status_t st = validate(s);
+  if (st != MOE_OK) return st;
+  if (!dx_perm || !dx || !disp || !disp->row_of) return MOE_ERR_NULL_PTR;
+  if (!aligned({dx_perm, dx}, 16)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_token_backward(s->dtype, dx_perm, disp->row_of, nullptr, nullptr, nullptr, s->T, s->k,
+                                               s->d, s->E, dx, stream));
+}
+
+moe_status_t moe_route_backward(const moe_shape_t* s, const void* x, const void* w_router, const int32_t* topk_ids,
+                                const float* topk_w, const float* dtopk_w, void* dx, void* dw_router, float* dbias,
+                                void* workspace, size_t ws_bytes, hipStream_t stream) {
+  moe_status_t st = validate(s);
+  if (st != MOE_OK) return st;
+  if (!x || !w_router || !topk_ids || !topk_w || !dtopk_w || !dx || !dw_router || !workspace) return MOE_ERR_NULL_PTR;
+  const BackPlan b = back_plan(*s);
+  if (ws_bytes < b.route_ws) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned({x, w_router, dx, dw_router}, 16) || !aligned({topk_ids, topk_w, dtopk_w, dbias}, 4) ||
+      !aligned({workspace}, kAlign))
+    return MOE_ERR_INVALID_ARG;
+  return enqueue_route_backward(*s, b, x, w_router, topk_ids, topk_w, dtopk_w, nullptr, nullptr, dx, dw_router, dbias,
+                                static_cast<char*>(workspace), stream);
+}
+
+moe_status_t moe_grouped_ffn_backward(const moe_shape_t* s, const void* x, const void* dout, const float* topk_w,
+                                      const void* w_gate, const void* w_up, const void* w_down,
+                                      const moe_dispatch_t* disp, const moe_saved8_t* saved, void* dx_perm,
+                                      float* dtopk_w, void* dw_gate, void* dw_up, void* dw_down, void* workspace,
+                                      size_t ws_bytes, hipStream_t stream) {
+  moe_status_t st = validate(s);
+  if (st != MOE_OK) return st;
+  if (!x || !dout || !topk_w || !w_gate || !w_up || !w_down || !dx_perm || !dtopk_w || !workspace)
+    return MOE_ERR_NULL_PTR;
+  if ((dw_gate == nullptr) != (dw_up == nullptr)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_dispatch(*s, make_plan(*s), disp)) != MOE_OK) return st;
+  if ((st = check_saved(saved)) != MOE_OK) return st;
+  const BackPlan b = back_plan(*s);
+  if (ws_bytes < b.ffn_ws) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned({x, dout, w_gate, w_up, w_down, dx_perm, dw_gate, dw_up, dw_down}, 16) ||
+      !aligned({topk_w, dtopk_w}, 4) || !aligned({workspace}, kAlign))
+    return MOE_ERR_INVALID_ARG;
+  return enqueue_ffn_backward(*s, b, x, dout, topk_w, w_gate, w_up, w_down, *disp, *saved, dx_perm, dtopk_w, dw_gate,
+                              dw_up, dw_down, static_cast<char*>(workspace), stream);
+}
+
+moe_status_t moe_forward_save8(const moe_shape_t* s, const void* x, const void* w_router, const float* bias,
+                               int32_t* topk_ids, float* topk_w, const void* w_gate, const void* w_up,
+                               const void* w_down, void* out, const moe_dispatch_t* disp, const moe_saved8_t* saved,
+                               void* workspace, size_t ws_bytes, hipStream_t stream) {
+  moe_status_t st = validate(s);
+  if (st != MOE_OK) return st;
+  if ((st = validate_gather(*s)) != MOE_OK) return st;
+  if (!x || !topk_ids || !topk_w || !w_gate || !w_up || !w_down || !out || !workspace) return MOE_ERR_NULL_PTR;
+  const Plan p = make_plan(*s);
+  if ((st = check_dispatch(*s, p, disp)) != MOE_OK) return st;
+  if ((st = check_saved(saved)) != MOE_OK) return st;
+  if (ws_bytes < p.forward_ws) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned({x, w_router, w_gate, w_up, w_down, out}, 16) || !aligned({bias, topk_ids, topk_w}, 4) ||
+      !aligned({workspace}, kAlign))
+    return MOE_ERR_INVALID_ARG;
+  char* ws = static_cast<char*>(workspace);
+  return enqueue_layer(*s, p, x, w_router, bias, topk_ids, topk_w, w_gate, w_up, w_down, nullptr, nullptr, nullptr, out,
+                       *disp, ws + p.ws_h, ws + p.ws_y, ws + p.ws_perm, saved, stream);
+}
+
+moe_status_t moe_backward(const moe_shape_t* s, const void* x, const void* w_router, const int32_t* topk_ids,
+                          const float* topk_w, const void* w_gate, const void* w_up, const void* w_down,
+                          const moe_dispatch_t* disp, const moe_saved8_t* saved, const void* dout, void* dx,
+                          float* dtopk_w, void* dw_router, float* dbias, void* dw_gate, void* dw_up, void* dw_down,
+                          void* workspace, size_t ws_bytes, hipStream_t stream) {
+  moe_status_t st = validate(s);
+  if (st != MOE_OK) return st;
+  if (!x || !topk_ids || !topk_w || !w_gate || !w_up || !w_down || !dout || !dx || !dtopk_w || !workspace)
+    return MOE_ERR_NULL_PTR;
+  if (w_router == nullptr && (dw_router != nullptr || dbias != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (w_router != nullptr && dw_router == nullptr) return MOE_ERR_NULL_PTR;
+  if ((dw_gate == nullptr) != (dw_up == nullptr)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_dispatch(*s, make_plan(*s), disp)) != MOE_OK) return st;
+  if ((st = check_saved(saved)) != MOE_OK) return st;
+  const BackPlan b = back_plan(*s);
+  if (ws_bytes < b.backward_ws) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned({x, w_router, w_gate, w_up, w_down, dout, dx, dw_router, dw_gate, dw_up, dw_down}, 16) ||
+      !aligned({topk_ids, topk_w, dtopk_w, dbias}, 4) || !aligned({workspace}, kAlign))
+    return MOE_ERR_INVALID_ARG;
+  char* ws = static_cast<char*>(workspace);
+  void* dx_perm = ws + b.dx_perm;
+  if ((st = enqueue_ffn_backward(*s, b, x, dout, topk_w, w_gate, w_up, w_down, *disp, *saved, dx_perm, dtopk_w,
+                                 dw_gate, dw_up, dw_down, ws + b.route_ws, stream)) != MOE_OK)
+    return st;
+  if (w_router == nullptr)
+    return hip_status(moe::launch_token_backward(s->dtype, dx_perm, disp->row_of, nullptr, nullptr, nullptr, s->T,
+                                                 s->k, s->d, s->E, dx, stream));
+  return enqueue_route_backward(*s, b, x, w_router, topk_ids, topk_w, dtopk_w, dx_perm, disp->row_of, dx, dw_router,
+                                dbias, ws, stream);
 }
 
 }  // extern "C"

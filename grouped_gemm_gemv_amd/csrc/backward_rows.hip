@@ -1,0 +1,380 @@
+// Row kernels of the backward pass: the gradients of the weighted combine and
+// of the sorted dispatch, the router's gradient apart from its matrix product,
+// the gather in front of the experts' backward GEMMs, and the values of the
+// 8-bit projections.  All of them move whole rows once and are bound by that;
+// every sum is fp32 in a fixed order.
+#include <algorithm>
+
+#include "device_common.hpp"
+#include "launch.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kSlots = 4;  // slots of a token worked at a time
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// Gradient of out_t = sum_j w_j y_j for slots 4 blockIdx.y .. + 3 of token
+// blockIdx.x: dy_j = w_j dout_t (one rounding) and dw_j = <dout_t, y_j>.  dout_t
+// is read once for the four slots.  dw: thread partials over its chunks, then
+// lanes, then wavefronts in order.
+template <class Tr>
+__global__ __launch_bounds__(256) void combine_backward_kernel(const char* __restrict__ dout,
+                                                               const char* __restrict__ y,
+                                                               const float* __restrict__ topk_w,
+                                                               const int32_t* __restrict__ row_of, int k, int d,
+                                                               char* __restrict__ dy, float* __restrict__ dw) {
+  using Elt = typename Tr::T;
+  constexpr int EPC = Tr::EPC;
+  __shared__ float part[4][kSlots];
+  const size_t row_bytes = (size_t)d * sizeof(Elt);
+  const int nchunk = d / EPC;
+  const size_t t = blockIdx.x;
+  const int j0 = blockIdx.y * kSlots;
+  size_t at[kSlots];
+  float w[kSlots], acc[kSlots];
+  bool ok[kSlots];
+#pragma unroll
+  for (int u = 0; u < kSlots; ++u) {
+    const int row = j0 + u < k ? row_of[t * k + j0 + u] : -1;
+    ok[u] = row >= 0;
+    w[u] = ok[u] ? topk_w[t * k + j0 + u] : 0.f;
+    at[u] = ok[u] ? (size_t)row * row_bytes : 0;
+    acc[u] = 0.f;
+  }
+  const char* dt = dout + t * row_bytes;
+  for (int c = threadIdx.x; c < nchunk; c += blockDim.x) {
+    const size_t o = (size_t)c * 16;
+    float g[EPC];
+    const uint4 gc = *reinterpret_cast<const uint4*>(dt + o);
+    uint4 yc[kSlots];
+#pragma unroll
+    for (int u = 0; u < kSlots; ++u)
+      yc[u] = ok[u] ? *reinterpret_cast<const uint4*>(y + at[u] + o) : make_uint4(0, 0, 0, 0);
+    widen<Tr>(gc, g);
+#pragma unroll
+    for (int u = 0; u < kSlots; ++u) {
+      if (!ok[u]) continue;
+      float v[EPC];
+      widen<Tr>(yc[u], v);
+#pragma unroll
+      for (int i = 0; i < EPC; ++i) acc[u] = fmaf(g[i], v[i], acc[u]);
+#pragma unroll
+      for (int i = 0; i < EPC; ++i) v[i] = w[u] * g[i];
+      *reinterpret_cast<uint4*>(dy + at[u] + o) = narrow<Tr>(v);
+    }
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+#pragma unroll
+  for (int u = 0; u < kSlots; ++u) {
+    acc[u] = wave_sum(acc[u]);
+    if (lane == 0) part[wave][u] = acc[u];
+  }
+  __syncthreads();
+  if (threadIdx.x < kSlots && j0 + (int)threadIdx.x < k) {
+    float s = part[0][threadIdx.x];
+    for (int i = 1; i < waves; ++i) s += part[i][threadIdx.x];
+    dw[t * k + j0 + threadIdx.x] = s;
+  }
+}
+
+// dx_t = sum_j dx_perm[row_j] + sum_j dz_j w_router[id_j]: fp32, the rows in
+// slot order and then the router's part, one rounding.  Either sum may be
+// absent (row_of or dz null).  The router's rows stay in L2.
+template <class Tr>
+__global__ __launch_bounds__(256) void token_backward_kernel(const char* __restrict__ dx_perm,
+                                                             const int32_t* __restrict__ row_of,
+                                                             const float* __restrict__ dz,
+                                                             const int32_t* __restrict__ ids,
+                                                             const char* __restrict__ w_router, int k, int d, int E,
+                                                             char* __restrict__ dx) {
+  using Elt = typename Tr::T;
+  constexpr int EPC = Tr::EPC;
+  const size_t row_bytes = (size_t)d * sizeof(Elt);
+  const int nchunk = d / EPC;
+  const size_t t = blockIdx.x;
+  for (int c = threadIdx.x; c < nchunk; c += blockDim.x) {
+    const size_t o = (size_t)c * 16;
+    float acc[EPC];
+#pragma unroll
+    for (int i = 0; i < EPC; ++i) acc[i] = 0.f;
+    if (row_of != nullptr) {
+      for (int j0 = 0; j0 < k; j0 += kSlots) {
+        uint4 ch[kSlots];
+        bool ok[kSlots];
+#pragma unroll
+        for (int u = 0; u < kSlots; ++u) {
+          const int row = j0 + u < k ? row_of[t * k + j0 + u] : -1;
+          ok[u] = row >= 0;
+          ch[u] = ok[u] ? *reinterpret_cast<const uint4*>(dx_perm + (size_t)row * row_bytes + o)
+                        : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kSlots; ++u) {
+          if (!ok[u]) continue;
+          float v[EPC];
+          widen<Tr>(ch[u], v);
+#pragma unroll
+          for (int i = 0; i < EPC; ++i) acc[i] += v[i];
+        }
+      }
+    }
+    if (dz != nullptr) {
+      for (int j0 = 0; j0 < k; j0 += kSlots) {
+        uint4 ch[kSlots];
+        float z[kSlots];
+        bool ok[kSlots];
+#pragma unroll
+        for (int u = 0; u < kSlots; ++u) {
+          const int id = j0 + u < k ? ids[t * k + j0 + u] : -1;
+          ok[u] = id >= 0 && id < E;
+          z[u] = ok[u] ? dz[t * k + j0 + u] : 0.f;
+          ch[u] = ok[u] ? *reinterpret_cast<const uint4*>(w_router + (size_t)id * row_bytes + o)
+                        : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kSlots; ++u) {
+          if (!ok[u]) continue;
+          float v[EPC];
+          widen<Tr>(ch[u], v);
+#pragma unroll
+          for (int i = 0; i < EPC; ++i) acc[i] = fmaf(z[u], v[i], acc[i]);
+        }
+      }
+    }
+    *reinterpret_cast<uint4*>(dx + t * row_bytes + o) = narrow<Tr>(acc);
+  }
+}
+
+// The softmax's gradient over the chosen logits, dz_j = w_j (dw_j - sum_i w_i
+// dw_i), and its dense form for the router's weight gradient: workgroup b
+// holds the KS tokens of one K step, one thread each, and writes [E][KS]
+// (bf16: the rounded value, and the rounded rest).
+template <class Tr>
+__global__ __launch_bounds__(256) void route_dz_kernel(const int32_t* __restrict__ ids, const float* __restrict__ w,
+                                                       const float* __restrict__ dw, int T, int k, int E,
+                                                       float* __restrict__ dz, typename Tr::T* __restrict__ hi,
+                                                       typename Tr::T* __restrict__ lo) {
+  constexpr int KS = 64 / sizeof(typename Tr::T);
+  extern __shared__ float dense[];  // [E][KS]
+  for (int i = threadIdx.x; i < E * KS; i += 256) dense[i] = 0.f;
+  __syncthreads();
+  const int64_t t = (int64_t)blockIdx.x * KS + threadIdx.x;
+  if (threadIdx.x < KS && t < T) {
+    const float* wt = w + t * k;
+    const float* dt = dw + t * k;
+    float s = 0.f;
+    for (int j = 0; j < k; ++j) s = fmaf(wt[j], dt[j], s);
+    for (int j = 0; j < k; ++j) {
+      const float z = wt[j] * (dt[j] - s);
+      dz[t * k + j] = z;
+      const int id = ids[t * k + j];
+      if (id >= 0 && id < E) dense[id * KS + threadIdx.x] += z;
+    }
+  }
+  __syncthreads();
+  const size_t base = (size_t)blockIdx.x * E * KS;
+  for (int i = threadIdx.x; i < E * KS; i += 256) {
+    const float v = dense[i];
+    if constexpr (sizeof(typename Tr::T) == 2) {
+      const uint32_t h = f32_to_bf16(v);
+      hi[base + i] = (uint16_t)h;
+      lo[base + i] = (uint16_t)f32_to_bf16(v - bf16_to_f32(h));
+    } else {
+      hi[base + i] = v;
+    }
+  }
+}
+
+// dw_router = the token ranges' partial sums in order, one rounding
+// (blocks 0 .. sum_blocks - 1); dbias_e = sum of dz over the entries of expert e
+// (the E blocks behind them).
+template <class Tr>
+__global__ __launch_bounds__(256) void route_finish_kernel(const float* __restrict__ part, int ranges, int sum_blocks,
+                                                           const int32_t* __restrict__ ids,
+                                                           const float* __restrict__ dz, int64_t Tk, int64_t Ed,
+                                                           char* __restrict__ dw_router, float* __restrict__ dbias) {
+  using Elt = typename Tr::T;
+  if ((int)blockIdx.x < sum_blocks) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= Ed) return;
+    float4 s = *reinterpret_cast<const float4*>(part + i);
+    for (int r = 1; r < ranges; ++r) {
+      const float4 v = *reinterpret_cast<const float4*>(part + r * Ed + i);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    store4<Tr>(dw_router + i * sizeof(Elt), s.x, s.y, s.z, s.w);
+    return;
+  }
+  __shared__ float wave_part[4];
+  const int e = blockIdx.x - sum_blocks;
+  float s = 0.f;
+  for (int64_t f = threadIdx.x; f < Tk; f += 256 * 4) {
+    float v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t q = f + 256 * u;
+      v[u] = q < Tk && ids[q] == e ? dz[q] : 0.f;
+    }
+    s += (v[0] + v[1]) + (v[2] + v[3]);
+  }
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) wave_part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) dbias[e] = (wave_part[0] + wave_part[1]) + (wave_part[2] + wave_part[3]);
+}
+
+// Rows of x and dout in expert order and the routing weight of each row: one
+// wavefront per entry.
+__global__ __launch_bounds__(256) void gather_backward_kernel(const char* __restrict__ x,
+                                                              const char* __restrict__ dout,
+                                                              const float* __restrict__ topk_w,
+                                                              const int32_t* __restrict__ row_of, int Tk, int k,
+                                                              int64_t row_bytes, char* __restrict__ x_perm,
+                                                              char* __restrict__ dout_perm,
+                                                              float* __restrict__ wrow) {
+  const int64_t f = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (f >= Tk) return;
+  const int row = row_of[f];
+  if (row < 0) return;
+  const int lane = threadIdx.x & 63;
+  if (lane == 0) wrow[row] = topk_w[f];
+  const int64_t src = f / k * row_bytes, dst = (int64_t)row * row_bytes;
+  for (int64_t c = lane * 16; c < row_bytes; c += 64 * 16) {
+    const uint4 a = *reinterpret_cast<const uint4*>(x + src + c);
+    const uint4 b = *reinterpret_cast<const uint4*>(dout + src + c);
+    *reinterpret_cast<uint4*>(x_perm + dst + c) = a;
+    *reinterpret_cast<uint4*>(dout_perm + dst + c) = b;
+  }
+}
+
+// dw_f = the row's partial sums of <D, h>: lane i takes i, i + 64, ... in order.
+__global__ __launch_bounds__(256) void dot_finish_kernel(const float* __restrict__ dot, int ld,
+                                                         const int32_t* __restrict__ row_of, int Tk,
+                                                         float* __restrict__ dw) {
+  const int64_t f = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (f >= Tk) return;
+  const int row = row_of[f];
+  const int lane = threadIdx.x & 63;
+  float s = 0.f;
+  if (row >= 0)
+    for (int i = lane; i < ld; i += 64) s += dot[(size_t)row * ld + i];
+  s = wave_sum(s);
+  if (lane == 0) dw[f] = s;
+}
+
+// Values of one projection's codes (blockIdx.y: gate, up): a thread turns one
+// block of 16 into bf16, which holds every such value exactly.
+__global__ __launch_bounds__(256) void saved8_unpack_kernel(const int8_t* __restrict__ g8,
+                                                            const int8_t* __restrict__ u8,
+                                                            const uint8_t* __restrict__ gx,
+                                                            const uint8_t* __restrict__ ux,
+                                                            const int32_t* __restrict__ token_of, int64_t blocks,
+                                                            int per_row, uint16_t* __restrict__ gate,
+                                                            uint16_t* __restrict__ up) {
+  const int8_t* codes = blockIdx.y ? u8 : g8;
+  const uint8_t* exps = blockIdx.y ? ux : gx;
+  uint16_t* out = blockIdx.y ? up : gate;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < blocks; i += (int64_t)gridDim.x * 256) {
+    if (token_of[i / per_row] < 0) continue;
+    const uint4 c = *reinterpret_cast<const uint4*>(codes + i * 16);
+    const float s = exp_scale(exps[i]);
+    const unsigned w[4] = {c.x, c.y, c.z, c.w};
+    float v[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) v[q] = code_of(w[q >> 2], q & 3) * s;
+    *reinterpret_cast<uint4*>(out + i * 16) = narrow<TBF16>(v);
+    *reinterpret_cast<uint4*>(out + i * 16 + 8) = narrow<TBF16>(v + 8);
+  }
+}
+
+int row_threads(int dtype, int d) { return d / (dtype == 1 ? 8 : 4) <= 64 ? 64 : 256; }
+
+}  // namespace
+
+hipError_t launch_combine_backward(int dtype, const void* dout, const void* y, const float* topk_w,
+                                   const int32_t* row_of, int T, int k, int d, void* dy, float* dw,
+                                   hipStream_t stream) {
+  const dim3 grid(T, (k + kSlots - 1) / kSlots), block(row_threads(dtype, d));
+  if (dtype == 1)
+    hipLaunchKernelGGL(combine_backward_kernel<TBF16>, grid, block, 0, stream, static_cast<const char*>(dout),
+                       static_cast<const char*>(y), topk_w, row_of, k, d, static_cast<char*>(dy), dw);
+  else
+    hipLaunchKernelGGL(combine_backward_kernel<TF32>, grid, block, 0, stream, static_cast<const char*>(dout),
+                       static_cast<const char*>(y), topk_w, row_of, k, d, static_cast<char*>(dy), dw);
+  return hipGetLastError();
+}
+
+hipError_t launch_token_backward(int dtype, const void* dx_perm, const int32_t* row_of, const float* dz,
+                                 const int32_t* ids, const void* w_router, int T, int k, int d, int E, void* dx,
+                                 hipStream_t stream) {
+  const dim3 grid(T), block(row_threads(dtype, d));
+  if (dtype == 1)
+    hipLaunchKernelGGL(token_backward_kernel<TBF16>, grid, block, 0, stream, static_cast<const char*>(dx_perm),
+                       row_of, dz, ids, static_cast<const char*>(w_router), k, d, E, static_cast<char*>(dx));
+  else
+    hipLaunchKernelGGL(token_backward_kernel<TF32>, grid, block, 0, stream, static_cast<const char*>(dx_perm),
+                       row_of, dz, ids, static_cast<const char*>(w_router), k, d, E, static_cast<char*>(dx));
+  return hipGetLastError();
+}
+
+hipError_t launch_route_dz(int dtype, const int32_t* ids, const float* w, const float* dw, int T, int k, int E,
+                           float* dz, void* dense_hi, void* dense_lo, hipStream_t stream) {
+  const int KS = dtype == 1 ? 32 : 16;
+  const dim3 grid((unsigned)(((int64_t)T + KS - 1) / KS)), block(256);
+  const size_t lds = (size_t)E * KS * sizeof(float);
+  if (dtype == 1)
+    hipLaunchKernelGGL(route_dz_kernel<TBF16>, grid, block, lds, stream, ids, w, dw, T, k, E, dz,
+                       static_cast<uint16_t*>(dense_hi), static_cast<uint16_t*>(dense_lo));
+  else
+    hipLaunchKernelGGL(route_dz_kernel<TF32>, grid, block, lds, stream, ids, w, dw, T, k, E, dz,
+                       static_cast<float*>(dense_hi), static_cast<float*>(nullptr));
+  return hipGetLastError();
+}
+
+hipError_t launch_route_finish(int dtype, const float* part, int ranges, const int32_t* ids, const float* dz, int T,
+                               int k, int E, int d, void* dw_router, float* dbias, hipStream_t stream) {
+  const int64_t Ed = (int64_t)E * d;
+  const int sum_blocks = (int)((Ed / 4 + 255) / 256);
+  const dim3 grid(sum_blocks + (dbias != nullptr ? E : 0)), block(256);
+  if (dtype == 1)
+    hipLaunchKernelGGL(route_finish_kernel<TBF16>, grid, block, 0, stream, part, ranges, sum_blocks, ids, dz,
+                       (int64_t)T * k, Ed, static_cast<char*>(dw_router), dbias);
+  else
+    hipLaunchKernelGGL(route_finish_kernel<TF32>, grid, block, 0, stream, part, ranges, sum_blocks, ids, dz,
+                       (int64_t)T * k, Ed, static_cast<char*>(dw_router), dbias);
+  return hipGetLastError();
+}
+
+hipError_t launch_gather_backward(const void* x, const void* dout, const float* topk_w, const int32_t* row_of, int Tk,
+                                  int k, int64_t row_bytes, void* x_perm, void* dout_perm, float* wrow,
+                                  hipStream_t stream) {
+  hipLaunchKernelGGL(gather_backward_kernel, dim3((Tk + 3) / 4), dim3(256), 0, stream, static_cast<const char*>(x),
+                     static_cast<const char*>(dout), topk_w, row_of, Tk, k, row_bytes, static_cast<char*>(x_perm),
+                     static_cast<char*>(dout_perm), wrow);
+  return hipGetLastError();
+}
+
+hipError_t launch_dot_finish(const float* dot, int ld, const int32_t* row_of, int Tk, float* dw, hipStream_t stream) {
+  hipLaunchKernelGGL(dot_finish_kernel, dim3((Tk + 3) / 4), dim3(256), 0, stream, dot, ld, row_of, Tk, dw);
+  return hipGetLastError();
+}
+
+hipError_t launch_saved8_unpack(const int8_t* g8, const int8_t* u8, const uint8_t* gx, const uint8_t* ux,
+                                const int32_t* token_of, int64_t rows, int F, void* gate, void* up,
+                                hipStream_t stream) {
+  const int64_t blocks = rows * (F / 16);
+  hipLaunchKernelGGL(saved8_unpack_kernel, dim3((unsigned)std::min<int64_t>((blocks + 255) / 256, 1 << 20), 2), dim3(256), 0, stream, g8, u8,
+                     gx, ux, token_of, blocks, F / 16, static_cast<uint16_t*>(gate), static_cast<uint16_t*>(up));
+  return hipGetLastError();
+}
+
+}  // namespace moe

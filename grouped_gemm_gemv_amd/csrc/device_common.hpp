@@ -116,6 +116,28 @@ __device__ __forceinline__ uint4 narrow<TF32>(const float* v) {
   return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
 }
 
+// The 8-bit projections (moe_saved8_t): 16 consecutive values of a row share the
+// exponent b = max(7, exponent field of the largest magnitude) and are kept as
+// code = rint(v 2^(133 - b)) in [-127, 127]; b = 255 marks a block that holds a
+// NaN or an infinity, whose values all read as NaN.
+// Scale of a block's codes: 2^(b - 133), a normal number for every b.
+__device__ __forceinline__ float exp_scale(unsigned b) {
+  return b == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((max(b, 7u) - 6u) << 23);
+}
+// Code r (0..3) of a word of four.
+__device__ __forceinline__ float code_of(unsigned word, int r) { return (float)((int)(word << (24 - 8 * r)) >> 24); }
+// Four values with exponent b to a word of codes (b = 255: zeros).
+__device__ __forceinline__ unsigned pack_codes(float v0, float v1, float v2, float v3, unsigned b) {
+  if (b == 255u) return 0u;
+  const float s = __uint_as_float((260u - b) << 23);
+  const float v[4] = {v0, v1, v2, v3};
+  unsigned w = 0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    w |= ((unsigned)(int)fminf(fmaxf(rintf(v[r] * s), -127.f), 127.f) & 255u) << (8 * r);
+  return w;
+}
+
 __device__ __forceinline__ uint64_t lanemask_lt(int lane) { return (lane == 0) ? 0ull : (~0ull >> (64 - lane)); }
 
 }  // namespace moe

@@ -1,0 +1,45 @@
+// Backward grouped GEMM instantiations: bf16.
+#include "gemm_grad.hpp"
+
+namespace moe {
+namespace {
+using namespace grad;
+// data gradients, by row-tile height
+using D256 = Tile<TBF16, 256, 256, 2, 4, false, 4, false>;
+using D128 = Tile<TBF16, 128, 256, 2, 4, false, 4, false>;
+using D64 = Tile<TBF16, 64, 128, 1, 4, false, 4, false>;
+using D32 = Tile<TBF16, 32, 128, 1, 4, false, 4, false>;
+// weight gradients
+using W256 = Tile<TBF16, 256, 256, 2, 4, true, 4, false>;
+using W128 = Tile<TBF16, 128, 128, 2, 2, true, 4, false>;
+// router weight gradient: experts by columns
+using R64 = Tile<TBF16, 64, 128, 1, 4, false, 4, false>;
+
+template <bool DH>
+hipError_t dgrad_bm(int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
+  switch (BM) {
+    case 256: return launch_dgrad_cfg<TBF16, D256, DH>(a, max_tiles, stream);
+    case 128: return launch_dgrad_cfg<TBF16, D128, DH>(a, max_tiles, stream);
+    case 64: return launch_dgrad_cfg<TBF16, D64, DH>(a, max_tiles, stream);
+    case 32: return launch_dgrad_cfg<TBF16, D32, DH>(a, max_tiles, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+}  // namespace
+
+hipError_t launch_dgrad_bf16(bool dh, int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
+  return dh ? dgrad_bm<true>(BM, a, max_tiles, stream) : dgrad_bm<false>(BM, a, max_tiles, stream);
+}
+
+hipError_t launch_wgrad_bf16(int BM, const WgradArgs& a, hipStream_t stream) {
+  return BM == 256 ? launch_wgrad_cfg<TBF16, W256>(a, stream) : launch_wgrad_cfg<TBF16, W128>(a, stream);
+}
+
+hipError_t launch_route_wgrad_bf16(const RouteWgradArgs& a, int ranges, hipStream_t stream) {
+  hipLaunchKernelGGL((route_wgrad_kernel<TBF16, R64>),
+                     dim3((a.d + R64::BN - 1) / R64::BN, (a.E + R64::BM - 1) / R64::BM, ranges), dim3(R64::NTH), 0,
+                     stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,50 @@
+// Backward grouped GEMM instantiations: fp32, and the tile choice of both types.
+#include "gemm_grad.hpp"
+
+namespace moe {
+namespace {
+using namespace grad;
+// fp32 MFMAs run at a sixteenth of the bf16 rate, so small tiles keep up
+using D64 = Tile<TF32, 64, 64, 2, 2, false, 4, false>;
+using W64 = Tile<TF32, 64, 64, 2, 2, true, 4, false>;
+}  // namespace
+
+hipError_t launch_dgrad_f32(bool dh, int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
+  if (BM != D64::BM) return hipErrorInvalidValue;
+  return dh ? launch_dgrad_cfg<TF32, D64, true>(a, max_tiles, stream)
+            : launch_dgrad_cfg<TF32, D64, false>(a, max_tiles, stream);
+}
+
+hipError_t launch_wgrad_f32(int, const WgradArgs& a, hipStream_t stream) {
+  return launch_wgrad_cfg<TF32, W64>(a, stream);
+}
+
+hipError_t launch_route_wgrad_f32(const RouteWgradArgs& a, int ranges, hipStream_t stream) {
+  hipLaunchKernelGGL((route_wgrad_kernel<TF32, D64>),
+                     dim3((a.d + D64::BN - 1) / D64::BN, (a.E + D64::BM - 1) / D64::BM, ranges), dim3(D64::NTH), 0,
+                     stream, a);
+  return hipGetLastError();
+}
+
+int dgrad_tile_rows(int dtype, int mean) {
+  if (dtype != 1) return 64;
+  return mean > 192 ? 256 : mean > 64 ? 128 : mean > 32 ? 64 : 32;
+}
+
+int dgrad_dot_ld(int dtype, int mean, int F) {
+  // one partial sum per wavefront column: 64 columns (bf16 tiles of 128 and 256
+  // rows) or 32, rounded up to whole column tiles
+  if (dtype != 1) return (F + 63) / 64 * 2;
+  return dgrad_tile_rows(dtype, mean) >= 128 ? (F + 255) / 256 * 4 : (F + 127) / 128 * 4;
+}
+
+hipError_t launch_dgrad(int dtype, bool dh, int mean, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
+  const int BM = dgrad_tile_rows(dtype, mean);
+  return dtype == 1 ? launch_dgrad_bf16(dh, BM, a, max_tiles, stream) : launch_dgrad_f32(dh, BM, a, max_tiles, stream);
+}
+
+hipError_t launch_wgrad(int dtype, int mean, const WgradArgs& a, hipStream_t stream) {
+  return dtype == 1 ? launch_wgrad_bf16(mean > 192 ? 256 : 128, a, stream) : launch_wgrad_f32(64, a, stream);
+}
+
+}  // namespace moe

@@ -131,12 +131,16 @@ __device__ __forceinline__ uint4 widen_e4m3(unsigned lo, unsigned hi) {
 // KS workgroups (KS = 1 or 2).  With KS = 2 each workgroup stores its fp32
 // partial sums, unrounded, in plane ks of a [2][R][N] buffer, and a separate
 // kernel adds the two planes (k_split_finish): no workgroup waits for another.
+// SAVE (gate+up): the epilogue also keeps both projections in 8 bits for a
+// backward pass (moe_saved8_t).  A 16-column block of a row is exactly one
+// MFMA subtile's column of accumulators (four lanes of four values), so the
+// shared exponent takes two lane exchanges and no LDS.
 template <class Tr, int BM, int WTN, int WN, int WK, bool GATED, int PF, int NTMS, bool WQ, int WS = 0, int KS = 1,
-          int PP = 0>
+          int PP = 0, bool SAVE = false>
 struct Gemm {
   using Elt = typename Tr::T;
   static_assert(!WQ || std::is_same<Tr, TBF16>::value, "fp8 weights take bf16 activations");
-  static constexpr bool WQ_ = WQ;
+  static constexpr bool WQ_ = WQ, SAVE_ = SAVE;
   static constexpr int WTN_ = WTN, WN_ = WN, WK_ = WK;
   static constexpr int NTH = 64 * WN * WK;
   static constexpr int NSUB = WTN / 16;
@@ -155,6 +159,7 @@ struct Gemm {
   static constexpr int STAGE = BM * ROWB;         // bytes per activation stage
   static_assert(WTN % 16 == 0 && BM % 16 == 0 && PF >= 2 && PF <= 7, "tile shape");
   static_assert(KS == 1 || (KS == 2 && WK == 1 && !GATED), "K split");
+  static_assert(!SAVE || (GATED && !WQ), "8-bit projections");
 
   struct Ctx {
     __amdgpu_buffer_rsrc_t act;      // activation rows of the tile (reads past its rows return 0)
@@ -169,6 +174,8 @@ struct Gemm {
     int ld;                          // activation/weight row bytes
     int nk, nit, rows, n0, N, wk;
     int s0;                          // first K step of this workgroup's range (K split), else 0
+    int8_t* save[2];                 // SAVE: codes of gate and up, of the tile's row0
+    uint8_t* save_exp[2];            // SAVE: exponents of their blocks
   };
 
   // LDS swizzle of the activation tile: in row r, the 16-byte chunk c of each
@@ -695,6 +702,14 @@ struct Gemm {
         sc[m][i][2] = v4.z;
         sc[m][i][3] = v4.w;
       }
+    if constexpr (SAVE) {
+#pragma unroll
+      for (int jm = 0; jm < MS; ++jm)
+#pragma unroll
+        for (int i = 0; i < NSUB; ++i)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) save_block(c, q, jm * 16 + (lane & 15), c.n0 + i * 16, acc[q][i][jm]);
+    }
 #pragma unroll
     for (int jm = 0; jm < MS; ++jm) {
       const int m = jm * 16 + (lane & 15);
@@ -716,6 +731,24 @@ struct Gemm {
           }
         }
       }
+    }
+  }
+
+  // Columns n .. n + 15 of row m of projection q (0 gate, 1 up), four in each of
+  // the lanes l, l + 16, l + 32, l + 48: codes and the block's exponent.  The
+  // magnitudes are compared as integers, which orders infinities and NaN last.
+  __device__ __forceinline__ static void save_block(const Ctx& c, int q, int m, int n, const f32x4_t& v) {
+    const int lane = threadIdx.x & 63;
+    unsigned top = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) top = max(top, __float_as_uint(v[r]) & 0x7fffffffu);
+    top = max(top, (unsigned)__shfl_xor((int)top, 16));
+    top = max(top, (unsigned)__shfl_xor((int)top, 32));
+    const unsigned b = max(top >> 23, 7u);
+    if (m < c.rows && n < c.N) {
+      const size_t o = (size_t)m * c.N + n;
+      *reinterpret_cast<unsigned*>(c.save[q] + o + (lane >> 4) * 4) = pack_codes(v[0], v[1], v[2], v[3], b);
+      if (lane < 16) c.save_exp[q][o >> 4] = (uint8_t)b;
     }
   }
 
@@ -767,6 +800,12 @@ __device__ __forceinline__ void setup_ctx(typename G::Ctx& c, const GemmArgs& p,
   c.wk = wave / G::WN_;
   c.n0 = nbase + (wave % G::WN_) * G::WTN_;
   c.out = reinterpret_cast<char*>(p.out) + (size_t)row0 * c.ldo;
+  if constexpr (G::SAVE_) {
+    c.save[0] = p.save_gate + (size_t)row0 * p.N;
+    c.save[1] = p.save_up + (size_t)row0 * p.N;
+    c.save_exp[0] = p.save_gate_exp + (size_t)row0 * (p.N / 16);
+    c.save_exp[1] = p.save_up_exp + (size_t)row0 * (p.N / 16);
+  }
 #pragma unroll
   for (int i = 0; i < G::NA; ++i) c.stage[i] = stages[i];
   if (p.act_rows != nullptr) {
@@ -802,9 +841,9 @@ __device__ __forceinline__ void setup_ctx(typename G::Ctx& c, const GemmArgs& p,
 }
 
 template <class Tr, int BM, int WTN, int WN, int WK, bool GATED, int PF, int NTMS, bool WQ, int RS, int WS, int KS,
-          int PP>
+          int PP, bool SAVE>
 __global__ __launch_bounds__(64 * WN * WK) void grouped_gemm_kernel(GemmArgs p) {
-  using G = Gemm<Tr, BM, WTN, WN, WK, GATED, PF, NTMS, WQ, WS, KS, PP>;
+  using G = Gemm<Tr, BM, WTN, WN, WK, GATED, PF, NTMS, WQ, WS, KS, PP, SAVE>;
   // one LDS array per activation stage (stages past NA are 16-byte stubs)
   __shared__ __attribute__((aligned(16))) char st0[G::STAGE];
   __shared__ __attribute__((aligned(16))) char st1[G::STAGE];
@@ -914,10 +953,10 @@ __global__ __launch_bounds__(64 * WN * WK) void grouped_gemm_kernel(GemmArgs p) 
 // expert's weights stay consecutive: in column group g, the expert's
 // CW-width unit (if its last tile is short) and then its full tiles at the
 // CN-width columns 2g and 2g + 1.
-template <class Tr, class CW, class CN>
+template <class Tr, class CW, class CN, bool SAVE>
 __global__ __launch_bounds__(64 * CN::WN) void grouped_gemm_wide_kernel(GemmArgs p) {
-  using GW = Gemm<Tr, CW::BM, CW::WTN, CW::WN, 1, true, CW::PF, CW::NTMS, false, CW::WS>;
-  using GN = Gemm<Tr, CN::BM, CN::WTN, CN::WN, 1, true, CN::PF, CN::NTMS, false, CN::WS>;
+  using GW = Gemm<Tr, CW::BM, CW::WTN, CW::WN, 1, true, CW::PF, CW::NTMS, false, CW::WS, 1, 0, SAVE>;
+  using GN = Gemm<Tr, CN::BM, CN::WTN, CN::WN, 1, true, CN::PF, CN::NTMS, false, CN::WS, 1, 0, SAVE>;
   static_assert(CW::WN == CN::WN && CW::WK == 1 && CN::WK == 1 && CW::RS == 1 && CN::RS == 1, "wide pair");
   static_assert(CW::BM < CN::BM && CN::BM <= 2 * CW::BM && GW::BN == 2 * GN::BN, "wide pair");
   constexpr int STAGE = GW::STAGE > GN::STAGE ? GW::STAGE : GN::STAGE;
@@ -1016,7 +1055,7 @@ __global__ __launch_bounds__(64 * CN::WN) void grouped_gemm_wide_kernel(GemmArgs
   }
 }
 
-template <class Tr, class Pair>
+template <class Tr, class Pair, bool SAVE>
 hipError_t launch_wide(const GemmArgs& a, hipStream_t stream) {
   using CN = typename Pair::narrow;
   constexpr int BNn = CN::WN * CN::WTN;
@@ -1025,12 +1064,12 @@ hipError_t launch_wide(const GemmArgs& a, hipStream_t stream) {
   const long long round = a.skew_map ? 8LL * kXcdChunk : 8;
   const long long grid = ((units + round - 1) / round) * round;
   if (grid == 0) return hipSuccess;
-  hipLaunchKernelGGL((grouped_gemm_wide_kernel<Tr, typename Pair::wide, CN>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((grouped_gemm_wide_kernel<Tr, typename Pair::wide, CN, SAVE>), dim3((unsigned)grid),
                      dim3(64 * CN::WN), 0, stream, a);
   return hipGetLastError();
 }
 
-template <class Tr, class Cfg, bool GATED, bool WQ, int KS = 1>
+template <class Tr, class Cfg, bool GATED, bool WQ, int KS = 1, bool SAVE = false>
 hipError_t launch_cfg(const GemmArgs& a, hipStream_t stream) {
   constexpr int BN = Cfg::WN * Cfg::WTN;
   const int NT = (a.N + BN - 1) / BN;
@@ -1039,7 +1078,7 @@ hipError_t launch_cfg(const GemmArgs& a, hipStream_t stream) {
   const long long grid = ((units + round - 1) / round) * round;
   if (grid == 0) return hipSuccess;
   hipLaunchKernelGGL((grouped_gemm_kernel<Tr, Cfg::BM, Cfg::WTN, Cfg::WN, Cfg::WK, GATED, Cfg::PF, Cfg::NTMS, WQ, Cfg::RS,
-                                         Cfg::WS, KS, Cfg::PP>),
+                                         Cfg::WS, KS, Cfg::PP, SAVE>),
                      dim3((unsigned)grid), dim3(64 * Cfg::WN * Cfg::WK), 0, stream, a);
   return hipGetLastError();
 }
@@ -1116,10 +1155,10 @@ hipError_t launch_down_combine(const GemmArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <class Tr, bool GATED, bool WQ = false>
+template <class Tr, bool GATED, bool WQ = false, bool SAVE = false>
 hipError_t dispatch_bm(int BM, const GemmArgs& a, hipStream_t stream) {
   if constexpr (GATED && !WQ && std::is_same<Tr, TBF16>::value) {
-    if (BM == 160 && a.wide && a.tile_off2 == nullptr) return launch_wide<Tr, Wide160>(a, stream);
+    if (BM == 160 && a.wide && a.tile_off2 == nullptr) return launch_wide<Tr, Wide160, SAVE>(a, stream);
   }
   if constexpr (!GATED && std::is_same<Tr, TBF16>::value) {
     if (BM == 160 && a.kpart != nullptr) return launch_cfg<Tr, Split160, false, WQ, 2>(a, stream);
@@ -1130,7 +1169,7 @@ hipError_t dispatch_bm(int BM, const GemmArgs& a, hipStream_t stream) {
   switch (BM) {
 #define MOE_BM_CASE(bm) \
   case bm:              \
-    return launch_cfg<Tr, typename TileCfg<bm, GATED, WQ>::type, GATED, WQ>(a, stream);
+    return launch_cfg<Tr, typename TileCfg<bm, GATED, WQ>::type, GATED, WQ, 1, SAVE>(a, stream);
     MOE_BM_CASE(16)
     MOE_BM_CASE(32)
     MOE_BM_CASE(48)

@@ -114,6 +114,12 @@ struct GemmArgs {
   const float* comb_w;
   const int32_t* comb_row_of;
   int comb_T, comb_k;
+  // Gate+up that also keeps both projections in 8 bits (moe_saved8_t): codes
+  // [R][N] and exponents [R][N / 16], else null.
+  int8_t* save_gate;
+  int8_t* save_up;
+  uint8_t* save_gate_exp;
+  uint8_t* save_up_exp;
 };
 
 // y[r] = rounded(part[0][r] + part[1][r]) for every row r with token_of[r] >= 0:
@@ -134,6 +140,8 @@ constexpr size_t kNoallocScratchBytes = size_t(128) << 20;
 hipError_t noalloc_scratch(void** out);
 
 hipError_t launch_gemm_bf16_gateup(int BM, const GemmArgs& a, hipStream_t stream);
+hipError_t launch_gemm_bf16_gateup_save(int BM, const GemmArgs& a, hipStream_t stream);
+hipError_t launch_gemm_f32_gateup_save(int BM, const GemmArgs& a, hipStream_t stream);
 hipError_t launch_gemm_bf16_down(int BM, const GemmArgs& a, hipStream_t stream);
 hipError_t launch_gemm_f32_gateup(int BM, const GemmArgs& a, hipStream_t stream);
 hipError_t launch_gemm_f32_down(int BM, const GemmArgs& a, hipStream_t stream);
@@ -141,9 +149,110 @@ hipError_t launch_gemm_fp8w_gateup(int BM, const GemmArgs& a, hipStream_t stream
 hipError_t launch_gemm_fp8w_down(int BM, const GemmArgs& a, hipStream_t stream);
 
 inline hipError_t launch_grouped_gemm(int dtype, bool gated, int BM, const GemmArgs& a, hipStream_t stream) {
+  if (gated && a.save_gate != nullptr)
+    return dtype == 1 ? launch_gemm_bf16_gateup_save(BM, a, stream) : launch_gemm_f32_gateup_save(BM, a, stream);
   if (a.s0 != nullptr) return gated ? launch_gemm_fp8w_gateup(BM, a, stream) : launch_gemm_fp8w_down(BM, a, stream);
   if (dtype == 1) return gated ? launch_gemm_bf16_gateup(BM, a, stream) : launch_gemm_bf16_down(BM, a, stream);
   return gated ? launch_gemm_f32_gateup(BM, a, stream) : launch_gemm_f32_down(BM, a, stream);
 }
+
+// ---- backward pass ----
+
+// dy[row_of[f]] = w_f dout[f / k] and dw_f = <dout[f / k], y[row_of[f]]>.
+hipError_t launch_combine_backward(int dtype, const void* dout, const void* y, const float* topk_w,
+                                   const int32_t* row_of, int T, int k, int d, void* dy, float* dw,
+                                   hipStream_t stream);
+
+// dx[t] = sum_j dx_perm[row_of[t k + j]], plus, with dz set, sum_j dz[t k + j]
+// w_router[ids[t k + j]] (dx_perm may then be null).
+hipError_t launch_token_backward(int dtype, const void* dx_perm, const int32_t* row_of, const float* dz,
+                                 const int32_t* ids, const void* w_router, int T, int k, int d, int E, void* dx,
+                                 hipStream_t stream);
+
+// dz_f = w_f (dw_f - sum_i w_i dw_i), and its dense form by K step for the
+// router's weight gradient (hi, and with bf16 lo: [ceil(T / KS)][E][KS]).
+hipError_t launch_route_dz(int dtype, const int32_t* ids, const float* w, const float* dw, int T, int k, int E,
+                           float* dz, void* dense_hi, void* dense_lo, hipStream_t stream);
+
+struct RouteWgradArgs {
+  const void* dz_hi;  // [steps of all tokens][E][64 bytes]
+  const void* dz_lo;  // the same, or null (fp32)
+  const void* x;      // [T][d]
+  float* part;        // [ranges][E][d]
+  int T, E, d;
+  int steps;          // K steps of one range of tokens
+};
+// Columns of x that one workgroup of it takes, by moe_dtype_t (64 experts each).
+constexpr int kRouteGradCols[2] = {64, 128};
+hipError_t launch_route_wgrad_bf16(const RouteWgradArgs& a, int ranges, hipStream_t stream);
+hipError_t launch_route_wgrad_f32(const RouteWgradArgs& a, int ranges, hipStream_t stream);
+// dw_router = sum of the ranges (fp32, in order, one rounding); dbias_e = sum of dz over the entries of e.
+hipError_t launch_route_finish(int dtype, const float* part, int ranges, const int32_t* ids, const float* dz, int T,
+                               int k, int E, int d, void* dw_router, float* dbias, hipStream_t stream);
+
+// Rows in expert order for the backward GEMMs: x_perm and dout_perm (bit
+// copies) and the routing weight of each row.
+hipError_t launch_gather_backward(const void* x, const void* dout, const float* topk_w, const int32_t* row_of, int Tk,
+                                  int k, int64_t row_bytes, void* x_perm, void* dout_perm, float* wrow,
+                                  hipStream_t stream);
+// dw_f = sum of the row's partial sums in order; 0 for an entry without a row.
+hipError_t launch_dot_finish(const float* dot, int ld, const int32_t* row_of, int Tk, float* dw, hipStream_t stream);
+
+// Values of the 8-bit projections of every live row (bf16 holds each exactly).
+hipError_t launch_saved8_unpack(const int8_t* g8, const int8_t* u8, const uint8_t* gx, const uint8_t* ux,
+                                const int32_t* token_of, int64_t rows, int F, void* gate, void* up,
+                                hipStream_t stream);
+
+// Where each expert's rows lie (C = 0: one run from offsets[e]).
+struct GradRows {
+  const int32_t* counts;
+  const int32_t* offsets;
+  const int32_t* spill_offsets;
+  int E, C;
+};
+
+struct DgradArgs {
+  GradRows rows;
+  const void* a0;  // [R][K]
+  const void* a1;  // second activation operand, or null
+  const void* b0;  // [E][K][N]
+  const void* b1;
+  int K, N, blocked16;
+  void* out;  // [R][N]
+  // with the SwiGLU's gradient (out unused): a0 = dout rows, K = d, N = F
+  const float* wrow;
+  const int8_t* g8;
+  const int8_t* u8;
+  const uint8_t* gx;
+  const uint8_t* ux;
+  void* dg;
+  void* du;
+  void* hw;    // w_r h, or null
+  float* dot;  // [R][dot_ld] partial sums of <D, h>
+  int dot_ld;
+};
+
+struct WgradArgs {
+  GradRows rows;
+  int n;              // products
+  const void* P[3];   // [R][M]
+  const void* Q[3];   // [R][N]
+  void* out[3];       // [E][M][N]
+  int M[3], N[3];
+  int first[3];       // first unit of each product inside an expert (set by the launcher)
+  int units;
+  int blocked16;
+};
+
+// Partial sums of <D, h> that dgrad writes for a row, and the row-tile bound
+// of its grid: both depend on the tile the mean row count selects.
+int dgrad_dot_ld(int dtype, int mean, int F);
+int dgrad_tile_rows(int dtype, int mean);
+hipError_t launch_dgrad(int dtype, bool dh, int mean, const DgradArgs& a, long long max_tiles, hipStream_t stream);
+hipError_t launch_wgrad(int dtype, int mean, const WgradArgs& a, hipStream_t stream);
+hipError_t launch_dgrad_bf16(bool dh, int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream);
+hipError_t launch_dgrad_f32(bool dh, int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream);
+hipError_t launch_wgrad_bf16(int BM, const WgradArgs& a, hipStream_t stream);
+hipError_t launch_wgrad_f32(int BM, const WgradArgs& a, hipStream_t stream);
 
 }  // namespace moe

@@ -315,6 +315,130 @@ moe_status_t moe_forward_fp8(const moe_shape_t* s, const void* x, const void* w_
                              const float* s_up, const float* s_down, void* out, void* workspace,
                              size_t ws_bytes, moe_forward_views_t* views_out, hipStream_t stream);
 
+/* ---- backward pass -------------------------------------------------------
+ * Gradients of the layer and of its steps, for training.  What a layer keeps
+ * between its forward and its backward pass: its input x, topk_ids and topk_w,
+ * the dispatch arrays, and the two projections g = x W_gate^T, u = x W_up^T of
+ * every row in 8 bits (moe_saved8_t); h and y_perm are not kept.
+ *
+ * 8-bit form.  16 consecutive columns of a row of g (or u) are a block.  With
+ * b = max(7, exponent field of the block's largest magnitude as fp32):
+ *   code = min(127, max(-127, rint(v 2^(133 - b)))),   value = code 2^(b - 133),
+ * rint rounding ties to even, taken from the fp32 sums.  A value is off by at
+ * most 2^(b - 134) (half a step), or by less than one step where the largest
+ * code is clamped; relative to the block's largest magnitude that is at most
+ * 2^-7.  A block with a NaN or an infinity has b = 255 and reads as NaN in all
+ * 16 columns.  Magnitudes below 2^-127 read as 0.  Every value is exact in bf16.
+ *
+ * Beyond the conventions above: the pointers of these calls must be 16-byte
+ * aligned (topk arrays, their gradients, dbias and counts 4-byte; else
+ * MOE_ERR_INVALID_ARG); output buffers must not overlap inputs.  Rows that hold no
+ * token are neither read nor written.  Entries without a row (an id outside
+ * [0, E)) get gradient 0 for their routing weight and contribute nothing. */
+
+/* Sizes for a shape (host values). */
+typedef struct moe_backward_sizes {
+  size_t saved8_bytes;      /* for moe_saved8_carve                                */
+  size_t route_ws_bytes;    /* workspace of moe_route_backward                     */
+  size_t ffn_ws_bytes;      /* workspace of moe_grouped_ffn_backward               */
+  size_t backward_ws_bytes; /* workspace of moe_backward (the largest of the three) */
+} moe_backward_sizes_t;
+moe_status_t moe_backward_query(const moe_shape_t* s, moe_backward_sizes_t* out);
+
+/* The two projections of every row in 8 bits (device arrays). */
+typedef struct moe_saved8 {
+  int8_t* gate;      /* [R][F]    codes of g                 */
+  int8_t* up;        /* [R][F]    codes of u                 */
+  uint8_t* gate_exp; /* [R][F/16] exponent b of each block   */
+  uint8_t* up_exp;   /* [R][F/16]                            */
+} moe_saved8_t;
+
+/* Point the arrays of `saved` (host struct) into the device buffer `base` of
+ * `bytes` bytes (>= saved8_bytes; 256-byte aligned).  Host only. */
+moe_status_t moe_saved8_carve(const moe_shape_t* s, void* base, size_t bytes, moe_saved8_t* saved);
+
+/* moe_ffn_gate_up_gather that also writes g and u in the 8-bit form; h is
+ * bitwise that of moe_ffn_gate_up_gather. */
+moe_status_t moe_ffn_gate_up_save8(const moe_shape_t* s, const void* x, const void* w_gate, const void* w_up,
+                                   const moe_dispatch_t* disp, int pass, void* h, const moe_saved8_t* saved,
+                                   hipStream_t stream);
+
+/* The values that the codes stand for, as bf16 whatever the shape's dtype
+ * (exact): gate, up [R,F]. */
+moe_status_t moe_saved8_unpack(const moe_shape_t* s, const moe_saved8_t* saved, const moe_dispatch_t* disp,
+                               void* gate, void* up, hipStream_t stream);
+
+/* Gradient of moe_combine:
+ *   dy_perm[row_of[f]] = topk_w[f] * dout[f / k]              (rounded to dtype)
+ *   dtopk_w[f] = sum_i dout[f / k, i] * y_perm[row_of[f], i]  (fp32)
+ * dout [T,d]; y_perm, dy_perm [R,d]; topk_w, dtopk_w [T,k] fp32. */
+moe_status_t moe_combine_backward(const moe_shape_t* s, const void* dout, const void* y_perm, const float* topk_w,
+                                  const moe_dispatch_t* disp, void* dy_perm, float* dtopk_w, hipStream_t stream);
+
+/* Gradient of moe_permute's gather:
+ *   dx[t] = sum_j dx_perm[row_of[t k + j]]   (fp32 in ascending j, one rounding)
+ * dx_perm [R,d]; dx [T,d]. */
+moe_status_t moe_permute_backward(const moe_shape_t* s, const void* dx_perm, const moe_dispatch_t* disp, void* dx,
+                                  hipStream_t stream);
+
+/* Gradient of moe_route for given topk_ids and topk_w [T,k].  The weights are
+ * the softmax over a token's chosen logits, so with dtopk_w [T,k] fp32
+ *   dz[f] = topk_w[f] (dtopk_w[f] - sum_i topk_w[t,i] dtopk_w[t,i])
+ *   dx[t] = sum_j dz[t k + j] w_router[topk_ids[t,j]]
+ *   dw_router[e] = sum over entries f of expert e of dz[f] x[f / k]
+ *   dbias[e] = sum over entries f of expert e of dz[f]
+ * x, dx [T,d]; w_router, dw_router [E,d] (dtype); dbias [E] fp32 or NULL.  In
+ * dw_router of a bf16 shape dz enters as a sum of two bf16 terms (16 bits of its
+ * significand).  workspace of >= route_ws_bytes (256-byte aligned). */
+moe_status_t moe_route_backward(const moe_shape_t* s, const void* x, const void* w_router, const int32_t* topk_ids,
+                                const float* topk_w, const float* dtopk_w, void* dx, void* dw_router, float* dbias,
+                                void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/* Gradient of the experts' products and of the weights applied to them, from
+ * the 8-bit projections, over every pass.  For row r of expert e, token t and
+ * entry f, with sg = 1 / (1 + exp(-g)), h = g sg u:
+ *   D = dout[t] W_down             dtopk_w[f] = <D, h>    (fp32)
+ *   du = topk_w[f] D g sg,         dg = topk_w[f] D u sg (1 + g (1 - sg))
+ *   dx_perm[r] = dg W_gate + du W_up
+ *   dw_down[e] = sum_r dout[t]^T (topk_w[f] h)
+ *   dw_gate[e] = sum_r dg^T x[t],  dw_up[e] = sum_r du^T x[t]
+ * <D, h> equals <dout, y> up to h's 8 bits, which is why no y_perm is needed.
+ * dg, du and topk_w h are rounded to dtype between the products.  x, dout
+ * [T,d]; dx_perm [R,d]; weights and their gradients as in moe_grouped_ffn, the
+ * gradients in the weights' storage order (weight_layout).  Every element of a
+ * given gradient is written (an expert without rows gets zeros); dw_gate and
+ * dw_up (both or neither) and dw_down may be NULL: not computed.  workspace of
+ * >= ffn_ws_bytes (256-byte aligned). */
+moe_status_t moe_grouped_ffn_backward(const moe_shape_t* s, const void* x, const void* dout, const float* topk_w,
+                                      const void* w_gate, const void* w_up, const void* w_down,
+                                      const moe_dispatch_t* disp, const moe_saved8_t* saved, void* dx_perm,
+                                      float* dtopk_w, void* dw_gate, void* dw_up, void* dw_down, void* workspace,
+                                      size_t ws_bytes, hipStream_t stream);
+
+/* moe_forward for training: `out` is bitwise that of moe_forward, and what the
+ * backward pass needs is left in the caller's buffers: topk_ids and topk_w
+ * [T,k] (computed where w_router is not NULL, else read), disp (from
+ * moe_dispatch_carve) and saved (from moe_saved8_carve).  workspace as for
+ * moe_forward; it may be reused as soon as the call's work is done. */
+moe_status_t moe_forward_save8(const moe_shape_t* s, const void* x, const void* w_router, const float* bias,
+                               int32_t* topk_ids, float* topk_w, const void* w_gate, const void* w_up,
+                               const void* w_down, void* out, const moe_dispatch_t* disp, const moe_saved8_t* saved,
+                               void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/* The whole layer's backward pass after moe_forward_save8 with the same x,
+ * weights, topk_ids and topk_w: moe_grouped_ffn_backward, then the router's
+ * gradient (w_router not NULL) and
+ *   dx[t] = sum_j dx_perm[row_of[t k + j]] + sum_j dz[t k + j] w_router[topk_ids[t,j]]
+ * in fp32 with one rounding.  dout, dx [T,d]; dtopk_w [T,k] is always written.
+ * With w_router NULL (the routing is the caller's) dw_router and dbias must be
+ * NULL; else dw_router is required and dbias may be NULL.  workspace of >=
+ * backward_ws_bytes (256-byte aligned). */
+moe_status_t moe_backward(const moe_shape_t* s, const void* x, const void* w_router, const int32_t* topk_ids,
+                          const float* topk_w, const void* w_gate, const void* w_up, const void* w_down,
+                          const moe_dispatch_t* disp, const moe_saved8_t* saved, const void* dout, void* dx,
+                          float* dtopk_w, void* dw_router, float* dbias, void* dw_gate, void* dw_up, void* dw_down,
+                          void* workspace, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -3,6 +3,6 @@
 Only the test suite, the package smoke check and the benchmark's CPU-baseline
 leg use this package.
 """
-from . import brute, moe_oracle
+from . import backward, brute, moe_oracle
 
-__all__ = ["brute", "moe_oracle"]
+__all__ = ["backward", "brute", "moe_oracle"]

@@ -5,15 +5,15 @@ namespace moe {
 namespace {
 using namespace grad;
 // data gradients, by row-tile height
-using D256 = Tile<TBF16, 256, 256, 2, 4, false, 4, false>;
-using D128 = Tile<TBF16, 128, 256, 2, 4, false, 4, false>;
-using D64 = Tile<TBF16, 64, 128, 1, 4, false, 4, false>;
-using D32 = Tile<TBF16, 32, 128, 1, 4, false, 4, false>;
+using D256 = Tile<TBF16, 256, 256, 2, 4, false, 4, 1, true>;
+using D128 = Tile<TBF16, 128, 256, 2, 4, false, 4, 1, true>;
+using D64 = Tile<TBF16, 64, 128, 1, 4, false, 4, 3, false>;
+using D32 = Tile<TBF16, 32, 128, 1, 4, false, 4, 3, false>;
 // weight gradients
-using W256 = Tile<TBF16, 256, 256, 2, 4, true, 4, false>;
-using W128 = Tile<TBF16, 128, 128, 2, 2, true, 4, false>;
+using W256 = Tile<TBF16, 256, 256, 2, 4, true, 4, 1, true>;
+using W128 = Tile<TBF16, 128, 128, 2, 2, true, 4, 2, false>;
 // router weight gradient: experts by columns
-using R64 = Tile<TBF16, 64, 128, 1, 4, false, 4, false>;
+using R64 = Tile<TBF16, 64, 128, 1, 4, false, 4, 3, false>;
 
 template <bool DH>
 hipError_t dgrad_bm(int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream) {

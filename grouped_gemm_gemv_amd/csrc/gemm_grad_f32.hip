@@ -5,8 +5,8 @@ namespace moe {
 namespace {
 using namespace grad;
 // fp32 MFMAs run at a sixteenth of the bf16 rate, so small tiles keep up
-using D64 = Tile<TF32, 64, 64, 2, 2, false, 4, false>;
-using W64 = Tile<TF32, 64, 64, 2, 2, true, 4, false>;
+using D64 = Tile<TF32, 64, 64, 2, 2, false, 4, 4, false>;
+using W64 = Tile<TF32, 64, 64, 2, 2, true, 4, 4, false>;
 }  // namespace
 
 hipError_t launch_dgrad_f32(bool dh, int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream) {

@@ -550,7 +550,7 @@ BackPlan back_plan(const moe_shape_t& s) {
   b.part = take(4 * (size_t)b.ranges * s.E * s.d);
   b.route_ws = o;
   b.mean = (int)mean_rows(s);
-  b.dot_ld = moe::dgrad_dot_ld(s.dtype, b.mean, s.F);
+  b.dot_ld = s.F / moe::dgrad_dot_cols(s.dtype, b.mean);
   o = 0;
   b.x_perm = take(R * s.d * eb);
   b.dout_perm = take(R * s.d * eb);
@@ -590,14 +590,15 @@ moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const
   const int Tk = s.T * s.k;
   const int64_t row_bytes = (int64_t)s.d * elt_bytes(s);
   float* wrow = reinterpret_cast<float*>(ws + b.wrow);
-  if (moe::launch_gather_backward(x, dout, topk_w, d.row_of, Tk, s.k, row_bytes, ws + b.x_perm, ws + b.dout_perm, wrow,
-                                  st) != hipSuccess)
+  if (moe::launch_gather_backward(x, dout, topk_w, d.token_of, d.row_of, row_space(s), s.k, row_bytes, ws + b.x_perm,
+                                  ws + b.dout_perm, wrow, st) != hipSuccess)
     return MOE_ERR_HIP;
   const int BM = moe::dgrad_tile_rows(s.dtype, b.mean);
   const int64_t tiles = pass_max_tiles(s, BM, 0) + pass_max_tiles(s, BM, 1);
   moe::DgradArgs a{};
   a.rows = grad_rows(s, d);
   a.blocked16 = s.weight_layout == MOE_LAYOUT_BLOCKED16 ? 1 : 0;
+  a.panel = (size_t)row_space(s) * 64;
   a.a0 = ws + b.dout_perm;
   a.b0 = w_down;
   a.K = s.d;
@@ -624,6 +625,7 @@ moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const
   moe::WgradArgs g{};
   g.rows = a.rows;
   g.blocked16 = a.blocked16;
+  g.panel = a.panel;
   auto add = [&](const void* P, const void* Q, void* out, int M, int N) {
     g.P[g.n] = P;
     g.Q[g.n] = Q;

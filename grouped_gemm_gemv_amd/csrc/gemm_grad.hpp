@@ -12,17 +12,21 @@
 // The data gradients contract over the rows of a weight matrix, the weight
 // gradients over the rows of the activations, so at least one operand of
 // every product has its K index on the strided axis of memory.  Such an
-// operand is staged in LDS as it lies in memory ([K][columns]) and turned on
-// the way to the registers: bf16 by the transposing LDS read (in each group
-// of 16 lanes, lane i receives column i of a 4 x 16 block), fp32 by reading
-// one element per K row.
+// operand is staged in LDS as it lies in memory and turned on the way to the
+// registers: bf16 by the transposing LDS read (in each group of 16 lanes, lane
+// i receives column i of a 4 x 16 block), fp32 by reading one element per K row.
 //
 // out[m][n] = sum_k Mop[m][k] Nop[k][n]; a workgroup owns a BM x BN tile,
-// WM x WN wavefronts of TM x TN each.  The N operand always has K on the
-// strided axis; the M operand has it contiguous (activation rows of the data
-// gradients) or strided (MKS: the weight gradients).  N is the MFMA "A"
-// operand, so a lane ends with 4 consecutive n of one m, as the outputs lie
-// in memory.
+// WM x WN wavefronts of TM x TN each.  N is the MFMA "A" operand, so a lane ends
+// with 4 consecutive n of one m, as the outputs lie in memory.
+//
+// Activations between the products (x and dout in expert order, dg, du, w_r h)
+// are kept in panels: [columns of 64 bytes][R rows][64 bytes].  A K step of the
+// data gradients (64 bytes of every row of a tile) and 16 K rows of 64 bytes of
+// the weight gradients are then both one run of memory, whatever the width of
+// a row: with rows of 8 or 28 KB the 256 rows of a step lay a multiple of 4 KB
+// apart, on few memory channels, and the first data gradient took 2500 cycles
+// a step instead of 1200.  Weights are read as the caller keeps them.
 //
 // A K step is 64 bytes of a K-contiguous row (32 bf16 or 16 fp32), so each
 // operand takes 64 bytes of LDS per tile row or column whatever its
@@ -117,33 +121,97 @@ __device__ __forceinline__ void swap16(unsigned& a, unsigned& b) {
 #endif
 }
 
-// Stores one row's NI blocks of 16 columns, of which lane group g = lane / 16
-// holds columns 4g .. 4g + 3 (v[ni][0..3]).  at(n) gives the address of column n
-// of the run; the NI * 16 columns are within a row of a matrix whose storage
-// order keeps 8 (bf16) columns together.  bf16: two blocks at a time, lanes 16
-// apart trade halves so that each lane stores 16 bytes (half the store
-// instructions of 8 bytes a lane, in 64-byte pieces).
-template <class Tr, int NI, class At>
-__device__ __forceinline__ void store_blocks(const float (&v)[NI][4], bool live, int lane, At&& at) {
-  const int g = lane >> 4;
-  if constexpr (sizeof(typename Tr::T) == 2) {
-    static_assert(NI % 2 == 0, "blocks pair up");
-#pragma unroll
-    for (int ni = 0; ni < NI; ni += 2) {
-      unsigned a0 = pack2(v[ni][0], v[ni][1]), a1 = pack2(v[ni][2], v[ni][3]);
-      unsigned b0 = pack2(v[ni + 1][0], v[ni + 1][1]), b1 = pack2(v[ni + 1][2], v[ni + 1][3]);
-      swap16(a0, b0);
-      swap16(a1, b1);
-      // lane groups 0, 2: columns 0-7, 8-15 of block ni; groups 1, 3: of block ni + 1
-      if (live) *reinterpret_cast<uint4*>(at((ni + (g & 1)) * 16 + (g >> 1) * 8)) = make_uint4(a0, a1, b0, b1);
-    }
-  } else {
-#pragma unroll
-    for (int ni = 0; ni < NI; ++ni)
-      if (live)
-        *reinterpret_cast<float4*>(at(ni * 16 + g * 4)) = make_float4(v[ni][0], v[ni][1], v[ni][2], v[ni][3]);
-  }
+// Lanes 32..63 of a trade places with lanes 0..31 of b.
+__device__ __forceinline__ void swap32(unsigned& a, unsigned& b) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+#endif
 }
+// Word w of lane group g (of 16 lanes) becomes word g of lane group w.
+__device__ __forceinline__ void transpose4(unsigned (&w)[4]) {
+  swap32(w[0], w[2]);
+  swap32(w[1], w[3]);
+  swap16(w[0], w[1]);
+  swap16(w[2], w[3]);
+}
+
+// Stores and loads of a buffer of `bytes` bytes at `base`, which the compiler
+// counts itself: past the bound, stores are dropped and loads return zero.
+__device__ __forceinline__ void store16(const char* base, int bytes, int offset, const uint4& v) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass knows no descriptors
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, bytes, 0x00020000);
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), r, offset, 0, 0);
+#endif
+}
+__device__ __forceinline__ uint4 load16(const char* base, int bytes, int offset) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, bytes, 0x00020000);
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
+#else
+  return uint4{};
+#endif
+}
+__device__ __forceinline__ unsigned load4(const char* base, int bytes, int offset) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, bytes, 0x00020000);
+  return __builtin_amdgcn_raw_buffer_load_b32(r, offset, 0, 0);
+#else
+  return 0;
+#endif
+}
+
+// Where a lane's 16 bytes of a wavefront's tile of an output matrix lie: the
+// rows of the matrix (ld bytes), 64-byte pieces of 16 rows in turn (the blocked
+// weight order), or panels.  A store takes 64 bytes of 16 rows: two blocks of
+// 16 columns (bf16) or one (fp32); rows past the bound are dropped.
+template <class Tr>
+struct OutTile {
+  static constexpr int EB = sizeof(typename Tr::T);
+  const char* base;  // of the tile's first row
+  size_t piece;      // bytes to the next 64 bytes of columns
+  int bytes, ld, lane0;
+  // a lane's bytes in the 64: bf16, after the trade below, 16 of block g mod 2
+  __device__ __forceinline__ static int lane_byte(int g) { return EB == 2 ? (g & 1) * 32 + (g >> 1) * 16 : g * 16; }
+  // a row-major or blocked matrix: m0, col0 the wavefront's first row and column
+  __device__ __forceinline__ static OutTile matrix(const char* base, int rows, int ld, int m0, int col0, int lane,
+                                                   int blocked16) {
+    const int g = lane >> 4, i = lane & 15;
+    return OutTile{base + (size_t)(blocked16 ? col0 * EB * 16 : col0 * EB), (size_t)(blocked16 ? 1024 : 64),
+                   rows > 0 ? rows * ld - (blocked16 ? 0 : col0 * EB) : 0, ld,
+                   m0 * ld + i * (blocked16 ? 64 : ld) + lane_byte(g)};
+  }
+  // panels: base of the tile's first row in the panel of the wavefront's first columns
+  __device__ __forceinline__ static OutTile panels(const char* base, size_t panel, int rows, int m0, int lane) {
+    return OutTile{base, panel, rows * 64, 64, (m0 + (lane & 15)) * 64 + lane_byte(lane >> 4)};
+  }
+  // Rows m .. m + 15 (m a multiple of 16, from m0 on), NI blocks of 16 columns of
+  // which lane group g = lane / 16 holds columns 4g .. 4g + 3.  bf16: lanes 16
+  // apart trade halves, so that each stores 16 bytes.
+  template <int NI>
+  __device__ __forceinline__ void put(int m, const float (&v)[NI][4]) const {
+    const int at = lane0 + m * ld;
+    if constexpr (EB == 2) {
+      static_assert(NI % 2 == 0, "blocks pair up");
+#pragma unroll
+      for (int ni = 0; ni < NI; ni += 2) {
+        unsigned a0 = pack2(v[ni][0], v[ni][1]), a1 = pack2(v[ni][2], v[ni][3]);
+        unsigned b0 = pack2(v[ni + 1][0], v[ni + 1][1]), b1 = pack2(v[ni + 1][2], v[ni + 1][3]);
+        swap16(a0, b0);
+        swap16(a1, b1);
+        // lane groups 0, 2: columns 0-7, 8-15 of block ni; groups 1, 3: of block ni + 1
+        store16(base + (ni >> 1) * piece, bytes, at, make_uint4(a0, a1, b0, b1));
+      }
+    } else {
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni)
+        store16(base + ni * piece, bytes, at,
+                make_uint4(__float_as_uint(v[ni][0]), __float_as_uint(v[ni][1]), __float_as_uint(v[ni][2]),
+                           __float_as_uint(v[ni][3])));
+    }
+  }
+};
 
 // Where the operands of one K step lie: base addresses and descriptor bounds.
 struct Step {
@@ -152,10 +220,18 @@ struct Step {
   int mbytes, nbytes;
 };
 
-template <class Tr, int BM_, int BN_, int WM_, int WN_, bool MKS, int S_, int OCC_, bool PP>
+// How an operand lies in memory and LDS.
+enum Operand {
+  kPanelK,  // panels, K along the columns: a step is one panel
+  kPanelR,  // panels, K along the rows: a step is KS rows of every panel of the tile
+  kRows     // a matrix (or blocked weights), K along its rows: a step is KS rows
+};
+
+template <class Tr, int BM_, int BN_, int WM_, int WN_, Operand MOP_, Operand NOP_, int S_, int OCC_, bool PP>
 struct Tile {
   using Elt = typename Tr::T;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, OCC = OCC_;
+  static constexpr Operand MOP = MOP_, NOP = NOP_;
   static constexpr int EB = sizeof(Elt);
   static constexpr int KS = 64 / EB;  // K elements per step
   static constexpr int NW = WM * WN, NTH = 64 * NW;
@@ -165,28 +241,54 @@ struct Tile {
   // ones repeat an operand's final load, so every wavefront issues NL)
   static constexpr int QM = BM / 16, QN = BN / 16;
   static constexpr int LM = (QM + NW - 1) / NW, LN = (QN + NW - 1) / NW, NL = LM + LN;
+  static constexpr int PL = EB == 2 ? 2 : 1;  // loads per panel of KS rows (kPanelR)
+  static_assert(MOP != kRows && NOP != kPanelK, "the M operand comes in panels, the N operand has K along the rows");
   static_assert(TM % 16 == 0 && TN % 16 == 0, "wavefront tile");
-  static_assert(BN * EB % 256 == 0 && (!MKS || BM * EB % 256 == 0), "K-strided operands are swizzled within 256 bytes");
-  static_assert(S >= 3 && (S - 2) * NL < 64, "ring");
+  static_assert(NOP != kRows || BN * EB % 256 == 0, "rows are swizzled within 256 bytes");
+  static_assert(MOP != kPanelR || (QM % NW == 0 && NW % 2 == 0 && TM * EB % 64 == 0), "panels of the M operand");
+  static_assert(NOP != kPanelR || (QN % NW == 0 && NW % 2 == 0 && TN * EB % 64 == 0), "panels of the N operand");
+  static_assert(S >= 3 && (S - 2) * NL + MI * NI * EB / 4 < 64, "ring");
 
-  // LDS swizzle.  A K-contiguous row is 64 bytes: chunk c (16 bytes) of row r
-  // sits at c ^ (r / 2 & 3), so the 8 rows that eight lanes of an operand read
-  // take spread over all banks (r / 4 & 3 took 40 % more LDS cycles).  A K-strided row k holds BM or BN columns (a multiple of 256 bytes):
-  // its chunks are moved in pairs (bf16: a transposing read takes 32 bytes of
-  // 4 rows per 16 lanes; the 8 rows of 32 lanes get 8 different pairs) or in
-  // fours (fp32: 64 bytes of one row per 16 lanes).
+  // LDS layouts, each free of bank conflicts:
+  //  kPanelK: rows of 64 bytes; chunk c (16 bytes) of row r sits at c ^ (r / 2 & 3),
+  //    so the 8 rows that eight lanes of a 16-byte read take cover 128 bytes of
+  //    banks twice over (with r / 4 & 3 the reads took 40 % more cycles);
+  //  kPanelR: the tile's panels in turn, KS rows of 64 bytes each.  bf16: a
+  //    transposing read takes 32 bytes of 4 rows per 16 lanes, 8 rows per 32
+  //    lanes; the halves of rows with bit 3 set trade places.  fp32: 16 lanes
+  //    read 64 bytes of one row, lane groups rows 4 apart; rows are stored in the
+  //    order 0 4 8 12 1 5 ..;
+  //  kRows: KS rows of BN columns (a multiple of 256 bytes); pairs of chunks (bf16)
+  //    or fours (fp32) move within 256 bytes so that the 8 rows (lane groups) of
+  //    32 lanes get different ones.
   __device__ __forceinline__ static int swz_c(int r) { return (r >> 1) & 3; }
   __device__ __forceinline__ static int swz_k(int k) {
     return EB == 2 ? (((k & 3) | ((k >> 1) & 4)) << 1) : ((k >> 2) & 3) << 2;
   }
 
-  // Byte offset inside the operand's step and LDS offset of this lane's slot
-  // in load q of a K-strided operand of `width` columns starting at column
-  // col0 of rows of `cols` elements (ld bytes each).  blocked16: the rows are in
-  // groups of 16, each stored as 1024-byte blocks of 64 bytes from every row.
-  template <int WIDTH>
-  __device__ __forceinline__ static int strided_offset(int q, int lane, int col0, int cols, int ld, int blocked16) {
-    constexpr int CPR = WIDTH * EB / 16;  // chunks per K row
+  __device__ __forceinline__ static int mq(int wave, int i) { return min(wave + i * NW, QM - 1); }
+  __device__ __forceinline__ static int nq(int wave, int i) { return min(wave + i * NW, QN - 1); }
+
+  // Offset in memory of this lane's 16 bytes of a load whose LDS slot is lane * 16:
+  // 16 rows of 64 bytes from one run.
+  template <Operand OP>
+  __device__ __forceinline__ static int panel_offset(int q, int lane) {
+    const int s = lane >> 2, c = lane & 3;
+    if constexpr (OP == kPanelK) {
+      const int r = q * 16 + s;
+      return r * 64 + ((c ^ swz_c(r)) << 4);
+    } else if constexpr (EB == 2) {
+      return s * 64 + ((c ^ ((s >> 2) & 2)) << 4);
+    } else {
+      return ((s >> 2) | (s & 3) << 2) * 64 + (c << 4);
+    }
+  }
+  // kRows: byte offset inside the step of this lane's slot in load q, for a tile
+  // from column col0 on of rows of `cols` elements (ld bytes each).  blocked16: the
+  // rows are in groups of 16, each stored as 1024-byte blocks of 64 bytes from
+  // every row.
+  __device__ __forceinline__ static int rows_offset(int q, int lane, int col0, int cols, int ld, int blocked16) {
+    constexpr int CPR = BN * EB / 16;  // chunks per K row
     const int pos = q * 64 + lane;
     const int k = pos / CPR;
     const int c = (pos - k * CPR) ^ swz_k(k);
@@ -196,64 +298,52 @@ struct Tile {
     return blocked16 ? (k >> 4) * 16 * ld + (byte >> 6) * 1024 + (k & 15) * 64 + (byte & 63) : k * ld + byte;
   }
 
-  // Offset of load q of a K-contiguous operand: 16 rows of 64 bytes.
-  __device__ __forceinline__ static int rows_offset(int q, int lane, int ld) {
-    const int r = q * 16 + (lane >> 2);
-    return r * ld + (((lane & 3) ^ swz_c(r)) << 4);
-  }
-
-  __device__ __forceinline__ static int mq(int wave, int i) { return min(wave + i * NW, QM - 1); }
-  __device__ __forceinline__ static int nq(int wave, int i) { return min(wave + i * NW, QN - 1); }
-
-  // The loads of one step into the stage at LDS address `st`: lane offsets moff, noff.
-  __device__ __forceinline__ static void load(const int (&moff)[LM], const int (&noff)[LN], const Step& s, unsigned st,
-                                              int wave) {
-    const u32x4_t m = descriptor(s.m, s.mbytes), n = descriptor(s.n, s.nbytes);
-#pragma unroll
-    for (int i = 0; i < LM; ++i) load_lds(m, moff[i], st + mq(wave, i) * 1024);
-#pragma unroll
-    for (int i = 0; i < LN; ++i) load_lds(n, noff[i], st + MBYTES + nq(wave, i) * 1024);
-  }
-
   // Operand of the 16 columns (or rows) number sub of the wavefront's part:
-  // columns in one run, rows dealt to the WM wavefront rows in turn, so that a
-  // tile that is not full loads them evenly.  Lane group g = lane / 16 holds K elements 8g..8g+7 (bf16)
-  // or 4g..4g+3 (fp32), whatever the orientation.  `lane0`: lane part of the LDS
-  // address, from frag_lane.
-  template <bool STRIDED, int WIDTH>
+  // columns in one run, rows of kPanelK dealt to the WM wavefront rows in turn,
+  // so that a tile that is not full loads them evenly.  Lane group g = lane / 16
+  // holds K elements 8g..8g+7 (bf16) or 4g..4g+3 (fp32), whatever the layout.
+  // lane0: lane part of the LDS address, from frag_lane.
+  template <Operand OP>
   __device__ __forceinline__ static int frag_lane(int lane, int first) {
     const int g = lane >> 4, i = lane & 15;
-    if constexpr (!STRIDED) {
+    if constexpr (OP == kPanelK) {
       const int r = first + i;
       return r * 64 + ((g ^ swz_c(r)) << 4);
+    } else if constexpr (OP == kPanelR) {
+      const int panel = first * EB / 64 * (KS * 64);
+      return panel + (EB == 2 ? (8 * g + (i >> 2)) * 64 + ((i & 3) * 8 ^ (g & 1) * 32) : g * 64 + i * 4);
     } else if constexpr (EB == 2) {
       const int k = 8 * g + (i >> 2);
       const int byte = first * 2 + (i & 3) * 8;
-      return k * WIDTH * 2 + ((((byte >> 4) ^ swz_k(k)) << 4) | (byte & 15));
+      return k * BN * 2 + ((((byte >> 4) ^ swz_k(k)) << 4) | (byte & 15));
     } else {
       const int k = 4 * g;
       const int byte = (first + i) * 4;
-      return k * WIDTH * 4 + ((((byte >> 4) ^ swz_k(k)) << 4) | (byte & 15));
+      return k * BN * 4 + ((((byte >> 4) ^ swz_k(k)) << 4) | (byte & 15));
     }
   }
-  template <bool STRIDED, int WIDTH>
+  template <Operand OP>
   __device__ __forceinline__ static uint4 frag(const char* st, int lane0, int sub) {
-    if constexpr (!STRIDED) {
+    if constexpr (OP == kPanelK) {
       return *reinterpret_cast<const uint4*>(st + lane0 + sub * WM * 1024);
     } else if constexpr (EB == 2) {
-      // 16 columns are 32 bytes, one pair of chunks: column blocks differ by an
-      // exclusive or in the address (the swizzle stays within 256 bytes)
-      const char* p = st + (lane0 ^ ((sub & 7) << 5)) + (sub >> 3) * 256;
-      const uint2 a = read_tr16(p), b = read_tr16(p + 4 * WIDTH * 2);
+      // kRows: 16 columns are 32 bytes, and column blocks differ by an exclusive
+      // or in the address (the swizzle stays within 256 bytes)
+      const char* p = OP == kPanelR ? st + (lane0 ^ ((sub & 1) << 5)) + (sub >> 1) * 2048
+                                    : st + (lane0 ^ ((sub & 7) << 5)) + (sub >> 3) * 256;
+      const uint2 a = read_tr16(p), b = read_tr16(p + 4 * (OP == kPanelR ? 64 : BN * 2));
       return uint4{a.x, a.y, b.x, b.y};
     } else {
-      const char* p = st + (lane0 ^ ((sub & 3) << 6)) + (sub >> 2) * 256;
+      const char* p = OP == kPanelR ? st + lane0 + sub * 1024 : st + (lane0 ^ ((sub & 3) << 6)) + (sub >> 2) * 256;
+      constexpr int NEXT = OP == kPanelR ? 64 : BN;  // elements to the lane group's next K row
       const unsigned* q = reinterpret_cast<const unsigned*>(p);
-      return uint4{q[0], q[WIDTH], q[2 * WIDTH], q[3 * WIDTH]};
+      return uint4{q[0], q[NEXT], q[2 * NEXT], q[3 * NEXT]};
     }
   }
 
+  static constexpr bool MKS = MOP == kPanelR;
   static __device__ __forceinline__ int m_first(int wave) { return MKS ? (wave / WN) * TM : (wave / WN) * 16; }
+  static constexpr int M_STEP = MKS ? 16 : 16 * WM;  // rows between a wavefront's blocks
   // Row (or column) of the tile that accumulator block mi of this lane holds.
   static __device__ __forceinline__ int m_of(int wave, int mi, int lane) {
     return MKS ? (wave / WN) * TM + mi * 16 + (lane & 15) : (mi * WM + wave / WN) * 16 + (lane & 15);
@@ -284,8 +374,7 @@ struct Tile {
     __device__ __forceinline__ Runner(Job& job_, const char* ring_, unsigned ring_at_, int first, int stride_, int end_,
                                       int lane_, int wave_)
         : job(job_), ring(ring_), ring_at(ring_at_), stride(stride_), end(end_), lane(lane_), wave(wave_),
-          ml(frag_lane<MKS, BM>(lane_, m_first(wave_))),
-          nl(MBYTES + frag_lane<true, BN>(lane_, (wave_ % WN) * TN)), L(first), lj(0), lpad(0), ls(0), cs(0), stores(0) {}
+          ml(frag_lane<MOP>(lane_, m_first(wave_))), nl(MBYTES + frag_lane<NOP>(lane_, (wave_ % WN) * TN)), L(first), lj(0), lpad(0), ls(0), cs(0), stores(0) {}
 
     // A unit takes at least S steps (empty ones behind its own), so the loads,
     // S - 1 steps ahead, are never more than one unit ahead.
@@ -294,7 +383,10 @@ struct Tile {
       const bool in = L < end;  // else past the last unit: empty loads from here on
       if (in) {
         lt = job.decode(L);
-        job.offsets(lt, wave, lane, moff, noff);
+        if constexpr (NOP == kRows) {
+#pragma unroll
+          for (int i = 0; i < LN; ++i) noff[i] = job.rows_offset(lt, nq(wave, i), lane);
+        }
       }
       // (selects, not an else branch: stores of two branches merged into one
       // through a pointer would keep the state in scratch memory)
@@ -303,15 +395,42 @@ struct Tile {
       lj = 0;
       ld = job.first(lt);
     }
-    // issue the next loads; move on to the ones after them
-    __device__ __forceinline__ void feed() { load(moff, noff, ld, ring_at + ls * STAGE, wave); }
+    // Where the loads after the next ones lie: worked out without a branch
+    // (`turn`, behind it, opens the next unit), so that it fits between MFMAs.
     __device__ __forceinline__ void advance() {
       ls = ls == S - 1 ? 0 : ls + 1;
-      if (++lj == lpad) {
+      ++lj;
+      job.next(lt, lj, ld);
+    }
+    __device__ __forceinline__ void turn() {
+      if (lj == lpad) {
         L += stride;
         open();
-      } else {
-        job.next(lt, lj, ld);
+      }
+    }
+    // Load i of this wavefront of an operand in panels with K along the rows: 16
+    // of the step's rows of one panel, nothing behind the last row or panel.
+    __device__ __forceinline__ u32x4_t panel_desc(const char* base, int bytes, int i, int panels) const {
+      const int q = wave + i * NW, panel = q / PL, half = q % PL * 1024;
+      const int n = panel < panels ? min(max(bytes - half, 0), 1024) : 0;
+      return descriptor(base + panel * lt.panel + half, n);
+    }
+    // Issues the next loads and, from i = 0 on, an equal share of the work `between`
+    // after each of them.
+    template <class Between>
+    __device__ __forceinline__ void feed(Between&& between) {
+      const u32x4_t m = descriptor(ld.m, ld.mbytes), n = descriptor(ld.n, ld.nbytes);
+      const unsigned at = ring_at + ls * STAGE;
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int in = i < LM ? 0 : i - LM;
+        if (i < LM)
+          load_lds(MOP == kPanelR ? panel_desc(ld.m, ld.mbytes, i, lt.mpanels) : m, moff[i < LM ? i : 0],
+                   at + mq(wave, i) * 1024);
+        else
+          load_lds(NOP == kPanelR ? panel_desc(ld.n, ld.nbytes, in, lt.npanels) : n, noff[in],
+                   at + MBYTES + nq(wave, in) * 1024);
+        between(i);
       }
     }
     __device__ __forceinline__ static void barrier() {
@@ -320,13 +439,22 @@ struct Tile {
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
       __builtin_amdgcn_sched_barrier(0);
     }
+    // The next loads and this step's operands.  The loads go through the vector
+    // memory path (64 bytes a cycle and compute unit), the operands through LDS:
+    // issued in turn, they overlap.
     template <int MB>
-    __device__ __forceinline__ void read_frags() {
+    __device__ __forceinline__ void move() {
       const char* st = ring + cs * STAGE;
+      constexpr int FR = NI + MB, PER = (FR + NL - 1) / NL;  // operands behind each load
+      feed([&](int i) {
 #pragma unroll
-      for (int ni = 0; ni < NI; ++ni) nf[ni] = frag<true, BN>(st, nl, ni);
-#pragma unroll
-      for (int mi = 0; mi < MB; ++mi) mf[mi] = frag<MKS, BM>(st, ml, mi);
+        for (int f = i * PER; f < (i + 1) * PER && f < FR; ++f) {
+          if (f < NI)
+            nf[f < NI ? f : 0] = frag<NOP>(st, nl, f);
+          else
+            mf[f < NI ? 0 : f - NI] = frag<MOP>(st, ml, f - NI);
+        }
+      });
       cs = cs == S - 1 ? 0 : cs + 1;
     }
     template <int MB>
@@ -345,10 +473,10 @@ struct Tile {
     __device__ __forceinline__ void step() {
       wait_step();
       barrier();
-      feed();
-      read_frags<MB>();
+      move<MB>();
       advance();
       multiply<MB>();
+      turn();
     }
 
     // Ping-pong step (PP): the two wavefronts of each SIMD (w and w + NW / 2) take
@@ -362,13 +490,18 @@ struct Tile {
     // it in the data phase, that phase was the longer one and set the pace.
     template <int MB>
     __device__ __forceinline__ void step_pp() {
-      read_frags<MB>();
-      feed();
+      move<MB>();
       wait_step();
       wait_lds();
       barrier();
       advance();
       multiply<MB>();
+#pragma unroll
+      for (int i = 0; i < MB * NI; ++i) {  // one MFMA, then up to two scalar instructions in its shadow
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x4, 2, 0);
+      }
+      turn();
       barrier();
     }
     // Waits until this wavefront's loads of one step have landed, with those of the
@@ -398,14 +531,21 @@ struct Tile {
       }
     }
 
+    __device__ __forceinline__ bool done() const { return L >= end; }
+
     __device__ __forceinline__ void run() {
       if (L >= end) return;
+#pragma unroll
+      for (int i = 0; i < LM; ++i) moff[i] = panel_offset<MOP>(mq(wave, i), lane);
+#pragma unroll
+      for (int i = 0; i < LN; ++i) noff[i] = NOP == kPanelR ? panel_offset<NOP>(0, lane) : 0;
       open();
       ct = lt;
 #pragma unroll 1
       for (int u = 0; u < S - 1; ++u) {  // within the first unit's padded steps
-        feed();
+        feed([](int) {});
         advance();
+        turn();
       }
       const bool second = wave >= NW / 2;
       if constexpr (PP) {
@@ -425,11 +565,14 @@ struct Tile {
           steps<(MI + 1) / 2>(padded(ct));
         else
           steps<MI>(padded(ct));
+        // both halves store at the same time: in turn, each would wait for the
+        // other's stores (4000 of a tile's 62000 cycles)
+        if (PP && !second) barrier();
         stores = job.store(ct, wave, lane, acc) ? S - 2 : 0;
-        if (L >= end) break;
-        ct = lt;  // the next unit
+        if (done()) break;
+        if (PP && second) barrier();
+        ct = lt;  // the next unit: the loads are S - 1 steps ahead, less than a unit
       }
-      if (PP && !second) barrier();
       wait_vm<0>();  // the empty loads past the last unit still write LDS
     }
   };
@@ -503,6 +646,8 @@ struct DgradJob {
   struct Info {
     int steps, row0, rows, nbase, e;
     const char *a0, *a1, *b0, *b1;  // operands of the tile's rows and expert
+    size_t panel;                   // bytes of a panel of activations
+    int mpanels, npanels;
   };
   const DgradArgs& p;
   const ExpertTable& tab;
@@ -536,89 +681,114 @@ struct DgradJob {
     i.rows = min(T::BM, n - first);
     i.nbase = nt * T::BN;
     i.steps = per * (p.a1 != nullptr ? 2 : 1);
-    const size_t act = (size_t)i.row0 * p.K * EB, mat = (size_t)e * p.K * p.N * EB;
+    const size_t act = (size_t)i.row0 * 64, mat = (size_t)e * p.K * p.N * EB;
+    i.panel = p.panel;
     i.a0 = static_cast<const char*>(p.a0) + act;
     i.b0 = static_cast<const char*>(p.b0) + mat;
     i.a1 = DH ? i.a0 : static_cast<const char*>(p.a1) + act;
     i.b1 = DH ? i.b0 : static_cast<const char*>(p.b1) + mat;
     return i;
   }
-  __device__ __forceinline__ void offsets(const Info& t, int wave, int lane, int (&moff)[T::LM],
-                                          int (&noff)[T::LN]) const {
-#pragma unroll
-    for (int i = 0; i < T::LM; ++i) moff[i] = T::rows_offset(T::mq(wave, i), lane, p.K * EB);
-#pragma unroll
-    for (int i = 0; i < T::LN; ++i)
-      noff[i] = T::template strided_offset<T::BN>(T::nq(wave, i), lane, t.nbase, p.N, p.N * EB, p.blocked16);
+  __device__ __forceinline__ int rows_offset(const Info& t, int q, int lane) const {
+    return T::rows_offset(q, lane, t.nbase, p.N, p.N * EB, p.blocked16);
   }
   __device__ __forceinline__ Step first(const Info& t) const {
-    return t.steps > 0 ? Step{t.a0, t.b0, t.rows * p.K * EB, T::KS * p.N * EB} : Step{t.a0, t.b0, 0, 0};
+    return t.steps > 0 ? Step{t.a0, t.b0, t.rows * 64, T::KS * p.N * EB} : Step{t.a0, t.b0, 0, 0};
   }
-  // Step j: 64 bytes on in the activation rows, KS rows on in the weights.
+  // Step j: a panel on in the activations, KS rows on in the weights.
   __device__ __forceinline__ void next(const Info& t, int j, Step& s) const {
     const int nrows = T::KS * p.N * EB;
-    s.m += 64;
-    s.n += nrows;
-    s.mbytes = max(s.mbytes - 64, 0);
-    if (!DH && j == per) {
-      s.m = t.a1;
-      s.n = t.b1;
-      s.mbytes = t.rows * p.K * EB;
-    }
-    if (j >= t.steps) s.mbytes = s.nbytes = 0;
+    const bool turn = !DH && j == per, in = j < t.steps;
+    s.m = turn ? t.a1 : s.m + t.panel;
+    s.n = turn ? t.b1 : s.n + nrows;
+    s.mbytes = in ? t.rows * 64 : 0;
+    s.nbytes = in ? nrows : 0;
   }
   // The saved projections of one row's NI blocks of 16 columns.
   struct Saved {
-    unsigned g[T::NI], u[T::NI], gx, ux;  // four codes each; the blocks' exponents, one byte each
+    unsigned g[4], u[4], gx, ux;  // NI words of four codes each; the blocks' exponents, one byte each
     float w;
   };
-  __device__ __forceinline__ void read_saved(const Info& t, int mi, int n0, int wave, int lane, Saved& s) const {
-    const int m = T::m_of(wave, mi, lane);
-    const size_t row = (size_t)t.row0 + (m < t.rows ? m : 0);
-    const size_t o = row * p.N + n0;
+  // With four blocks a lane reads the 16 codes of block g = lane / 16 of its row;
+  // `turn` then deals out the words, so that it holds its four columns of every
+  // block (a word at a time, the reads of the scattered rows took 0.8 ms of the
+  // 1.7 of 8192 rows at d = 4096, F = 14336).  Rows past the tile's last read zeros.
+  __device__ __forceinline__ void read_saved(const Info& t, int m, int n0, int lane, Saved& s) const {
+    const size_t o = (size_t)t.row0 * p.N;
+    const char *g8 = reinterpret_cast<const char*>(p.g8) + o, *u8 = reinterpret_cast<const char*>(p.u8) + o;
+    const char *gx = reinterpret_cast<const char*>(p.gx) + (o >> 4), *ux = reinterpret_cast<const char*>(p.ux) + (o >> 4);
+    const int row = m * p.N + n0, bytes = t.rows * p.N, g = lane >> 4;
+    if constexpr (T::NI == 4) {
+      const uint4 a = load16(g8, bytes, row + g * 16), b = load16(u8, bytes, row + g * 16);
+      s.g[0] = a.x, s.g[1] = a.y, s.g[2] = a.z, s.g[3] = a.w;
+      s.u[0] = b.x, s.u[1] = b.y, s.u[2] = b.z, s.u[3] = b.w;
+    } else {
 #pragma unroll
-    for (int ni = 0; ni < T::NI; ++ni) {
-      s.g[ni] = *reinterpret_cast<const unsigned*>(p.g8 + o + ni * 16 + (lane >> 4) * 4);
-      s.u[ni] = *reinterpret_cast<const unsigned*>(p.u8 + o + ni * 16 + (lane >> 4) * 4);
+      for (int ni = 0; ni < T::NI; ++ni) {
+        s.g[ni] = load4(g8, bytes, row + ni * 16 + g * 4);
+        s.u[ni] = load4(u8, bytes, row + ni * 16 + g * 4);
+      }
     }
-    using Exps = std::conditional_t<T::NI == 4, uint32_t, uint16_t>;
+    // exponents of four blocks, of which two are this wavefront's with NI = 2
     static_assert(T::NI == 4 || T::NI == 2, "exponents of a wavefront's columns in one load");
-    s.gx = *reinterpret_cast<const Exps*>(p.gx + (o >> 4));
-    s.ux = *reinterpret_cast<const Exps*>(p.ux + (o >> 4));
-    s.w = p.wrow[row];
+    const int xb = T::NI == 2 ? (n0 >> 4) & 2 : 0;
+    s.gx = load4(gx, bytes >> 4, (row >> 4) - xb);
+    s.ux = load4(ux, bytes >> 4, (row >> 4) - xb);
+    s.w = __uint_as_float(load4(reinterpret_cast<const char*>(p.wrow + t.row0), t.rows * 4, m * 4));
+  }
+  __device__ __forceinline__ void turn(Saved& s, int n0) const {
+    if constexpr (T::NI == 4) {
+      transpose4(s.g);
+      transpose4(s.u);
+    } else {
+      const int xb = (n0 >> 4) & 2;
+      s.gx >>= 8 * xb;
+      s.ux >>= 8 * xb;
+    }
   }
   __device__ __forceinline__ bool store(const Info& t, int wave, int lane, f32x4_t (&acc)[T::MI][T::NI]) const {
     // a wavefront's columns are all inside the matrix or all behind it (both
     // are multiples of 64, or of 32 with tiles of 128 columns)
     const int n0 = t.nbase + (wave % T::WN) * T::TN;
+    const bool in = n0 < p.N;
+    const int m0 = T::m_first(wave);
     if constexpr (!DH) {
-      if (n0 >= p.N) return false;
+      if (!in) return false;
+      const int ld = p.N * EB;
+      const OutTile<Tr> out =
+          OutTile<Tr>::matrix(static_cast<const char*>(p.out) + (size_t)t.row0 * ld, t.rows, ld, m0, n0, lane, 0);
 #pragma unroll
       for (int mi = 0; mi < T::MI; ++mi) {
-        const int m = T::m_of(wave, mi, lane);
-        char* row = static_cast<char*>(p.out) + (((size_t)t.row0 + m) * p.N + n0) * EB;
         float v[T::NI][4];
 #pragma unroll
         for (int ni = 0; ni < T::NI; ++ni)
 #pragma unroll
           for (int r = 0; r < 4; ++r) v[ni][r] = acc[mi][ni][r];
-        store_blocks<Tr, T::NI>(v, m < t.rows, lane, [&](int n) { return row + n * EB; });
+        out.template put<T::NI>(mi * T::M_STEP, v);
       }
-      return t.rows == T::BM;
+      return true;
     } else {
-      const bool in = n0 < p.N;
-      // the next block's codes are on their way while this one's are worked
-      Saved s[2];
-      if (in) read_saved(t, 0, n0, wave, lane, s[0]);
+      const size_t o = (size_t)(n0 / T::KS) * p.panel + (size_t)t.row0 * 64;
+      const OutTile<Tr> odg = OutTile<Tr>::panels(static_cast<const char*>(p.dg) + o, p.panel, t.rows, m0, lane);
+      const OutTile<Tr> odu = OutTile<Tr>::panels(static_cast<const char*>(p.du) + o, p.panel, t.rows, m0, lane);
+      const OutTile<Tr> ohw = OutTile<Tr>::panels(static_cast<const char*>(p.hw) + o, p.panel,
+                                                  p.hw != nullptr ? t.rows : 0, m0, lane);
+      // the codes of the next AHEAD blocks are on their way while one's are worked
+      constexpr int AHEAD = T::MI < 3 ? T::MI - 1 : 2;
+      Saved s[AHEAD + 1];
+      if (in) {
+#pragma unroll
+        for (int mi = 0; mi < AHEAD; ++mi) read_saved(t, T::m_of(wave, mi, lane), n0, lane, s[mi]);
+      }
 #pragma unroll
       for (int mi = 0; mi < T::MI; ++mi) {
         const int m = T::m_of(wave, mi, lane);
-        const bool live = m < t.rows;
-        const size_t row = (size_t)t.row0 + (live ? m : 0);
         float dot = 0.f;
         if (in) {
-          if (mi + 1 < T::MI) read_saved(t, mi + 1, n0, wave, lane, s[(mi + 1) & 1]);
-          const Saved& q = s[mi & 1];
+          if (mi + AHEAD < T::MI)
+            read_saved(t, T::m_of(wave, mi + AHEAD, lane), n0, lane, s[(mi + AHEAD) % (AHEAD + 1)]);
+          Saved& q = s[mi % (AHEAD + 1)];
+          turn(q, n0);
           float dg[T::NI][4], du[T::NI][4], hw[T::NI][4];
 #pragma unroll
           for (int ni = 0; ni < T::NI; ++ni) {
@@ -636,18 +806,15 @@ struct DgradJob {
               hw[ni][r] = q.w * h;
             }
           }
-          const size_t o = (row * p.N + n0) * EB;
-          store_blocks<Tr, T::NI>(dg, live, lane, [&](int n) { return static_cast<char*>(p.dg) + o + n * EB; });
-          store_blocks<Tr, T::NI>(du, live, lane, [&](int n) { return static_cast<char*>(p.du) + o + n * EB; });
-          if (p.hw != nullptr)
-            store_blocks<Tr, T::NI>(hw, live, lane, [&](int n) { return static_cast<char*>(p.hw) + o + n * EB; });
+          odg.template put<T::NI>(mi * T::M_STEP, dg);
+          odu.template put<T::NI>(mi * T::M_STEP, du);
+          ohw.template put<T::NI>(mi * T::M_STEP, hw);
         }
         // the wavefront's columns of <D, h>: the four lanes of a row, then one
         // partial sum per wavefront column, added in order by a later step
         dot += __shfl_xor(dot, 16);
         dot += __shfl_xor(dot, 32);
-        if (live && lane < 16)
-          p.dot[row * (size_t)p.dot_ld + (t.nbase / T::BN) * T::WN + wave % T::WN] = dot;
+        if (in && m < t.rows && lane < 16) p.dot[((size_t)t.row0 + m) * p.dot_ld + n0 / T::TN] = dot;
         __builtin_amdgcn_sched_barrier(0);  // one block's values at a time, or the registers overflow
       }
       return false;
@@ -679,8 +846,10 @@ template <class Tr, class T>
 struct WgradJob {
   static constexpr int EB = T::EB;
   struct Info {
-    int steps, rows, steps0, e, w, mbase, nbase, ldm, ldn;
+    int steps, rows, steps0, e, w, mbase, nbase;
     int n0, n1;
+    size_t panel;
+    int mpanels, npanels;           // panels of either operand from the tile's first on
     const char *p0, *q0, *p1, *q1;  // the operands' first rows of either run
   };
   const WgradArgs& p;
@@ -708,69 +877,50 @@ struct WgradJob {
     i.n0 = __builtin_amdgcn_readfirstlane(tab.rows[i.e].n0);
     const int r1 = __builtin_amdgcn_readfirstlane(tab.rows[i.e].r1);
     i.n1 = __builtin_amdgcn_readfirstlane(tab.rows[i.e].n1);
-    i.ldm = p.M[i.w] * EB;
-    i.ldn = p.N[i.w] * EB;
-    i.p0 = static_cast<const char*>(p.P[i.w]) + (size_t)r0 * i.ldm;
-    i.q0 = static_cast<const char*>(p.Q[i.w]) + (size_t)r0 * i.ldn;
-    i.p1 = static_cast<const char*>(p.P[i.w]) + (size_t)r1 * i.ldm;
-    i.q1 = static_cast<const char*>(p.Q[i.w]) + (size_t)r1 * i.ldn;
+    i.panel = p.panel;
+    i.mpanels = (p.M[i.w] - i.mbase) / T::KS;  // (M and N are multiples of 64)
+    i.npanels = (p.N[i.w] - i.nbase) / T::KS;
+    const char* P = static_cast<const char*>(p.P[i.w]) + (size_t)(i.mbase / T::KS) * p.panel;
+    const char* Q = static_cast<const char*>(p.Q[i.w]) + (size_t)(i.nbase / T::KS) * p.panel;
+    i.p0 = P + (size_t)r0 * 64;
+    i.q0 = Q + (size_t)r0 * 64;
+    i.p1 = P + (size_t)r1 * 64;
+    i.q1 = Q + (size_t)r1 * 64;
     i.steps0 = (i.n0 + T::KS - 1) / T::KS;
     i.steps = i.steps0 + (i.n1 + T::KS - 1) / T::KS;
     return i;
   }
-  __device__ __forceinline__ void offsets(const Info& t, int wave, int lane, int (&moff)[T::LM],
-                                          int (&noff)[T::LN]) const {
-    const int M = p.M[t.w], N = p.N[t.w];
-#pragma unroll
-    for (int i = 0; i < T::LM; ++i)
-      moff[i] = T::template strided_offset<T::BM>(T::mq(wave, i), lane, t.mbase, M, t.ldm, 0);
-#pragma unroll
-    for (int i = 0; i < T::LN; ++i)
-      noff[i] = T::template strided_offset<T::BN>(T::nq(wave, i), lane, t.nbase, N, t.ldn, 0);
-  }
   __device__ __forceinline__ Step first(const Info& t) const {
-    Step s{t.n0 > 0 ? t.p0 : t.p1, t.n0 > 0 ? t.q0 : t.q1, 0, 0};
-    const int left = t.steps > 0 ? min(T::KS, t.n0 > 0 ? t.n0 : t.n1) : 0;
-    s.mbytes = left * t.ldm;
-    s.nbytes = left * t.ldn;
-    return s;
+    const int left = t.steps > 0 ? min(T::KS, t.n0 > 0 ? t.n0 : t.n1) * 64 : 0;
+    return Step{t.n0 > 0 ? t.p0 : t.p1, t.n0 > 0 ? t.q0 : t.q1, left, left};
   }
   // Step j: KS rows on; the rows behind the capacity follow those in front of it.
   __device__ __forceinline__ void next(const Info& t, int j, Step& s) const {
-    s.m += (size_t)(T::KS * t.ldm);
-    s.n += (size_t)(T::KS * t.ldn);
     const bool second = j >= t.steps0;
-    if (j == t.steps0) {
-      s.m = t.p1;
-      s.n = t.q1;
-    }
+    s.m = j == t.steps0 ? t.p1 : s.m + T::KS * 64;
+    s.n = j == t.steps0 ? t.q1 : s.n + T::KS * 64;
     const int left = max(0, min(T::KS, second ? t.n1 - (j - t.steps0) * T::KS : t.n0 - j * T::KS));
-    const int rows = j < t.steps ? left : 0;
-    s.mbytes = rows * t.ldm;
-    s.nbytes = rows * t.ldn;
+    s.mbytes = s.nbytes = j < t.steps ? left * 64 : 0;
   }
   __device__ __forceinline__ bool store(const Info& t, int wave, int lane, f32x4_t (&acc)[T::MI][T::NI]) const {
     const int M = p.M[t.w], N = p.N[t.w];
     const int n0 = t.nbase + (wave % T::WN) * T::TN;  // as in DgradJob: all in or all out
     if (n0 >= N) return false;
-    char* out = static_cast<char*>(p.out[t.w]) + (size_t)t.e * M * N * EB;
-    const int m0 = T::m_of(wave, 0, 0);
+    // M is a multiple of 64, so whole groups of 16 rows are in or out
+    const int ld = N * EB;
+    const OutTile<Tr> out =
+        OutTile<Tr>::matrix(static_cast<const char*>(p.out[t.w]) + ((size_t)t.e * M + t.mbase) * ld, M - t.mbase, ld,
+                            T::m_first(wave), n0, lane, p.blocked16);
 #pragma unroll
     for (int mi = 0; mi < T::MI; ++mi) {
-      const int m = t.mbase + T::m_of(wave, mi, lane);
       float v[T::NI][4];
 #pragma unroll
       for (int ni = 0; ni < T::NI; ++ni)
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[ni][r] = acc[mi][ni][r];
-      // the weight's storage order: rows, or 64-byte pieces of 16 rows in turn
-      char* row = out + (p.blocked16 ? ((size_t)(m >> 4) * 16 * N + (m & 15) * T::KS) * EB : (size_t)m * N * EB);
-      store_blocks<Tr, T::NI>(v, m < M, lane, [&](int n) {
-        const int c = n0 + n;
-        return row + (p.blocked16 ? (size_t)(c / T::KS) * (16 * T::KS) + c % T::KS : (size_t)c) * EB;
-      });
+      out.template put<T::NI>(mi * T::M_STEP, v);
     }
-    return t.mbase + m0 + T::TM <= M;
+    return true;
   }
 };
 
@@ -795,6 +945,8 @@ struct RouteJob {
   static constexpr int EB = T::EB;
   struct Info {
     int steps, rows;
+    size_t panel;
+    int mpanels, npanels;
   };
   const RouteWgradArgs& p;
   const int nbase, mbase, rows, j0, per;
@@ -802,14 +954,9 @@ struct RouteJob {
       : p(p_), nbase(blockIdx.x * T::BN), mbase(blockIdx.y * T::BM), rows(min(T::BM, p_.E - mbase)),
         j0(min((p_.T + T::KS - 1) / T::KS, (int)blockIdx.z * p_.steps)),
         per(min((p_.T + T::KS - 1) / T::KS - j0, p_.steps)) {}
-  __device__ __forceinline__ Info decode(int) const { return Info{per * (p.dz_lo != nullptr ? 2 : 1), rows}; }
-  __device__ __forceinline__ void offsets(const Info&, int wave, int lane, int (&moff)[T::LM],
-                                          int (&noff)[T::LN]) const {
-#pragma unroll
-    for (int i = 0; i < T::LM; ++i) moff[i] = T::rows_offset(T::mq(wave, i), lane, 64);
-#pragma unroll
-    for (int i = 0; i < T::LN; ++i)
-      noff[i] = T::template strided_offset<T::BN>(T::nq(wave, i), lane, nbase, p.d, p.d * EB, 0);
+  __device__ __forceinline__ Info decode(int) const { return Info{per * (p.dz_lo != nullptr ? 2 : 1), rows, 0, 0, 0}; }
+  __device__ __forceinline__ int rows_offset(const Info&, int q, int lane) const {
+    return T::rows_offset(q, lane, nbase, p.d, p.d * EB, 0);
   }
   __device__ __forceinline__ Step first(const Info& t) const {
     Step s{};

@@ -4,22 +4,25 @@
 namespace moe {
 namespace {
 using namespace grad;
-// data gradients, by row-tile height
-using D256 = Tile<TBF16, 256, 256, 2, 4, false, 4, 1, true>;
-using D128 = Tile<TBF16, 128, 256, 2, 4, false, 4, 1, true>;
-using D64 = Tile<TBF16, 64, 128, 1, 4, false, 4, 3, false>;
-using D32 = Tile<TBF16, 32, 128, 1, 4, false, 4, 3, false>;
+// data gradients, by rows and columns of a tile
+using D256 = Tile<TBF16, 256, 256, 2, 4, kPanelK, kRows, 4, 1, true>;
+using D256N = Tile<TBF16, 256, 128, 4, 2, kPanelK, kRows, 5, 1, true>;
+using D64 = Tile<TBF16, 64, 128, 1, 4, kPanelK, kRows, 4, 3, false>;
+using D32 = Tile<TBF16, 32, 128, 1, 4, kPanelK, kRows, 4, 3, false>;
 // weight gradients
-using W256 = Tile<TBF16, 256, 256, 2, 4, true, 4, 1, true>;
-using W128 = Tile<TBF16, 128, 128, 2, 2, true, 4, 2, false>;
+using W256 = Tile<TBF16, 256, 256, 2, 4, kPanelR, kPanelR, 4, 1, true>;
+using W128 = Tile<TBF16, 128, 128, 2, 2, kPanelR, kPanelR, 4, 2, false>;
 // router weight gradient: experts by columns
-using R64 = Tile<TBF16, 64, 128, 1, 4, false, 4, 3, false>;
+using R64 = Tile<TBF16, 64, 128, 1, 4, kPanelK, kRows, 4, 3, false>;
 
 template <bool DH>
 hipError_t dgrad_bm(int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
   switch (BM) {
-    case 256: return launch_dgrad_cfg<TBF16, D256, DH>(a, max_tiles, stream);
-    case 128: return launch_dgrad_cfg<TBF16, D128, DH>(a, max_tiles, stream);
+    case 256:
+      // narrow tiles where wide ones would not give every compute unit two
+      if (max_tiles * ((a.N + 255) / 256) < 2 * kComputeUnits)
+        return launch_dgrad_cfg<TBF16, D256N, DH>(a, max_tiles, stream);
+      return launch_dgrad_cfg<TBF16, D256, DH>(a, max_tiles, stream);
     case 64: return launch_dgrad_cfg<TBF16, D64, DH>(a, max_tiles, stream);
     case 32: return launch_dgrad_cfg<TBF16, D32, DH>(a, max_tiles, stream);
     default: return hipErrorInvalidValue;

@@ -5,8 +5,8 @@ namespace moe {
 namespace {
 using namespace grad;
 // fp32 MFMAs run at a sixteenth of the bf16 rate, so small tiles keep up
-using D64 = Tile<TF32, 64, 64, 2, 2, false, 4, 4, false>;
-using W64 = Tile<TF32, 64, 64, 2, 2, true, 4, 4, false>;
+using D64 = Tile<TF32, 64, 64, 2, 2, kPanelK, kRows, 4, 4, false>;
+using W64 = Tile<TF32, 64, 64, 2, 2, kPanelR, kPanelR, 4, 4, false>;
 }  // namespace
 
 hipError_t launch_dgrad_f32(bool dh, int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
@@ -28,15 +28,11 @@ hipError_t launch_route_wgrad_f32(const RouteWgradArgs& a, int ranges, hipStream
 
 int dgrad_tile_rows(int dtype, int mean) {
   if (dtype != 1) return 64;
-  return mean > 192 ? 256 : mean > 64 ? 128 : mean > 32 ? 64 : 32;
+  return mean > 64 ? 256 : mean > 32 ? 64 : 32;
 }
 
-int dgrad_dot_ld(int dtype, int mean, int F) {
-  // one partial sum per wavefront column: 64 columns (bf16 tiles of 128 and 256
-  // rows) or 32, rounded up to whole column tiles
-  if (dtype != 1) return (F + 63) / 64 * 2;
-  return dgrad_tile_rows(dtype, mean) >= 128 ? (F + 255) / 256 * 4 : (F + 127) / 128 * 4;
-}
+// one partial sum per wavefront column
+int dgrad_dot_cols(int dtype, int mean) { return dgrad_tile_rows(dtype, mean) == 256 ? 64 : 32; }
 
 hipError_t launch_dgrad(int dtype, bool dh, int mean, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
   const int BM = dgrad_tile_rows(dtype, mean);

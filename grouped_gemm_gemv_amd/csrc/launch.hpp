@@ -190,11 +190,12 @@ hipError_t launch_route_wgrad_f32(const RouteWgradArgs& a, int ranges, hipStream
 hipError_t launch_route_finish(int dtype, const float* part, int ranges, const int32_t* ids, const float* dz, int T,
                                int k, int E, int d, void* dw_router, float* dbias, hipStream_t stream);
 
-// Rows in expert order for the backward GEMMs: x_perm and dout_perm (bit
-// copies) and the routing weight of each row.
-hipError_t launch_gather_backward(const void* x, const void* dout, const float* topk_w, const int32_t* row_of, int Tk,
-                                  int k, int64_t row_bytes, void* x_perm, void* dout_perm, float* wrow,
-                                  hipStream_t stream);
+// x and dout in expert order for the backward GEMMs (bit copies), in panels
+// [row_bytes / 64][R][64 bytes], and the routing weight of each row.  Rows without
+// a token are left as they are.
+hipError_t launch_gather_backward(const void* x, const void* dout, const float* topk_w, const int32_t* token_of,
+                                  const int32_t* row_of, int64_t rows, int k, int64_t row_bytes, void* x_panels,
+                                  void* dout_panels, float* wrow, hipStream_t stream);
 // dw_f = sum of the row's partial sums in order; 0 for an entry without a row.
 hipError_t launch_dot_finish(const float* dot, int ld, const int32_t* row_of, int Tk, float* dw, hipStream_t stream);
 
@@ -213,19 +214,21 @@ struct GradRows {
 
 struct DgradArgs {
   GradRows rows;
-  const void* a0;  // [R][K]
+  // activations in panels ([columns of 64 bytes][R][64 bytes]; `panel` bytes each)
+  const void* a0;  // K columns
   const void* a1;  // second activation operand, or null
+  size_t panel;
   const void* b0;  // [E][K][N]
   const void* b1;
   int K, N, blocked16;
   void* out;  // [R][N]
-  // with the SwiGLU's gradient (out unused): a0 = dout rows, K = d, N = F
+  // with the SwiGLU's gradient (out unused): a0 = dout, K = d, N = F
   const float* wrow;
   const int8_t* g8;
   const int8_t* u8;
   const uint8_t* gx;
   const uint8_t* ux;
-  void* dg;
+  void* dg;    // panels
   void* du;
   void* hw;    // w_r h, or null
   float* dot;  // [R][dot_ld] partial sums of <D, h>
@@ -235,8 +238,9 @@ struct DgradArgs {
 struct WgradArgs {
   GradRows rows;
   int n;              // products
-  const void* P[3];   // [R][M]
-  const void* Q[3];   // [R][N]
+  const void* P[3];   // panels of M columns
+  const void* Q[3];   // panels of N columns
+  size_t panel;       // bytes of a panel
   void* out[3];       // [E][M][N]
   int M[3], N[3];
   int first[3];       // first unit of each product inside an expert (set by the launcher)
@@ -244,9 +248,9 @@ struct WgradArgs {
   int blocked16;
 };
 
-// Partial sums of <D, h> that dgrad writes for a row, and the row-tile bound
-// of its grid: both depend on the tile the mean row count selects.
-int dgrad_dot_ld(int dtype, int mean, int F);
+// Columns of one partial sum of <D, h>, and rows of a tile, of the data
+// gradients: both go by the mean row count of an expert.
+int dgrad_dot_cols(int dtype, int mean);
 int dgrad_tile_rows(int dtype, int mean);
 hipError_t launch_dgrad(int dtype, bool dh, int mean, const DgradArgs& a, long long max_tiles, hipStream_t stream);
 hipError_t launch_wgrad(int dtype, int mean, const WgradArgs& a, hipStream_t stream);

@@ -129,6 +129,15 @@ __device__ __forceinline__ void swap32(unsigned& a, unsigned& b) {
   b = r[1];
 #endif
 }
+// In each row of 16 lanes, lanes 8..15 of a trade places with lanes 0..7 of b.
+__device__ __forceinline__ void swap8(unsigned& a, unsigned& b) {
+#ifdef __HIP_DEVICE_COMPILE__
+  constexpr int kRor8 = 0x128;  // rotate within a row of 16 lanes by 8
+  const unsigned x = a;
+  a = (unsigned)__builtin_amdgcn_update_dpp((int)a, (int)b, kRor8, 0xf, 0xc, false);
+  b = (unsigned)__builtin_amdgcn_update_dpp((int)b, (int)x, kRor8, 0xf, 0x3, false);
+#endif
+}
 // Word w of lane group g (of 16 lanes) becomes word g of lane group w.
 __device__ __forceinline__ void transpose4(unsigned (&w)[4]) {
   swap32(w[0], w[2]);
@@ -139,13 +148,19 @@ __device__ __forceinline__ void transpose4(unsigned (&w)[4]) {
 
 // Stores and loads of a buffer of `bytes` bytes at `base`, which the compiler
 // counts itself: past the bound, stores are dropped and loads return zero.
-__device__ __forceinline__ void store16(const char* base, int bytes, int offset, const uint4& v) {
+__device__ __forceinline__ void buf_store16(const char* base, int bytes, int offset, const uint4& v) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass knows no descriptors
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, bytes, 0x00020000);
   __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), r, offset, 0, 0);
 #endif
 }
-__device__ __forceinline__ uint4 load16(const char* base, int bytes, int offset) {
+__device__ __forceinline__ void buf_store4(const char* base, int bytes, int offset, unsigned v) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, bytes, 0x00020000);
+  __builtin_amdgcn_raw_buffer_store_b32(v, r, offset, 0, 0);
+#endif
+}
+__device__ __forceinline__ uint4 buf_load16(const char* base, int bytes, int offset) {
 #ifdef __HIP_DEVICE_COMPILE__
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, bytes, 0x00020000);
   return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
@@ -153,7 +168,7 @@ __device__ __forceinline__ uint4 load16(const char* base, int bytes, int offset)
   return uint4{};
 #endif
 }
-__device__ __forceinline__ unsigned load4(const char* base, int bytes, int offset) {
+__device__ __forceinline__ unsigned buf_load4(const char* base, int bytes, int offset) {
 #ifdef __HIP_DEVICE_COMPILE__
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, bytes, 0x00020000);
   return __builtin_amdgcn_raw_buffer_load_b32(r, offset, 0, 0);
@@ -164,51 +179,73 @@ __device__ __forceinline__ unsigned load4(const char* base, int bytes, int offse
 
 // Where a lane's 16 bytes of a wavefront's tile of an output matrix lie: the
 // rows of the matrix (ld bytes), 64-byte pieces of 16 rows in turn (the blocked
-// weight order), or panels.  A store takes 64 bytes of 16 rows: two blocks of
-// 16 columns (bf16) or one (fp32); rows past the bound are dropped.
+// weight order), or panels.  A piece is 64 bytes of columns of 16 rows: two
+// blocks of 16 columns (bf16) or one (fp32).  Rows past the bound are dropped.
 template <class Tr>
 struct OutTile {
   static constexpr int EB = sizeof(typename Tr::T);
   const char* base;  // of the tile's first row
   size_t piece;      // bytes to the next 64 bytes of columns
   int bytes, ld, lane0;
+  int half;          // rows of a matrix: bytes to the second half of a pair's rows, else 0
   // a lane's bytes in the 64: bf16, after the trade below, 16 of block g mod 2
   __device__ __forceinline__ static int lane_byte(int g) { return EB == 2 ? (g & 1) * 32 + (g >> 1) * 16 : g * 16; }
-  // a row-major or blocked matrix: m0, col0 the wavefront's first row and column
+  // a row-major or blocked matrix: m0, col0 the wavefront's first row and column,
+  // `pairs` whether its pieces pair up
   __device__ __forceinline__ static OutTile matrix(const char* base, int rows, int ld, int m0, int col0, int lane,
-                                                   int blocked16) {
+                                                   int blocked16, bool pairs) {
     const int g = lane >> 4, i = lane & 15;
+    const int r = blocked16 ? i * 64 : pairs ? (i & 7) * ld + (i >> 3) * 64 : i * ld;
     return OutTile{base + (size_t)(blocked16 ? col0 * EB * 16 : col0 * EB), (size_t)(blocked16 ? 1024 : 64),
-                   rows > 0 ? rows * ld - (blocked16 ? 0 : col0 * EB) : 0, ld,
-                   m0 * ld + i * (blocked16 ? 64 : ld) + lane_byte(g)};
+                   rows > 0 ? rows * ld - (blocked16 ? 0 : col0 * EB) : 0, ld, m0 * ld + r + lane_byte(g),
+                   !blocked16 && pairs ? 8 * ld : 0};
   }
   // panels: base of the tile's first row in the panel of the wavefront's first columns
   __device__ __forceinline__ static OutTile panels(const char* base, size_t panel, int rows, int m0, int lane) {
-    return OutTile{base, panel, rows * 64, 64, (m0 + (lane & 15)) * 64 + lane_byte(lane >> 4)};
+    return OutTile{base, panel, rows * 64, 64, (m0 + (lane & 15)) * 64 + lane_byte(lane >> 4), 0};
   }
   // Rows m .. m + 15 (m a multiple of 16, from m0 on), NI blocks of 16 columns of
   // which lane group g = lane / 16 holds columns 4g .. 4g + 3.  bf16: lanes 16
-  // apart trade halves, so that each stores 16 bytes.
+  // apart trade halves, so that each stores 16 bytes.  In blocks and panels a
+  // piece is one run of 1 KB.  In rows it is half a cache line of each of 16 rows;
+  // two pieces trade rows, so that a store takes whole lines of 8 rows (a store
+  // costs a compute unit about 4 cycles a line it touches, whole or not).
   template <int NI>
   __device__ __forceinline__ void put(int m, const float (&v)[NI][4]) const {
-    const int at = lane0 + m * ld;
+    constexpr int PC = NI * EB / 4;
+    unsigned w[PC][4];
     if constexpr (EB == 2) {
       static_assert(NI % 2 == 0, "blocks pair up");
 #pragma unroll
-      for (int ni = 0; ni < NI; ni += 2) {
-        unsigned a0 = pack2(v[ni][0], v[ni][1]), a1 = pack2(v[ni][2], v[ni][3]);
-        unsigned b0 = pack2(v[ni + 1][0], v[ni + 1][1]), b1 = pack2(v[ni + 1][2], v[ni + 1][3]);
-        swap16(a0, b0);
-        swap16(a1, b1);
-        // lane groups 0, 2: columns 0-7, 8-15 of block ni; groups 1, 3: of block ni + 1
-        store16(base + (ni >> 1) * piece, bytes, at, make_uint4(a0, a1, b0, b1));
+      for (int q = 0; q < PC; ++q) {
+        const float(&a)[4] = v[2 * q];
+        const float(&b)[4] = v[2 * q + 1];
+        w[q][0] = pack2(a[0], a[1]), w[q][1] = pack2(a[2], a[3]);
+        w[q][2] = pack2(b[0], b[1]), w[q][3] = pack2(b[2], b[3]);
+        // lane groups 0, 2: columns 0-7, 8-15 of block 2q; groups 1, 3: of block 2q + 1
+        swap16(w[q][0], w[q][2]);
+        swap16(w[q][1], w[q][3]);
       }
     } else {
 #pragma unroll
-      for (int ni = 0; ni < NI; ++ni)
-        store16(base + ni * piece, bytes, at,
-                make_uint4(__float_as_uint(v[ni][0]), __float_as_uint(v[ni][1]), __float_as_uint(v[ni][2]),
-                           __float_as_uint(v[ni][3])));
+      for (int q = 0; q < PC; ++q)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w[q][r] = __float_as_uint(v[q][r]);
+    }
+    const int at = lane0 + m * ld;
+    if (PC % 2 == 0 && half != 0) {
+#pragma unroll
+      for (int q = 0; q + 1 < PC; q += 2) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) swap8(w[q][r], w[q + 1][r]);
+        buf_store16(base + q * piece, bytes - q * 64, at, make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]));
+        buf_store16(base + q * piece, bytes - q * 64, at + half,
+                make_uint4(w[q + 1][0], w[q + 1][1], w[q + 1][2], w[q + 1][3]));
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < PC; ++q)
+        buf_store16(base + q * piece, bytes, at, make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]));
     }
   }
 };
@@ -519,7 +556,8 @@ struct Tile {
       }
     }
 
-    // The steps of a unit, for its first MB blocks of 16 rows per wavefront.
+    // The steps of a unit, for its first MB blocks of 16 rows per wavefront, and
+    // the empty ones behind them, which keep the ring going and nothing else.
     template <int MB>
     __device__ __forceinline__ void steps(int n) {
 #pragma unroll 1
@@ -528,6 +566,24 @@ struct Tile {
           step_pp<MB>();
         else
           step<MB>();
+      }
+    }
+    __device__ __forceinline__ void empty_steps(int n) {
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        if constexpr (!PP) {
+          wait_step();
+          barrier();
+        }
+        feed([](int) {});
+        if constexpr (PP) {
+          wait_step();
+          barrier();
+        }
+        cs = cs == S - 1 ? 0 : cs + 1;
+        advance();
+        turn();
+        if constexpr (PP) barrier();
       }
     }
 
@@ -562,9 +618,10 @@ struct Tile {
           for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         // a tile of at most half the rows multiplies half the blocks
         if (!MKS && MI % 2 == 0 && ct.rows <= BM / 2)
-          steps<(MI + 1) / 2>(padded(ct));
+          steps<(MI + 1) / 2>(ct.steps);
         else
-          steps<MI>(padded(ct));
+          steps<MI>(ct.steps);
+        empty_steps(padded(ct) - ct.steps);
         // both halves store at the same time: in turn, each would wait for the
         // other's stores (4000 of a tile's 62000 cycles)
         if (PP && !second) barrier();
@@ -719,22 +776,22 @@ struct DgradJob {
     const char *gx = reinterpret_cast<const char*>(p.gx) + (o >> 4), *ux = reinterpret_cast<const char*>(p.ux) + (o >> 4);
     const int row = m * p.N + n0, bytes = t.rows * p.N, g = lane >> 4;
     if constexpr (T::NI == 4) {
-      const uint4 a = load16(g8, bytes, row + g * 16), b = load16(u8, bytes, row + g * 16);
+      const uint4 a = buf_load16(g8, bytes, row + g * 16), b = buf_load16(u8, bytes, row + g * 16);
       s.g[0] = a.x, s.g[1] = a.y, s.g[2] = a.z, s.g[3] = a.w;
       s.u[0] = b.x, s.u[1] = b.y, s.u[2] = b.z, s.u[3] = b.w;
     } else {
 #pragma unroll
       for (int ni = 0; ni < T::NI; ++ni) {
-        s.g[ni] = load4(g8, bytes, row + ni * 16 + g * 4);
-        s.u[ni] = load4(u8, bytes, row + ni * 16 + g * 4);
+        s.g[ni] = buf_load4(g8, bytes, row + ni * 16 + g * 4);
+        s.u[ni] = buf_load4(u8, bytes, row + ni * 16 + g * 4);
       }
     }
     // exponents of four blocks, of which two are this wavefront's with NI = 2
     static_assert(T::NI == 4 || T::NI == 2, "exponents of a wavefront's columns in one load");
     const int xb = T::NI == 2 ? (n0 >> 4) & 2 : 0;
-    s.gx = load4(gx, bytes >> 4, (row >> 4) - xb);
-    s.ux = load4(ux, bytes >> 4, (row >> 4) - xb);
-    s.w = __uint_as_float(load4(reinterpret_cast<const char*>(p.wrow + t.row0), t.rows * 4, m * 4));
+    s.gx = buf_load4(gx, bytes >> 4, (row >> 4) - xb);
+    s.ux = buf_load4(ux, bytes >> 4, (row >> 4) - xb);
+    s.w = __uint_as_float(buf_load4(reinterpret_cast<const char*>(p.wrow + t.row0), t.rows * 4, m * 4));
   }
   __device__ __forceinline__ void turn(Saved& s, int n0) const {
     if constexpr (T::NI == 4) {
@@ -750,13 +807,13 @@ struct DgradJob {
     // a wavefront's columns are all inside the matrix or all behind it (both
     // are multiples of 64, or of 32 with tiles of 128 columns)
     const int n0 = t.nbase + (wave % T::WN) * T::TN;
-    const bool in = n0 < p.N;
+    if (n0 >= p.N) return false;
     const int m0 = T::m_first(wave);
     if constexpr (!DH) {
-      if (!in) return false;
       const int ld = p.N * EB;
       const OutTile<Tr> out =
-          OutTile<Tr>::matrix(static_cast<const char*>(p.out) + (size_t)t.row0 * ld, t.rows, ld, m0, n0, lane, 0);
+          OutTile<Tr>::matrix(static_cast<const char*>(p.out) + (size_t)t.row0 * ld, t.rows, ld, m0, n0, lane, 0,
+                              T::TN * EB >= 128);
 #pragma unroll
       for (int mi = 0; mi < T::MI; ++mi) {
         float v[T::NI][4];
@@ -773,48 +830,48 @@ struct DgradJob {
       const OutTile<Tr> odu = OutTile<Tr>::panels(static_cast<const char*>(p.du) + o, p.panel, t.rows, m0, lane);
       const OutTile<Tr> ohw = OutTile<Tr>::panels(static_cast<const char*>(p.hw) + o, p.panel,
                                                   p.hw != nullptr ? t.rows : 0, m0, lane);
-      // the codes of the next AHEAD blocks are on their way while one's are worked
+      // The codes of the next AHEAD blocks are on their way while one's are
+      // worked.  No branch from here on: the compiler's waits count the loads and
+      // stores in flight, and where a branch left it in doubt it waited for the
+      // stores of the block before (1.7 ms instead of 0.9 in all).
       constexpr int AHEAD = T::MI < 3 ? T::MI - 1 : 2;
       Saved s[AHEAD + 1];
-      if (in) {
 #pragma unroll
-        for (int mi = 0; mi < AHEAD; ++mi) read_saved(t, T::m_of(wave, mi, lane), n0, lane, s[mi]);
-      }
+      for (int mi = 0; mi < AHEAD; ++mi) read_saved(t, T::m_of(wave, mi, lane), n0, lane, s[mi]);
+      char* dots = reinterpret_cast<char*>(p.dot + (size_t)t.row0 * p.dot_ld);
+      const int dots_bytes = t.rows * p.dot_ld * 4;
 #pragma unroll
       for (int mi = 0; mi < T::MI; ++mi) {
         const int m = T::m_of(wave, mi, lane);
-        float dot = 0.f;
-        if (in) {
-          if (mi + AHEAD < T::MI)
-            read_saved(t, T::m_of(wave, mi + AHEAD, lane), n0, lane, s[(mi + AHEAD) % (AHEAD + 1)]);
-          Saved& q = s[mi % (AHEAD + 1)];
-          turn(q, n0);
-          float dg[T::NI][4], du[T::NI][4], hw[T::NI][4];
+        if (mi + AHEAD < T::MI)
+          read_saved(t, T::m_of(wave, mi + AHEAD, lane), n0, lane, s[(mi + AHEAD) % (AHEAD + 1)]);
+        Saved& q = s[mi % (AHEAD + 1)];
+        turn(q, n0);
+        float dg[T::NI][4], du[T::NI][4], hw[T::NI][4], dot = 0.f;
 #pragma unroll
-          for (int ni = 0; ni < T::NI; ++ni) {
-            const float gs = exp_scale((q.gx >> (8 * ni)) & 255u), us = exp_scale((q.ux >> (8 * ni)) & 255u);
+        for (int ni = 0; ni < T::NI; ++ni) {
+          const float gs = exp_scale((q.gx >> (8 * ni)) & 255u), us = exp_scale((q.ux >> (8 * ni)) & 255u);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float D = acc[mi][ni][r];
-              const float g = code_of(q.g[ni], r) * gs, u = code_of(q.u[ni], r) * us;
-              const float sg = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
-              const float a = g * sg, h = a * u;
-              dot = fmaf(D, h, dot);
-              const float dh = q.w * D;
-              du[ni][r] = dh * a;
-              dg[ni][r] = dh * (u * sg * fmaf(g, 1.0f - sg, 1.0f));
-              hw[ni][r] = q.w * h;
-            }
+          for (int r = 0; r < 4; ++r) {
+            const float D = acc[mi][ni][r];
+            const float g = code_of(q.g[ni], r) * gs, u = code_of(q.u[ni], r) * us;
+            const float sg = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+            const float a = g * sg, h = a * u;
+            dot = fmaf(D, h, dot);
+            const float dh = q.w * D;
+            du[ni][r] = dh * a;
+            dg[ni][r] = dh * (u * sg * fmaf(g, 1.0f - sg, 1.0f));
+            hw[ni][r] = q.w * h;
           }
-          odg.template put<T::NI>(mi * T::M_STEP, dg);
-          odu.template put<T::NI>(mi * T::M_STEP, du);
-          ohw.template put<T::NI>(mi * T::M_STEP, hw);
         }
+        odg.template put<T::NI>(mi * T::M_STEP, dg);
+        odu.template put<T::NI>(mi * T::M_STEP, du);
+        ohw.template put<T::NI>(mi * T::M_STEP, hw);
         // the wavefront's columns of <D, h>: the four lanes of a row, then one
         // partial sum per wavefront column, added in order by a later step
         dot += __shfl_xor(dot, 16);
         dot += __shfl_xor(dot, 32);
-        if (in && m < t.rows && lane < 16) p.dot[((size_t)t.row0 + m) * p.dot_ld + n0 / T::TN] = dot;
+        buf_store4(dots, dots_bytes, lane < 16 ? (m * p.dot_ld + n0 / T::TN) * 4 : kOutside, __float_as_uint(dot));
         __builtin_amdgcn_sched_barrier(0);  // one block's values at a time, or the registers overflow
       }
       return false;
@@ -910,7 +967,7 @@ struct WgradJob {
     const int ld = N * EB;
     const OutTile<Tr> out =
         OutTile<Tr>::matrix(static_cast<const char*>(p.out[t.w]) + ((size_t)t.e * M + t.mbase) * ld, M - t.mbase, ld,
-                            T::m_first(wave), n0, lane, p.blocked16);
+                            T::m_first(wave), n0, lane, p.blocked16, T::TN * EB >= 128);
 #pragma unroll
     for (int mi = 0; mi < T::MI; ++mi) {
       float v[T::NI][4];

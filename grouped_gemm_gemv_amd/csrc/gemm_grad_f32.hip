@@ -40,7 +40,7 @@ hipError_t launch_dgrad(int dtype, bool dh, int mean, const DgradArgs& a, long l
 }
 
 hipError_t launch_wgrad(int dtype, int mean, const WgradArgs& a, hipStream_t stream) {
-  return dtype == 1 ? launch_wgrad_bf16(mean > 192 ? 256 : 128, a, stream) : launch_wgrad_f32(64, a, stream);
+  return dtype == 1 ? launch_wgrad_bf16(mean > 16 ? 256 : 128, a, stream) : launch_wgrad_f32(64, a, stream);
 }
 
 }  // namespace moe

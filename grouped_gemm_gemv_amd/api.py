@@ -90,7 +90,7 @@ class Dispatch:
 
     def arrays(self) -> dict:
         s, E, Tk = self.shape, self.shape.E, self.shape.T * self.shape.k
-        R = query(s).rows
+        R = _rows(s)
         mt = self.c.max_tiles
         return {
             "counts": self._view("counts", E),
@@ -255,11 +255,28 @@ def _in(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype, 
     """Device address of a tensor that must have this shape and type, contiguous on `device`; None stays None."""
     if t is None:
         return None
-    if tuple(t.shape) != shape or t.dtype != dtype:
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {list(shape)} of {dtype}, got {list(t.shape)} of {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return _p(t)
+    return _p(t)  # says what else is wrong
+
+
+def _c(s: Shape):
+    """The C struct of a shape, by reference; made once for each Shape, which is immutable."""
+    ref = s.__dict__.get("_cref")
+    if ref is None:
+        ref = ctypes.byref(s.c())
+        object.__setattr__(s, "_cref", ref)
+    return ref
+
+
+def _rows(s: Shape) -> int:
+    """R: rows of the dispatch's row space (moe_sizes_t.rows)."""
+    Tk = s.T * s.k
+    return s.E * s.capacity + max(0, Tk - s.capacity) if s.capacity > 0 else Tk
 
 
 def _disp(disp: Dispatch, shape: Shape, device):
@@ -289,15 +306,20 @@ def _call(name: str, device, stream, *args):
     """One entry point on the tensors' device, on `stream` or that device's current stream."""
     if device.type != "cuda":
         raise ValueError("libmoe takes device tensors")
-    with torch.cuda.device(device):
-        s = stream if stream is not None else torch.cuda.current_stream(device)
-        check(name, getattr(lib(), name)(*args, s.cuda_stream))
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    fn = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, s.cuda_stream)
+    check(name, status)
 
 
 def backward_query(shape: Shape) -> MoeBackwardSizes:
     """Bytes of the 8-bit projections and of the backward calls' workspaces (moe_backward_query)."""
     out = MoeBackwardSizes()
-    check("moe_backward_query", lib().moe_backward_query(ctypes.byref(shape.c()), ctypes.byref(out)))
+    check("moe_backward_query", lib().moe_backward_query(_c(shape), ctypes.byref(out)))
     return out
 
 
@@ -315,11 +337,11 @@ class Saved8:
         self.buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
         base = (self.buf.data_ptr() + 255) // 256 * 256
         self.c = MoeSaved8()
-        check("moe_saved8_carve", lib().moe_saved8_carve(ctypes.byref(shape.c()), base, n, ctypes.byref(self.c)))
+        check("moe_saved8_carve", lib().moe_saved8_carve(_c(shape), base, n, ctypes.byref(self.c)))
 
     def arrays(self) -> dict:
         """gate, up [R, F] int8 codes; gate_exp, up_exp [R, F / 16] uint8 exponents."""
-        R, F = query(self.shape).rows, self.shape.F
+        R, F = _rows(self.shape), self.shape.F
 
         def view(ptr, cols, dtype):
             off = ptr - self.buf.data_ptr()
@@ -344,23 +366,23 @@ def moe_ffn_gate_up_save8(shape: Shape, x, w_gate, w_up, disp: Dispatch, pass_id
     """Gate+up over a pass (x [T, d] read through the dispatch) that also keeps both projections in 8 bits."""
     s, dev = shape, x.device
     wg, wu, _ = _weights(s, "w", w_gate, w_up, None, dev)
-    _call("moe_ffn_gate_up_save8", dev, stream, ctypes.byref(s.c()), _in(x, "x", (s.T, s.d), s.dtype, dev), wg, wu,
-          _disp(disp, s, dev), pass_idx, _in(h, "h", (query(s).rows, s.F), s.dtype, dev), _saved(saved, s, dev))
+    _call("moe_ffn_gate_up_save8", dev, stream, _c(s), _in(x, "x", (s.T, s.d), s.dtype, dev), wg, wu,
+          _disp(disp, s, dev), pass_idx, _in(h, "h", (_rows(s), s.F), s.dtype, dev), _saved(saved, s, dev))
 
 
 def moe_saved8_unpack(shape: Shape, saved: Saved8, disp: Dispatch, gate, up, stream=None):
     """The values the codes stand for, in bf16 (gate, up [R, F]); rows without a token are left as they are."""
     s, dev = shape, gate.device
-    R = query(s).rows
-    _call("moe_saved8_unpack", dev, stream, ctypes.byref(s.c()), _saved(saved, s, dev), _disp(disp, s, dev),
+    R = _rows(s)
+    _call("moe_saved8_unpack", dev, stream, _c(s), _saved(saved, s, dev), _disp(disp, s, dev),
           _in(gate, "gate", (R, s.F), torch.bfloat16, dev), _in(up, "up", (R, s.F), torch.bfloat16, dev))
 
 
 def moe_combine_backward(shape: Shape, dout, y_perm, topk_w, disp: Dispatch, dy_perm, dtopk_w, stream=None):
     """Gradient of moe_combine: dy_perm [R, d] and dtopk_w [T, k] (fp32)."""
     s, dev = shape, dout.device
-    R = query(s).rows
-    _call("moe_combine_backward", dev, stream, ctypes.byref(s.c()), _in(dout, "dout", (s.T, s.d), s.dtype, dev),
+    R = _rows(s)
+    _call("moe_combine_backward", dev, stream, _c(s), _in(dout, "dout", (s.T, s.d), s.dtype, dev),
           _in(y_perm, "y_perm", (R, s.d), s.dtype, dev), _in(topk_w, "topk_w", (s.T, s.k), torch.float32, dev),
           _disp(disp, s, dev), _in(dy_perm, "dy_perm", (R, s.d), s.dtype, dev),
           _in(dtopk_w, "dtopk_w", (s.T, s.k), torch.float32, dev))
@@ -369,8 +391,8 @@ def moe_combine_backward(shape: Shape, dout, y_perm, topk_w, disp: Dispatch, dy_
 def moe_permute_backward(shape: Shape, dx_perm, disp: Dispatch, dx, stream=None):
     """Gradient of moe_permute's gather: dx [T, d] from dx_perm [R, d]."""
     s, dev = shape, dx_perm.device
-    _call("moe_permute_backward", dev, stream, ctypes.byref(s.c()),
-          _in(dx_perm, "dx_perm", (query(s).rows, s.d), s.dtype, dev), _disp(disp, s, dev),
+    _call("moe_permute_backward", dev, stream, _c(s),
+          _in(dx_perm, "dx_perm", (_rows(s), s.d), s.dtype, dev), _disp(disp, s, dev),
           _in(dx, "dx", (s.T, s.d), s.dtype, dev))
 
 
@@ -378,7 +400,7 @@ def moe_route_backward(shape: Shape, x, w_router, topk_ids, topk_w, dtopk_w, dx,
     """Gradient of moe_route from the routing weights' gradient; dbias may be None."""
     s, dev = shape, x.device
     tk = (s.T, s.k)
-    _call("moe_route_backward", dev, stream, ctypes.byref(s.c()), _in(x, "x", (s.T, s.d), s.dtype, dev),
+    _call("moe_route_backward", dev, stream, _c(s), _in(x, "x", (s.T, s.d), s.dtype, dev),
           _in(w_router, "w_router", (s.E, s.d), s.dtype, dev), _in(topk_ids, "topk_ids", tk, torch.int32, dev),
           _in(topk_w, "topk_w", tk, torch.float32, dev), _in(dtopk_w, "dtopk_w", tk, torch.float32, dev),
           _in(dx, "dx", (s.T, s.d), s.dtype, dev), _in(dw_router, "dw_router", (s.E, s.d), s.dtype, dev),
@@ -391,10 +413,10 @@ def moe_grouped_ffn_backward(shape: Shape, x, dout, topk_w, w_gate, w_up, w_down
     dw_down may be None: not computed."""
     s, dev = shape, x.device
     tk = (s.T, s.k)
-    _call("moe_grouped_ffn_backward", dev, stream, ctypes.byref(s.c()), _in(x, "x", (s.T, s.d), s.dtype, dev),
+    _call("moe_grouped_ffn_backward", dev, stream, _c(s), _in(x, "x", (s.T, s.d), s.dtype, dev),
           _in(dout, "dout", (s.T, s.d), s.dtype, dev), _in(topk_w, "topk_w", tk, torch.float32, dev),
           *_weights(s, "w", w_gate, w_up, w_down, dev), _disp(disp, s, dev), _saved(saved, s, dev),
-          _in(dx_perm, "dx_perm", (query(s).rows, s.d), s.dtype, dev),
+          _in(dx_perm, "dx_perm", (_rows(s), s.d), s.dtype, dev),
           _in(dtopk_w, "dtopk_w", tk, torch.float32, dev), *_weights(s, "dw", dw_gate, dw_up, dw_down, dev),
           *_ws(ws, dev))
 
@@ -405,7 +427,7 @@ def moe_forward_save8(shape: Shape, x, w_router, bias, topk_ids, topk_w, w_gate,
     disp and saved receive what moe_backward needs."""
     s, dev = shape, x.device
     tk = (s.T, s.k)
-    _call("moe_forward_save8", dev, stream, ctypes.byref(s.c()), _in(x, "x", (s.T, s.d), s.dtype, dev),
+    _call("moe_forward_save8", dev, stream, _c(s), _in(x, "x", (s.T, s.d), s.dtype, dev),
           _in(w_router, "w_router", (s.E, s.d), s.dtype, dev), _in(bias, "bias", (s.E,), torch.float32, dev),
           _in(topk_ids, "topk_ids", tk, torch.int32, dev), _in(topk_w, "topk_w", tk, torch.float32, dev),
           *_weights(s, "w", w_gate, w_up, w_down, dev), _in(out, "out", (s.T, s.d), s.dtype, dev),
@@ -418,7 +440,7 @@ def moe_backward(shape: Shape, x, w_router, topk_ids, topk_w, w_gate, w_up, w_do
     dw_router and dbias are None too."""
     s, dev = shape, x.device
     tk = (s.T, s.k)
-    _call("moe_backward", dev, stream, ctypes.byref(s.c()), _in(x, "x", (s.T, s.d), s.dtype, dev),
+    _call("moe_backward", dev, stream, _c(s), _in(x, "x", (s.T, s.d), s.dtype, dev),
           _in(w_router, "w_router", (s.E, s.d), s.dtype, dev), _in(topk_ids, "topk_ids", tk, torch.int32, dev),
           _in(topk_w, "topk_w", tk, torch.float32, dev), *_weights(s, "w", w_gate, w_up, w_down, dev),
           _disp(disp, s, dev), _saved(saved, s, dev), _in(dout, "dout", (s.T, s.d), s.dtype, dev),

@@ -516,7 +516,7 @@ moe_status_t forward_impl(const moe_shape_t* s, const void* x, const void* w_rou
 struct BackPlan {
   size_t saved_bytes, saved_up, saved_gate_exp, saved_up_exp;
   int ranges, range_steps;  // token ranges of the router's weight gradient, K steps each
-  size_t dz, dense_hi, dense_lo, part, route_ws;
+  size_t dz, dense_hi, dense_lo, sums, part, route_ws;
   int mean, dot_ld;
   size_t x_perm, dout_perm, dg, du, hw, wrow, dot, ffn_ws;  // from the start of the experts' part
   size_t dx_perm, backward_ws;
@@ -547,6 +547,7 @@ BackPlan back_plan(const moe_shape_t& s) {
   b.dz = take(4 * Tk);
   b.dense_hi = take((size_t)steps * s.E * 64);
   b.dense_lo = s.dtype == MOE_BF16 ? take((size_t)steps * s.E * 64) : 0;
+  b.sums = take(4 * (size_t)steps * s.E);
   b.part = take(4 * (size_t)b.ranges * s.E * s.d);
   b.route_ws = o;
   b.mean = (int)mean_rows(s);
@@ -639,7 +640,7 @@ moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const
     add(ws + b.dg, ws + b.x_perm, dw_gate, s.F, s.d);
     add(ws + b.du, ws + b.x_perm, dw_up, s.F, s.d);
   }
-  if (g.n > 0 && moe::launch_wgrad(s.dtype, b.mean, g, st) != hipSuccess) return MOE_ERR_HIP;
+  if (g.n > 0 && moe::launch_wgrad(s.dtype, g, st) != hipSuccess) return MOE_ERR_HIP;
   return hip_status(moe::launch_dot_finish(a.dot, a.dot_ld, d.row_of, Tk, dtopk_w, st));
 }
 
@@ -650,7 +651,8 @@ moe_status_t enqueue_route_backward(const moe_shape_t& s, const BackPlan& b, con
                                     hipStream_t st) {
   float* dz = reinterpret_cast<float*>(ws + b.dz);
   char* lo = s.dtype == MOE_BF16 ? ws + b.dense_lo : nullptr;
-  if (moe::launch_route_dz(s.dtype, ids, w, dw, s.T, s.k, s.E, dz, ws + b.dense_hi, lo, st) != hipSuccess)
+  float* sums = reinterpret_cast<float*>(ws + b.sums);
+  if (moe::launch_route_dz(s.dtype, ids, w, dw, s.T, s.k, s.E, dz, ws + b.dense_hi, lo, sums, st) != hipSuccess)
     return MOE_ERR_HIP;
   moe::RouteWgradArgs a{};
   a.dz_hi = ws + b.dense_hi;
@@ -668,7 +670,7 @@ moe_status_t enqueue_route_backward(const moe_shape_t& s, const BackPlan& b, con
       hipSuccess)
     return MOE_ERR_HIP;
   return hip_status(
-      moe::launch_route_finish(s.dtype, a.part, b.ranges, ids, dz, s.T, s.k, s.E, s.d, dw_router, dbias, st));
+      moe::launch_route_finish(s.dtype, a.part, b.ranges, sums, s.T, s.E, s.d, dw_router, dbias, st));
 }
 
 }  // namespace

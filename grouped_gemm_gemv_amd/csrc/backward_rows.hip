@@ -154,12 +154,13 @@ __global__ __launch_bounds__(256) void token_backward_kernel(const char* __restr
 // The softmax's gradient over the chosen logits, dz_j = w_j (dw_j - sum_i w_i
 // dw_i), and its dense form for the router's weight gradient: workgroup b
 // holds the KS tokens of one K step, one thread each, and writes [E][KS]
-// (bf16: the rounded value, and the rounded rest).
+// (bf16: the rounded value, and the rounded rest) and each expert's sum over
+// the step, the first half of dbias.
 template <class Tr>
 __global__ __launch_bounds__(256) void route_dz_kernel(const int32_t* __restrict__ ids, const float* __restrict__ w,
                                                        const float* __restrict__ dw, int T, int k, int E,
                                                        float* __restrict__ dz, typename Tr::T* __restrict__ hi,
-                                                       typename Tr::T* __restrict__ lo) {
+                                                       typename Tr::T* __restrict__ lo, float* __restrict__ sums) {
   constexpr int KS = 64 / sizeof(typename Tr::T);
   extern __shared__ float dense[];  // [E][KS]
   for (int i = threadIdx.x; i < E * KS; i += 256) dense[i] = 0.f;
@@ -189,16 +190,21 @@ __global__ __launch_bounds__(256) void route_dz_kernel(const int32_t* __restrict
       hi[base + i] = v;
     }
   }
+  for (int e = threadIdx.x; e < E; e += 256) {
+    float v = 0.f;
+    for (int i = 0; i < KS; ++i) v += dense[e * KS + (i + e) % KS];  // (e + i: rows of equal length share banks)
+    sums[(size_t)blockIdx.x * E + e] = v;
+  }
 }
 
 // dw_router = the token ranges' partial sums in order, one rounding
-// (blocks 0 .. sum_blocks - 1); dbias_e = sum of dz over the entries of expert e
-// (the E blocks behind them).
+// (blocks 0 .. sum_blocks - 1); dbias_e = expert e's sums over the K steps (the E
+// blocks behind them: threads, lanes, then wavefronts in order).
 template <class Tr>
 __global__ __launch_bounds__(256) void route_finish_kernel(const float* __restrict__ part, int ranges, int sum_blocks,
-                                                           const int32_t* __restrict__ ids,
-                                                           const float* __restrict__ dz, int64_t Tk, int64_t Ed,
-                                                           char* __restrict__ dw_router, float* __restrict__ dbias) {
+                                                           const float* __restrict__ sums, int steps, int E,
+                                                           int64_t Ed, char* __restrict__ dw_router,
+                                                           float* __restrict__ dbias) {
   using Elt = typename Tr::T;
   if ((int)blockIdx.x < sum_blocks) {
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
@@ -217,15 +223,7 @@ __global__ __launch_bounds__(256) void route_finish_kernel(const float* __restri
   __shared__ float wave_part[4];
   const int e = blockIdx.x - sum_blocks;
   float s = 0.f;
-  for (int64_t f = threadIdx.x; f < Tk; f += 256 * 4) {
-    float v[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t q = f + 256 * u;
-      v[u] = q < Tk && ids[q] == e ? dz[q] : 0.f;
-    }
-    s += (v[0] + v[1]) + (v[2] + v[3]);
-  }
+  for (int i = threadIdx.x; i < steps; i += 256) s += sums[(size_t)i * E + e];
   s = wave_sum(s);
   if ((threadIdx.x & 63) == 0) wave_part[threadIdx.x >> 6] = s;
   __syncthreads();
@@ -354,30 +352,31 @@ hipError_t launch_token_backward(int dtype, const void* dx_perm, const int32_t* 
 }
 
 hipError_t launch_route_dz(int dtype, const int32_t* ids, const float* w, const float* dw, int T, int k, int E,
-                           float* dz, void* dense_hi, void* dense_lo, hipStream_t stream) {
+                           float* dz, void* dense_hi, void* dense_lo, float* sums, hipStream_t stream) {
   const int KS = dtype == 1 ? 32 : 16;
   const dim3 grid((unsigned)(((int64_t)T + KS - 1) / KS)), block(256);
   const size_t lds = (size_t)E * KS * sizeof(float);
   if (dtype == 1)
     hipLaunchKernelGGL(route_dz_kernel<TBF16>, grid, block, lds, stream, ids, w, dw, T, k, E, dz,
-                       static_cast<uint16_t*>(dense_hi), static_cast<uint16_t*>(dense_lo));
+                       static_cast<uint16_t*>(dense_hi), static_cast<uint16_t*>(dense_lo), sums);
   else
     hipLaunchKernelGGL(route_dz_kernel<TF32>, grid, block, lds, stream, ids, w, dw, T, k, E, dz,
-                       static_cast<float*>(dense_hi), static_cast<float*>(nullptr));
+                       static_cast<float*>(dense_hi), static_cast<float*>(nullptr), sums);
   return hipGetLastError();
 }
 
-hipError_t launch_route_finish(int dtype, const float* part, int ranges, const int32_t* ids, const float* dz, int T,
-                               int k, int E, int d, void* dw_router, float* dbias, hipStream_t stream) {
+hipError_t launch_route_finish(int dtype, const float* part, int ranges, const float* sums, int T, int E, int d,
+                               void* dw_router, float* dbias, hipStream_t stream) {
   const int64_t Ed = (int64_t)E * d;
   const int sum_blocks = (int)((Ed / 4 + 255) / 256);
+  const int KS = dtype == 1 ? 32 : 16, steps = (int)(((int64_t)T + KS - 1) / KS);
   const dim3 grid(sum_blocks + (dbias != nullptr ? E : 0)), block(256);
   if (dtype == 1)
-    hipLaunchKernelGGL(route_finish_kernel<TBF16>, grid, block, 0, stream, part, ranges, sum_blocks, ids, dz,
-                       (int64_t)T * k, Ed, static_cast<char*>(dw_router), dbias);
+    hipLaunchKernelGGL(route_finish_kernel<TBF16>, grid, block, 0, stream, part, ranges, sum_blocks, sums, steps, E,
+                       Ed, static_cast<char*>(dw_router), dbias);
   else
-    hipLaunchKernelGGL(route_finish_kernel<TF32>, grid, block, 0, stream, part, ranges, sum_blocks, ids, dz,
-                       (int64_t)T * k, Ed, static_cast<char*>(dw_router), dbias);
+    hipLaunchKernelGGL(route_finish_kernel<TF32>, grid, block, 0, stream, part, ranges, sum_blocks, sums, steps, E,
+                       Ed, static_cast<char*>(dw_router), dbias);
   return hipGetLastError();
 }
 

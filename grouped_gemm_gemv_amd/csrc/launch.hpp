@@ -170,9 +170,10 @@ hipError_t launch_token_backward(int dtype, const void* dx_perm, const int32_t* 
                                  hipStream_t stream);
 
 // dz_f = w_f (dw_f - sum_i w_i dw_i), and its dense form by K step for the
-// router's weight gradient (hi, and with bf16 lo: [ceil(T / KS)][E][KS]).
+// router's weight gradient (hi, and with bf16 lo: [ceil(T / KS)][E][KS]) with
+// its sums over each step's tokens ([ceil(T / KS)][E]).
 hipError_t launch_route_dz(int dtype, const int32_t* ids, const float* w, const float* dw, int T, int k, int E,
-                           float* dz, void* dense_hi, void* dense_lo, hipStream_t stream);
+                           float* dz, void* dense_hi, void* dense_lo, float* sums, hipStream_t stream);
 
 struct RouteWgradArgs {
   const void* dz_hi;  // [steps of all tokens][E][64 bytes]
@@ -186,9 +187,9 @@ struct RouteWgradArgs {
 constexpr int kRouteGradCols[2] = {64, 128};
 hipError_t launch_route_wgrad_bf16(const RouteWgradArgs& a, int ranges, hipStream_t stream);
 hipError_t launch_route_wgrad_f32(const RouteWgradArgs& a, int ranges, hipStream_t stream);
-// dw_router = sum of the ranges (fp32, in order, one rounding); dbias_e = sum of dz over the entries of e.
-hipError_t launch_route_finish(int dtype, const float* part, int ranges, const int32_t* ids, const float* dz, int T,
-                               int k, int E, int d, void* dw_router, float* dbias, hipStream_t stream);
+// dw_router = sum of the ranges (fp32, in order, one rounding); dbias (or null) = sum of the steps' sums.
+hipError_t launch_route_finish(int dtype, const float* part, int ranges, const float* sums, int T, int E, int d,
+                               void* dw_router, float* dbias, hipStream_t stream);
 
 // x and dout in expert order for the backward GEMMs (bit copies), in panels
 // [row_bytes / 64][R][64 bytes], and the routing weight of each row.  Rows without
@@ -253,10 +254,10 @@ struct WgradArgs {
 int dgrad_dot_cols(int dtype, int mean);
 int dgrad_tile_rows(int dtype, int mean);
 hipError_t launch_dgrad(int dtype, bool dh, int mean, const DgradArgs& a, long long max_tiles, hipStream_t stream);
-hipError_t launch_wgrad(int dtype, int mean, const WgradArgs& a, hipStream_t stream);
+hipError_t launch_wgrad(int dtype, const WgradArgs& a, hipStream_t stream);
 hipError_t launch_dgrad_bf16(bool dh, int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream);
 hipError_t launch_dgrad_f32(bool dh, int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream);
-hipError_t launch_wgrad_bf16(int BM, const WgradArgs& a, hipStream_t stream);
-hipError_t launch_wgrad_f32(int BM, const WgradArgs& a, hipStream_t stream);
+hipError_t launch_wgrad_bf16(const WgradArgs& a, hipStream_t stream);
+hipError_t launch_wgrad_f32(const WgradArgs& a, hipStream_t stream);
 
 }  // namespace moe

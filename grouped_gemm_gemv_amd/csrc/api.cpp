@@ -628,12 +628,12 @@ moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const
   g.blocked16 = a.blocked16;
   g.panel = a.panel;
   auto add = [&](const void* P, const void* Q, void* out, int M, int N) {
-    g.P[g.n] = P;
-    g.Q[g.n] = Q;
-    g.out[g.n] = out;
-    g.M[g.n] = M;
-    g.N[g.n] = N;
-    ++g.n;
+    moe::WgradProduct& w = g.prod[g.n++];
+    w.P = P;
+    w.Q = Q;
+    w.out = out;
+    w.M = M;
+    w.N = N;
   };
   if (dw_down != nullptr) add(ws + b.dout_perm, ws + b.hw, dw_down, s.d, s.F);
   if (dw_gate != nullptr) {

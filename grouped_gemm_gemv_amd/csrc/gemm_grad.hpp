@@ -147,11 +147,16 @@ __device__ __forceinline__ void transpose4(unsigned (&w)[4]) {
 }
 
 // Stores and loads of a buffer of `bytes` bytes at `base`, which the compiler
-// counts itself: past the bound, stores are dropped and loads return zero.
+// counts itself: past the bound, stores are dropped and loads return zero.  The
+// 16-byte stores are the GEMMs' results, streamed past the caches (nt): kept
+// there, the gradients of the weights were still being written back while the
+// next kernel read (the first data gradient of the next call took 243 instead of
+// 181 us with 16 rows at the Mixtral shape, the weight gradients the same time).
+constexpr int kNonTemporal = 2;
 __device__ __forceinline__ void buf_store16(const char* base, int bytes, int offset, const uint4& v) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass knows no descriptors
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, bytes, 0x00020000);
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), r, offset, 0, 0);
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), r, offset, 0, kNonTemporal);
 #endif
 }
 __device__ __forceinline__ void buf_store4(const char* base, int bytes, int offset, unsigned v) {
@@ -653,8 +658,14 @@ __device__ __forceinline__ ExpertRows expert_rows(const GradRows& p, int i) {
 // wait would drain the ring.
 struct ExpertTable {
   ExpertRows rows[256];
-  int tiles[257];  // tiles of BM rows in front of expert i
+  Divisor own[256];  // tiles of BM rows of expert i
+  int tiles[257];    // those in front of it
 };
+
+__device__ __forceinline__ int quotient(int n, Divisor by) {
+  const unsigned q = __umulhi((unsigned)n, by.m);
+  return (int)(q + ((unsigned)n - q * by.d >= by.d ? 1u : 0u));
+}
 
 __device__ __forceinline__ int tiles_of(int n, int BM) { return (n + BM - 1) / BM; }
 
@@ -668,6 +679,7 @@ __device__ __forceinline__ void fill_table(const GradRows& p, ExpertTable& t) {
     const ExpertRows r = expert_rows(p, i);
     t.rows[i] = r;
     n = tiles_of(r.n0, BM) + tiles_of(r.n1, BM);
+    t.own[i] = Divisor{(unsigned)n, 0xffffffffu / (unsigned)max(n, 1)};
   }
   int inc = n;
 #pragma unroll
@@ -727,10 +739,12 @@ struct DgradJob {
     const int before = __builtin_amdgcn_readfirstlane(tab.tiles[e]);
     const int r0 = __builtin_amdgcn_readfirstlane(tab.rows[e].r0), n0 = __builtin_amdgcn_readfirstlane(tab.rows[e].n0);
     const int r1 = __builtin_amdgcn_readfirstlane(tab.rows[e].r1), n1 = __builtin_amdgcn_readfirstlane(tab.rows[e].n1);
-    const int t0 = tiles_of(n0, T::BM), t1 = tiles_of(n1, T::BM);
+    const Divisor own{(unsigned)__builtin_amdgcn_readfirstlane((int)tab.own[e].d),
+                      (unsigned)__builtin_amdgcn_readfirstlane((int)tab.own[e].m)};
+    const int t0 = tiles_of(n0, T::BM);
     const int local = L - before * NT;
-    const int nt = local / (t0 + t1);
-    const int ti = local - nt * (t0 + t1);
+    const int nt = quotient(local, own);
+    const int ti = local - nt * (int)own.d;
     const int n = ti < t0 ? n0 : n1, first = (ti < t0 ? ti : ti - t0) * T::BM;
     Info i;
     i.e = e;
@@ -914,20 +928,20 @@ struct WgradJob {
   __device__ __forceinline__ WgradJob(const WgradArgs& p_, const ExpertTable& t) : p(p_), tab(t) {}
 
   __device__ __forceinline__ Info decode(int L) const {
-    const int per_e = p.units / p.rows.E;
     Info i;
-    i.e = L / per_e;
-    L -= i.e * per_e;
-    i.w = (p.n > 1 && L >= p.first[1] ? 1 : 0) + (p.n > 2 && L >= p.first[2] ? 1 : 0);
-    L -= p.first[i.w];
-    const int MT = (p.M[i.w] + T::BM - 1) / T::BM, NT = (p.N[i.w] + T::BN - 1) / T::BN;
-    // groups of 8 row tiles by all column tiles, so the tiles at work at a time
-    // form a near-square patch of the output that shares both operands in L2
-    const int gsz = 8 * NT;
-    const int grp = L / gsz, in = L - grp * gsz;
-    const int gm = min(8, MT - grp * 8);
-    const int nt = in / gm;
-    i.mbase = (grp * 8 + in - nt * gm) * T::BM;
+    i.e = quotient(L, p.per_e);
+    L -= i.e * (int)p.per_e.d;
+    i.w = (p.n > 1 && L >= p.prod[1].first ? 1 : 0) + (p.n > 2 && L >= p.prod[2].first ? 1 : 0);
+    const WgradProduct& w = p.prod[i.w];
+    L -= w.first;
+    // bands of kBand row tiles by all column tiles: the tiles that an XCD works at
+    // a time share both operands in L2 and store long runs of each output row
+    // (bands of 2 against 8 row tiles, the Mixtral shape: 599 against 618 us with 16
+    // rows in all, 2985 against 3011 us with 8192)
+    const int band = quotient(L, w.band), in = L - band * (int)w.band.d;
+    const bool whole = (band + 1) * kBand <= w.MT;
+    const int nt = whole ? in / kBand : quotient(in, w.last);
+    i.mbase = (band * kBand + in - nt * (whole ? kBand : (int)w.last.d)) * T::BM;
     i.nbase = nt * T::BN;
     i.rows = T::BM;
     const int r0 = __builtin_amdgcn_readfirstlane(tab.rows[i.e].r0);
@@ -935,10 +949,10 @@ struct WgradJob {
     const int r1 = __builtin_amdgcn_readfirstlane(tab.rows[i.e].r1);
     i.n1 = __builtin_amdgcn_readfirstlane(tab.rows[i.e].n1);
     i.panel = p.panel;
-    i.mpanels = (p.M[i.w] - i.mbase) / T::KS;  // (M and N are multiples of 64)
-    i.npanels = (p.N[i.w] - i.nbase) / T::KS;
-    const char* P = static_cast<const char*>(p.P[i.w]) + (size_t)(i.mbase / T::KS) * p.panel;
-    const char* Q = static_cast<const char*>(p.Q[i.w]) + (size_t)(i.nbase / T::KS) * p.panel;
+    i.mpanels = (w.M - i.mbase) / T::KS;  // (M and N are multiples of 64)
+    i.npanels = (w.N - i.nbase) / T::KS;
+    const char* P = static_cast<const char*>(w.P) + (size_t)(i.mbase / T::KS) * p.panel;
+    const char* Q = static_cast<const char*>(w.Q) + (size_t)(i.nbase / T::KS) * p.panel;
     i.p0 = P + (size_t)r0 * 64;
     i.q0 = Q + (size_t)r0 * 64;
     i.p1 = P + (size_t)r1 * 64;
@@ -960,14 +974,15 @@ struct WgradJob {
     s.mbytes = s.nbytes = j < t.steps ? left * 64 : 0;
   }
   __device__ __forceinline__ bool store(const Info& t, int wave, int lane, f32x4_t (&acc)[T::MI][T::NI]) const {
-    const int M = p.M[t.w], N = p.N[t.w];
+    const WgradProduct& w = p.prod[t.w];
+    const int M = w.M, N = w.N;
     const int n0 = t.nbase + (wave % T::WN) * T::TN;  // as in DgradJob: all in or all out
     if (n0 >= N) return false;
     // M is a multiple of 64, so whole groups of 16 rows are in or out
     const int ld = N * EB;
     const OutTile<Tr> out =
-        OutTile<Tr>::matrix(static_cast<const char*>(p.out[t.w]) + ((size_t)t.e * M + t.mbase) * ld, M - t.mbase, ld,
-                            T::m_first(wave), n0, lane, p.blocked16, T::TN * EB >= 128);
+        OutTile<Tr>::matrix(static_cast<const char*>(w.out) + ((size_t)t.e * M + t.mbase) * ld,
+                            min(T::BM, M - t.mbase), ld, T::m_first(wave), n0, lane, p.blocked16, T::TN * EB >= 128);
 #pragma unroll
     for (int mi = 0; mi < T::MI; ++mi) {
       float v[T::NI][4];
@@ -1079,12 +1094,19 @@ template <class Tr, class T>
 hipError_t launch_wgrad_cfg(WgradArgs a, hipStream_t stream) {
   long long per_e = 0;
   for (int w = 0; w < a.n; ++w) {
-    a.first[w] = (int)per_e;
-    per_e += (long long)((a.M[w] + T::BM - 1) / T::BM) * ((a.N[w] + T::BN - 1) / T::BN);
+    WgradProduct& p = a.prod[w];
+    const long long NT = (p.N + T::BN - 1) / T::BN;
+    p.MT = (p.M + T::BM - 1) / T::BM;
+    p.first = (int)per_e;
+    if (p.MT == 0 || kBand * NT * p.MT > 0x7fffff00LL) return hipErrorInvalidValue;
+    p.band = divisor((unsigned)(kBand * NT));
+    p.last = divisor(p.MT % kBand != 0 ? p.MT % kBand : kBand);
+    per_e += NT * p.MT;
   }
   if (per_e == 0) return hipSuccess;
   if (per_e * a.rows.E > 0x7fffff00LL) return hipErrorInvalidValue;
   a.units = (int)(per_e * a.rows.E);
+  a.per_e = divisor((unsigned)per_e);
   hipLaunchKernelGGL((wgrad_kernel<Tr, T>), dim3(grid_of<T>(a.units)), dim3(T::NTH), 0, stream, a);
   return hipGetLastError();
 }

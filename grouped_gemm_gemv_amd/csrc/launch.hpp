@@ -236,15 +236,32 @@ struct DgradArgs {
   int dot_ld;
 };
 
+// Division of n < 2^31 by d: m = (2^32 - 1) / d puts n m / 2^32 between n / d - 1/2
+// and n / d, so its whole part is the quotient or one less.
+struct Divisor {
+  unsigned d, m;
+};
+inline Divisor divisor(unsigned d) { return Divisor{d, 0xffffffffu / d}; }
+
+// One weight gradient out[E][M][N] = P^T Q by expert (panels of M and N columns).
+struct WgradProduct {
+  const void* P;
+  const void* Q;
+  void* out;
+  int M, N;
+  // set by the launcher: the product's first unit inside an expert, its row tiles,
+  // the units of a band of kBand row tiles, the row tiles of the last band
+  int first, MT;
+  Divisor band, last;
+};
+
+constexpr int kBand = 2;
 struct WgradArgs {
   GradRows rows;
-  int n;              // products
-  const void* P[3];   // panels of M columns
-  const void* Q[3];   // panels of N columns
-  size_t panel;       // bytes of a panel
-  void* out[3];       // [E][M][N]
-  int M[3], N[3];
-  int first[3];       // first unit of each product inside an expert (set by the launcher)
+  int n;         // products
+  WgradProduct prod[3];
+  size_t panel;  // bytes of a panel
+  Divisor per_e;  // units of an expert (set by the launcher, as the next)
   int units;
   int blocked16;
 };

@@ -227,6 +227,15 @@ FFN_CASES = [
     dict(T=64, d=128, E=8, k=2, F=256, dtype="f32"),
     dict(T=70, d=192, E=5, k=2, F=320, dtype="f32", cap=20, layout=1, drop=0.1),
     dict(T=300, d=64, E=2, k=1, F=192, dtype="f32", hot=1),
+    # more tiles than workgroups, which take several in turn: wide, narrow, low
+    # and fp32 tiles of the first data gradient, wide ones of the second, with the
+    # weight gradients' in each
+    dict(T=2060, d=64, E=4, k=1, F=12288, cap=300),
+    dict(T=2060, d=64, E=4, k=1, F=6144),
+    dict(T=640, d=64, E=64, k=1, F=2048, drop=0.1),
+    dict(T=1500, d=64, E=8, k=1, F=4096, dtype="f32"),
+    dict(T=2060, d=12288, E=4, k=1, F=64),
+    dict(T=600, d=192, E=16, k=1, F=1536, cap=30, layout=1),
 ]
 
 
@@ -374,6 +383,7 @@ def test_layer_forward_then_backward(kw, router):
 @pytest.mark.parametrize("kw", [
     dict(T=200, d=256, E=8, k=2, F=320), dict(T=300, d=128, E=16, k=4, F=192, cap=40, layout=1),
     dict(T=3, d=64, E=8, k=2, F=128), dict(T=64, d=128, E=8, k=2, F=256, dtype="f32"),
+    dict(T=600, d=192, E=16, k=2, F=1536),  # several tiles for each workgroup
 ], ids=str)
 def test_graph_replays_match_eager(kw):
     """Both passes captured into one graph; two graphs share the workspace; eager work in between."""

@@ -515,7 +515,7 @@ moe_status_t forward_impl(const moe_shape_t* s, const void* x, const void* w_rou
 // `ffn`; dx_perm, which only the whole backward pass keeps here, is last.
 struct BackPlan {
   size_t saved_bytes, saved_up, saved_gate_exp, saved_up_exp;
-  int ranges, range_steps;  // token ranges of the router's weight gradient, K steps each
+  int steps, ranges, range_steps;  // K steps of the router's weight gradient, its token ranges, steps of one
   size_t dz, dense_hi, dense_lo, sums, part, route_ws;
   int mean, dot_ld;
   size_t x_perm, dout_perm, dg, du, hw, wrow, dot, ffn_ws;  // from the start of the experts' part
@@ -541,6 +541,7 @@ BackPlan back_plan(const moe_shape_t& s) {
   const int64_t steps = ceil_div(s.T, 64 / (int64_t)eb);
   const int64_t tiles = ceil_div(s.d, moe::kRouteGradCols[s.dtype]) * ceil_div(s.E, 64);
   const int64_t want = std::min(ceil_div(2 * kComputeUnits, tiles), std::max<int64_t>(1, steps / 8));
+  b.steps = (int)steps;
   b.range_steps = (int)ceil_div(steps, want);
   b.ranges = (int)ceil_div(steps, b.range_steps);
   o = 0;
@@ -588,7 +589,6 @@ moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const
                                   const float* topk_w, const void* w_gate, const void* w_up, const void* w_down,
                                   const moe_dispatch_t& d, const moe_saved8_t& saved, void* dx_perm, float* dtopk_w,
                                   void* dw_gate, void* dw_up, void* dw_down, char* ws, hipStream_t st) {
-  const int Tk = s.T * s.k;
   const int64_t row_bytes = (int64_t)s.d * elt_bytes(s);
   float* wrow = reinterpret_cast<float*>(ws + b.wrow);
   if (moe::launch_gather_backward(x, dout, topk_w, d.token_of, d.row_of, row_space(s), s.k, row_bytes, ws + b.x_perm,
@@ -622,6 +622,9 @@ moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const
   a.K = s.F;
   a.N = s.d;
   a.out = dx_perm;
+  a.row_of = d.row_of;
+  a.entries = s.T * s.k;
+  a.dw = dtopk_w;
   if (moe::launch_dgrad(s.dtype, false, b.mean, a, tiles, st) != hipSuccess) return MOE_ERR_HIP;
   moe::WgradArgs g{};
   g.rows = a.rows;
@@ -640,8 +643,7 @@ moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const
     add(ws + b.dg, ws + b.x_perm, dw_gate, s.F, s.d);
     add(ws + b.du, ws + b.x_perm, dw_up, s.F, s.d);
   }
-  if (g.n > 0 && moe::launch_wgrad(s.dtype, g, st) != hipSuccess) return MOE_ERR_HIP;
-  return hip_status(moe::launch_dot_finish(a.dot, a.dot_ld, d.row_of, Tk, dtopk_w, st));
+  return g.n > 0 ? hip_status(moe::launch_wgrad(s.dtype, g, st)) : MOE_OK;
 }
 
 // The router's gradient; with row_of set, dx also takes the sum of dx_perm's rows.
@@ -666,11 +668,15 @@ moe_status_t enqueue_route_backward(const moe_shape_t& s, const BackPlan& b, con
   if ((s.dtype == MOE_BF16 ? moe::launch_route_wgrad_bf16(a, b.ranges, st)
                            : moe::launch_route_wgrad_f32(a, b.ranges, st)) != hipSuccess)
     return MOE_ERR_HIP;
-  if (moe::launch_token_backward(s.dtype, dx_perm, row_of, dz, ids, w_router, s.T, s.k, s.d, s.E, dx, st) !=
-      hipSuccess)
-    return MOE_ERR_HIP;
+  moe::RouteFinish fin{};
+  fin.part = a.part;
+  fin.sums = sums;
+  fin.dw_router = dw_router;
+  fin.dbias = dbias;
+  fin.ranges = b.ranges;
+  fin.steps = b.steps;
   return hip_status(
-      moe::launch_route_finish(s.dtype, a.part, b.ranges, sums, s.T, s.E, s.d, dw_router, dbias, st));
+      moe::launch_token_backward(s.dtype, dx_perm, row_of, dz, ids, w_router, s.T, s.k, s.d, s.E, dx, fin, st));
 }
 
 }  // namespace
@@ -952,7 +958,7 @@ moe_status_t moe_permute_backward(const moe_shape_t* s, const void* dx_perm, con
   if (!dx_perm || !dx || !disp || !disp->row_of) return MOE_ERR_NULL_PTR;
   if (!aligned({dx_perm, dx}, 16)) return MOE_ERR_INVALID_ARG;
   return hip_status(moe::launch_token_backward(s->dtype, dx_perm, disp->row_of, nullptr, nullptr, nullptr, s->T, s->k,
-                                               s->d, s->E, dx, stream));
+                                               s->d, s->E, dx, moe::RouteFinish{}, stream));
 }
 
 moe_status_t moe_route_backward(const moe_shape_t* s, const void* x, const void* w_router, const int32_t* topk_ids,
@@ -1037,7 +1043,7 @@ moe_status_t moe_backward(const moe_shape_t* s, const void* x, const void* w_rou
     return st;
   if (w_router == nullptr)
     return hip_status(moe::launch_token_backward(s->dtype, dx_perm, disp->row_of, nullptr, nullptr, nullptr, s->T,
-                                                 s->k, s->d, s->E, dx, stream));
+                                                 s->k, s->d, s->E, dx, moe::RouteFinish{}, stream));
   return enqueue_route_backward(*s, b, x, w_router, topk_ids, topk_w, dtopk_w, dx_perm, disp->row_of, dx, dw_router,
                                 dbias, ws, stream);
 }

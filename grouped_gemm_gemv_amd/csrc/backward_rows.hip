@@ -13,12 +13,6 @@ namespace {
 
 constexpr int kSlots = 4;  // slots of a token worked at a time
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-
 // Gradient of out_t = sum_j w_j y_j for slots 4 blockIdx.y .. + 3 of token
 // blockIdx.x: dy_j = w_j dout_t (one rounding) and dw_j = <dout_t, y_j>.  dout_t
 // is read once for the four slots.  dw: thread partials over its chunks, then
@@ -83,22 +77,62 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const char* __res
   }
 }
 
+// dw_router = the token ranges' partial sums in order, one rounding
+// (workgroups 0 .. sum_blocks - 1); dbias_e = expert e's sums over the K steps (the
+// E workgroups behind them: threads, lanes, then wavefronts in order).
+template <class Tr>
+__device__ __forceinline__ void route_finish(const RouteFinish& p, int E, int d) {
+  using Elt = typename Tr::T;
+  if ((int)blockIdx.x < p.sum_blocks) {
+    const int64_t Ed = (int64_t)E * d, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= Ed) return;
+    float4 s = *reinterpret_cast<const float4*>(p.part + i);
+    for (int r = 1; r < p.ranges; ++r) {
+      const float4 v = *reinterpret_cast<const float4*>(p.part + r * Ed + i);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    store4<Tr>(static_cast<char*>(p.dw_router) + i * sizeof(Elt), s.x, s.y, s.z, s.w);
+    return;
+  }
+  __shared__ float wave_part[4];
+  const int e = blockIdx.x - p.sum_blocks;
+  float s = 0.f;
+  for (int i = threadIdx.x; i < p.steps; i += 256) s += p.sums[(size_t)i * E + e];
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) wave_part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) p.dbias[e] = (wave_part[0] + wave_part[1]) + (wave_part[2] + wave_part[3]);
+}
+
 // dx_t = sum_j dx_perm[row_j] + sum_j dz_j w_router[id_j]: fp32, the rows in
 // slot order and then the router's part, one rounding.  Either sum may be
-// absent (row_of or dz null).  The router's rows stay in L2.
+// absent (row_of or dz null).  The router's rows stay in L2.  `lanes` threads
+// (64 or 256) work on a token.  The first fin.blocks workgroups finish the
+// router's other gradients instead (nothing here needs them, and they would be
+// a launch of their own).
 template <class Tr>
 __global__ __launch_bounds__(256) void token_backward_kernel(const char* __restrict__ dx_perm,
                                                              const int32_t* __restrict__ row_of,
                                                              const float* __restrict__ dz,
                                                              const int32_t* __restrict__ ids,
-                                                             const char* __restrict__ w_router, int k, int d, int E,
-                                                             char* __restrict__ dx) {
+                                                             const char* __restrict__ w_router, int T, int k, int d,
+                                                             int E, int lanes, char* __restrict__ dx,
+                                                             RouteFinish fin) {
   using Elt = typename Tr::T;
+  if ((int)blockIdx.x < fin.blocks) {
+    route_finish<Tr>(fin, E, d);
+    return;
+  }
   constexpr int EPC = Tr::EPC;
   const size_t row_bytes = (size_t)d * sizeof(Elt);
   const int nchunk = d / EPC;
-  const size_t t = blockIdx.x;
-  for (int c = threadIdx.x; c < nchunk; c += blockDim.x) {
+  const int per = 256 / lanes;
+  const size_t t = (size_t)((int)blockIdx.x - fin.blocks) * per + threadIdx.x / lanes;
+  if (t >= (size_t)T) return;
+  for (int c = threadIdx.x & (lanes - 1); c < nchunk; c += lanes) {
     const size_t o = (size_t)c * 16;
     float acc[EPC];
 #pragma unroll
@@ -197,39 +231,6 @@ __global__ __launch_bounds__(256) void route_dz_kernel(const int32_t* __restrict
   }
 }
 
-// dw_router = the token ranges' partial sums in order, one rounding
-// (blocks 0 .. sum_blocks - 1); dbias_e = expert e's sums over the K steps (the E
-// blocks behind them: threads, lanes, then wavefronts in order).
-template <class Tr>
-__global__ __launch_bounds__(256) void route_finish_kernel(const float* __restrict__ part, int ranges, int sum_blocks,
-                                                           const float* __restrict__ sums, int steps, int E,
-                                                           int64_t Ed, char* __restrict__ dw_router,
-                                                           float* __restrict__ dbias) {
-  using Elt = typename Tr::T;
-  if ((int)blockIdx.x < sum_blocks) {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (i >= Ed) return;
-    float4 s = *reinterpret_cast<const float4*>(part + i);
-    for (int r = 1; r < ranges; ++r) {
-      const float4 v = *reinterpret_cast<const float4*>(part + r * Ed + i);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-    }
-    store4<Tr>(dw_router + i * sizeof(Elt), s.x, s.y, s.z, s.w);
-    return;
-  }
-  __shared__ float wave_part[4];
-  const int e = blockIdx.x - sum_blocks;
-  float s = 0.f;
-  for (int i = threadIdx.x; i < steps; i += 256) s += sums[(size_t)i * E + e];
-  s = wave_sum(s);
-  if ((threadIdx.x & 63) == 0) wave_part[threadIdx.x >> 6] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) dbias[e] = (wave_part[0] + wave_part[1]) + (wave_part[2] + wave_part[3]);
-}
-
 // Rows of x and dout in expert order, in panels, and the routing weight of each
 // row: a wavefront takes 16 rows and blockIdx.y a share of their columns.  It
 // reads 128 bytes of 8 rows at a time and writes 8 rows of 64 bytes, one run, to
@@ -281,21 +282,6 @@ __global__ __launch_bounds__(256) void gather_backward_kernel(const char* __rest
   }
 }
 
-// dw_f = the row's partial sums of <D, h>: lane i takes i, i + 64, ... in order.
-__global__ __launch_bounds__(256) void dot_finish_kernel(const float* __restrict__ dot, int ld,
-                                                         const int32_t* __restrict__ row_of, int Tk,
-                                                         float* __restrict__ dw) {
-  const int64_t f = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (f >= Tk) return;
-  const int row = row_of[f];
-  const int lane = threadIdx.x & 63;
-  float s = 0.f;
-  if (row >= 0)
-    for (int i = lane; i < ld; i += 64) s += dot[(size_t)row * ld + i];
-  s = wave_sum(s);
-  if (lane == 0) dw[f] = s;
-}
-
 // Values of one projection's codes (blockIdx.y: gate, up): a thread turns one
 // block of 16 into bf16, which holds every such value exactly.
 __global__ __launch_bounds__(256) void saved8_unpack_kernel(const int8_t* __restrict__ g8,
@@ -340,14 +326,19 @@ hipError_t launch_combine_backward(int dtype, const void* dout, const void* y, c
 
 hipError_t launch_token_backward(int dtype, const void* dx_perm, const int32_t* row_of, const float* dz,
                                  const int32_t* ids, const void* w_router, int T, int k, int d, int E, void* dx,
-                                 hipStream_t stream) {
-  const dim3 grid(T), block(row_threads(dtype, d));
+                                 RouteFinish fin, hipStream_t stream) {
+  const int lanes = row_threads(dtype, d), per = 256 / lanes;
+  fin.sum_blocks = fin.part != nullptr ? (int)(((int64_t)E * d / 4 + 255) / 256) : 0;
+  fin.blocks = fin.sum_blocks + (fin.dbias != nullptr ? E : 0);
+  const dim3 grid((unsigned)fin.blocks + ((unsigned)T + per - 1) / per), block(256);
   if (dtype == 1)
     hipLaunchKernelGGL(token_backward_kernel<TBF16>, grid, block, 0, stream, static_cast<const char*>(dx_perm),
-                       row_of, dz, ids, static_cast<const char*>(w_router), k, d, E, static_cast<char*>(dx));
+                       row_of, dz, ids, static_cast<const char*>(w_router), T, k, d, E, lanes,
+                       static_cast<char*>(dx), fin);
   else
     hipLaunchKernelGGL(token_backward_kernel<TF32>, grid, block, 0, stream, static_cast<const char*>(dx_perm),
-                       row_of, dz, ids, static_cast<const char*>(w_router), k, d, E, static_cast<char*>(dx));
+                       row_of, dz, ids, static_cast<const char*>(w_router), T, k, d, E, lanes,
+                       static_cast<char*>(dx), fin);
   return hipGetLastError();
 }
 
@@ -365,21 +356,6 @@ hipError_t launch_route_dz(int dtype, const int32_t* ids, const float* w, const 
   return hipGetLastError();
 }
 
-hipError_t launch_route_finish(int dtype, const float* part, int ranges, const float* sums, int T, int E, int d,
-                               void* dw_router, float* dbias, hipStream_t stream) {
-  const int64_t Ed = (int64_t)E * d;
-  const int sum_blocks = (int)((Ed / 4 + 255) / 256);
-  const int KS = dtype == 1 ? 32 : 16, steps = (int)(((int64_t)T + KS - 1) / KS);
-  const dim3 grid(sum_blocks + (dbias != nullptr ? E : 0)), block(256);
-  if (dtype == 1)
-    hipLaunchKernelGGL(route_finish_kernel<TBF16>, grid, block, 0, stream, part, ranges, sum_blocks, sums, steps, E,
-                       Ed, static_cast<char*>(dw_router), dbias);
-  else
-    hipLaunchKernelGGL(route_finish_kernel<TF32>, grid, block, 0, stream, part, ranges, sum_blocks, sums, steps, E,
-                       Ed, static_cast<char*>(dw_router), dbias);
-  return hipGetLastError();
-}
-
 hipError_t launch_gather_backward(const void* x, const void* dout, const float* topk_w, const int32_t* token_of,
                                   const int32_t* row_of, int64_t rows, int k, int64_t row_bytes, void* x_panels,
                                   void* dout_panels, float* wrow, hipStream_t stream) {
@@ -389,11 +365,6 @@ hipError_t launch_gather_backward(const void* x, const void* dout, const float* 
   hipLaunchKernelGGL(gather_backward_kernel, dim3((unsigned)groups, (unsigned)shares), dim3(256), 0, stream,
                      static_cast<const char*>(x), static_cast<const char*>(dout), topk_w, token_of, row_of, rows, k,
                      row_bytes, static_cast<char*>(x_panels), static_cast<char*>(dout_panels), wrow);
-  return hipGetLastError();
-}
-
-hipError_t launch_dot_finish(const float* dot, int ld, const int32_t* row_of, int Tk, float* dw, hipStream_t stream) {
-  hipLaunchKernelGGL(dot_finish_kernel, dim3((Tk + 3) / 4), dim3(256), 0, stream, dot, ld, row_of, Tk, dw);
   return hipGetLastError();
 }
 

@@ -672,7 +672,7 @@ __device__ __forceinline__ int tiles_of(int n, int BM) { return (n + BM - 1) / B
 // Filled by a whole workgroup of NTH >= 256 threads.
 template <int BM>
 __device__ __forceinline__ void fill_table(const GradRows& p, ExpertTable& t) {
-  __shared__ int wave_sum[4];
+  __shared__ int part[4];
   const int i = threadIdx.x, lane = i & 63;
   int n = 0;
   if (i < p.E) {
@@ -687,10 +687,10 @@ __device__ __forceinline__ void fill_table(const GradRows& p, ExpertTable& t) {
     const int v = __shfl_up(inc, o);
     if (lane >= o) inc += v;
   }
-  if (i < 256 && lane == 63) wave_sum[i >> 6] = inc;
+  if (i < 256 && lane == 63) part[i >> 6] = inc;
   __syncthreads();
   if (i < 256) {
-    for (int w = 0; w < (i >> 6); ++w) inc += wave_sum[w];
+    for (int w = 0; w < (i >> 6); ++w) inc += part[w];
     t.tiles[i + 1] = inc;  // experts past the last hold no tiles
     if (i == 0) t.tiles[0] = 0;
   }
@@ -903,6 +903,18 @@ template <class Tr, class T, bool DH>
 __global__ __launch_bounds__(T::NTH) void dgrad_kernel(DgradArgs p) {
   MOE_GRAD_RING;
   __shared__ ExpertTable tab;
+  if constexpr (!DH) {
+    // the routing weights' gradients, from the launch before: each wavefront sums
+    // some entries' rows of `dot`, lane i the columns i, i + 64, .. in order
+    for (int f = blockIdx.x * T::NW + wave; f < p.entries; f += gridDim.x * T::NW) {
+      const int row = p.row_of[f];
+      float s = 0.f;
+      if (row >= 0)
+        for (int i = lane; i < p.dot_ld; i += 64) s += p.dot[(size_t)row * p.dot_ld + i];
+      s = wave_sum(s);
+      if (lane == 0) p.dw[f] = s;
+    }
+  }
   fill_table<T::BM>(p.rows, tab);
   DgradJob<Tr, T, DH> job(p, tab);
   const Units u = my_units(job.units());

@@ -163,11 +163,23 @@ hipError_t launch_combine_backward(int dtype, const void* dout, const void* y, c
                                    const int32_t* row_of, int T, int k, int d, void* dy, float* dw,
                                    hipStream_t stream);
 
+// The end of the router's gradients: the weight gradient's partial sums over
+// `ranges` token ranges [ranges][E][d], and the bias gradient's over the K steps
+// [steps][E].  Nothing with part and dbias null.
+struct RouteFinish {
+  const float* part;
+  const float* sums;
+  void* dw_router;
+  float* dbias;
+  int ranges, steps;
+  int sum_blocks, blocks;  // workgroups (set by the launcher)
+};
+
 // dx[t] = sum_j dx_perm[row_of[t k + j]], plus, with dz set, sum_j dz[t k + j]
-// w_router[ids[t k + j]] (dx_perm may then be null).
+// w_router[ids[t k + j]] (dx_perm may then be null); and fin's work.
 hipError_t launch_token_backward(int dtype, const void* dx_perm, const int32_t* row_of, const float* dz,
                                  const int32_t* ids, const void* w_router, int T, int k, int d, int E, void* dx,
-                                 hipStream_t stream);
+                                 RouteFinish fin, hipStream_t stream);
 
 // dz_f = w_f (dw_f - sum_i w_i dw_i), and its dense form by K step for the
 // router's weight gradient (hi, and with bf16 lo: [ceil(T / KS)][E][KS]) with
@@ -187,9 +199,6 @@ struct RouteWgradArgs {
 constexpr int kRouteGradCols[2] = {64, 128};
 hipError_t launch_route_wgrad_bf16(const RouteWgradArgs& a, int ranges, hipStream_t stream);
 hipError_t launch_route_wgrad_f32(const RouteWgradArgs& a, int ranges, hipStream_t stream);
-// dw_router = sum of the ranges (fp32, in order, one rounding); dbias (or null) = sum of the steps' sums.
-hipError_t launch_route_finish(int dtype, const float* part, int ranges, const float* sums, int T, int E, int d,
-                               void* dw_router, float* dbias, hipStream_t stream);
 
 // x and dout in expert order for the backward GEMMs (bit copies), in panels
 // [row_bytes / 64][R][64 bytes], and the routing weight of each row.  Rows without
@@ -197,8 +206,6 @@ hipError_t launch_route_finish(int dtype, const float* part, int ranges, const f
 hipError_t launch_gather_backward(const void* x, const void* dout, const float* topk_w, const int32_t* token_of,
                                   const int32_t* row_of, int64_t rows, int k, int64_t row_bytes, void* x_panels,
                                   void* dout_panels, float* wrow, hipStream_t stream);
-// dw_f = sum of the row's partial sums in order; 0 for an entry without a row.
-hipError_t launch_dot_finish(const float* dot, int ld, const int32_t* row_of, int Tk, float* dw, hipStream_t stream);
 
 // Values of the 8-bit projections of every live row (bf16 holds each exactly).
 hipError_t launch_saved8_unpack(const int8_t* g8, const int8_t* u8, const uint8_t* gx, const uint8_t* ux,
@@ -234,6 +241,10 @@ struct DgradArgs {
   void* hw;    // w_r h, or null
   float* dot;  // [R][dot_ld] partial sums of <D, h>
   int dot_ld;
+  // without it: dw[f] = the sum of dot's row row_of[f] (0 where that is -1)
+  const int32_t* row_of;
+  int entries;
+  float* dw;
 };
 
 // Division of n < 2^31 by d: m = (2^32 - 1) / d puts n m / 2^32 between n / d - 1/2

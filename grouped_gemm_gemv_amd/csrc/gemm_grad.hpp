@@ -24,9 +24,9 @@
 // are kept in panels: [columns of 64 bytes][R rows][64 bytes].  A K step of the
 // data gradients (64 bytes of every row of a tile) and 16 K rows of 64 bytes of
 // the weight gradients are then both one run of memory, whatever the width of
-// a row: with rows of 8 or 28 KB the 256 rows of a step lay a multiple of 4 KB
-// apart, on few memory channels, and the first data gradient took 2500 cycles
-// a step instead of 1200.  Weights are read as the caller keeps them.
+// a row: with rows of 28 KB, a multiple of 4 KB apart, the second data gradient
+// took 2049 instead of 1722 us (8192 rows, d = 4096, F = 14336).  Weights are
+// read as the caller keeps them.
 //
 // A K step is 64 bytes of a K-contiguous row (32 bf16 or 16 fp32), so each
 // operand takes 64 bytes of LDS per tile row or column whatever its
@@ -39,6 +39,18 @@
 // its XCD's range, and the ring runs on across units, so the first steps of
 // the next tile are on their way while the last ones of this one are
 // multiplied and its results are stored.
+//
+// What bounds them, at d = 4096, F = 14336 with 8 experts (bf16):
+//  * many rows: the matrix cores.  8192 rows take 940 us (first data gradient,
+//    1.02 PF/s), 1800 (second, 1.07) and 2980 (weight gradients, 0.97), where a
+//    library product of 8192 cubed reaches 1.24, or 1.10 with a transposed
+//    operand.  The second loses a quarter of its last round of tiles (2.3 tiles
+//    for each workgroup); a step of the weight gradients takes 1640 cycles, of
+//    which 1024 are MFMAs, because both operands come through the transposing
+//    LDS read, at half the rate of the plain one;
+//  * few rows: memory.  32 rows take 181 and 290 us (0.94 and 1.88 GB of
+//    weights, 5.2 and 6.5 TB/s) and 610 (2.8 GB of weight gradients, 4.6 TB/s
+//    where a fill reaches 6.8: a tile's rows are 512-byte pieces).
 #pragma once
 
 #include <type_traits>
@@ -213,8 +225,8 @@ struct OutTile {
   // which lane group g = lane / 16 holds columns 4g .. 4g + 3.  bf16: lanes 16
   // apart trade halves, so that each stores 16 bytes.  In blocks and panels a
   // piece is one run of 1 KB.  In rows it is half a cache line of each of 16 rows;
-  // two pieces trade rows, so that a store takes whole lines of 8 rows (a store
-  // costs a compute unit about 4 cycles a line it touches, whole or not).
+  // two pieces trade rows, so that a store takes whole lines of 8 rows (weight
+  // gradients of 1024 rows at d = 4096, F = 14336: 939 against 969 us).
   template <int NI>
   __device__ __forceinline__ void put(int m, const float (&v)[NI][4]) const {
     constexpr int PC = NI * EB / 4;
@@ -628,7 +640,9 @@ struct Tile {
           steps<MI>(ct.steps);
         empty_steps(padded(ct) - ct.steps);
         // both halves store at the same time: in turn, each would wait for the
-        // other's stores (4000 of a tile's 62000 cycles)
+        // other's stores.  (Kept in registers and stored a few at a time in the
+        // next unit's steps, weight gradients took no less: 3128 against 3071 us
+        // with 8192 rows at d = 4096, F = 14336, 1094 against 1072 with 1024.)
         if (PP && !second) barrier();
         stores = job.store(ct, wave, lane, acc) ? S - 2 : 0;
         if (done()) break;
@@ -709,6 +723,7 @@ __device__ __forceinline__ Units my_units(int total) {
 }
 
 // out tile = act rows x weights (DH: with the SwiGLU's gradient in the epilogue).
+// A unit's steps go over K, a1 x b1 behind a0 x b0 into the same accumulators.
 template <class Tr, class T, bool DH>
 struct DgradJob {
   static constexpr int EB = T::EB;
@@ -1023,7 +1038,9 @@ __global__ __launch_bounds__(T::NTH) void wgrad_kernel(WgradArgs p) {
 // part[z][e][i] = sum over tokens t of range z of dz[e][t] x[t][i] (fp32 partial
 // sums).  dz is dense with zeros where expert e did not take token t, laid out
 // by K step: [step][E][64 bytes].  bf16 carries it as two terms (high and low
-// part), which keeps 16 bits of its significand.  One tile per workgroup.
+// part), which keeps 16 bits of its significand.  One tile per workgroup, over
+// enough token ranges for two on each compute unit: 12.6 us for 4096 tokens of
+// 2048 bf16 and 64 experts, most of it the latency of a range's 8 to 16 steps.
 template <class Tr, class T>
 struct RouteJob {
   static constexpr int EB = T::EB;

@@ -30,9 +30,10 @@ hipError_t launch_route_wgrad_f32(const RouteWgradArgs& a, int ranges, hipStream
 // Rows of a data gradient's tile.  bf16: 64 rows (three workgroups for each
 // compute unit) where an expert's rows fit one such tile; past 48 rows on
 // average many do not, and their weights would be read twice.  Both data
-// gradients at the Mixtral shape, 64- against 256-row tiles: 32 rows per expert
-// 268 + 299 against 296 + 427 us, 64 rows 293 + 509 against 289 + 372; 64 experts
-// of d = 3584, F = 2560 with 64 rows 376 + 602 against 356 + 462.
+// gradients, 64- against 256-row tiles, us: the Mixtral shape with 32 rows for each
+// expert 202 + 307 against 193 + 387, with 64 rows 269 + 497 against 205 + 402; 64
+// experts of d = 2048, F = 1408 with 48 rows 96 + 162 against 121 + 138, of
+// d = 3584, F = 2560 with 64 rows 331 + 589 against 291 + 446.
 int dgrad_tile_rows(int dtype, int mean) { return dtype == 1 && mean > 48 ? 256 : 64; }
 
 // one partial sum per wavefront column
@@ -40,7 +41,8 @@ int dgrad_dot_cols(int dtype, int mean) { return dgrad_tile_rows(dtype, mean) ==
 
 hipError_t launch_dgrad(int dtype, bool dh, int mean, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
   const int BM = dgrad_tile_rows(dtype, mean);
-  return dtype == 1 ? launch_dgrad_bf16(dh, BM, a, max_tiles, stream) : launch_dgrad_f32(dh, BM, a, max_tiles, stream);
+  return dtype == 1 ? launch_dgrad_bf16(dh, BM, mean, a, max_tiles, stream)
+                    : launch_dgrad_f32(dh, BM, a, max_tiles, stream);
 }
 
 hipError_t launch_wgrad(int dtype, const WgradArgs& a, hipStream_t stream) {

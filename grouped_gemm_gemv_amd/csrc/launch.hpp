@@ -283,7 +283,7 @@ int dgrad_dot_cols(int dtype, int mean);
 int dgrad_tile_rows(int dtype, int mean);
 hipError_t launch_dgrad(int dtype, bool dh, int mean, const DgradArgs& a, long long max_tiles, hipStream_t stream);
 hipError_t launch_wgrad(int dtype, const WgradArgs& a, hipStream_t stream);
-hipError_t launch_dgrad_bf16(bool dh, int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream);
+hipError_t launch_dgrad_bf16(bool dh, int BM, int mean, const DgradArgs& a, long long max_tiles, hipStream_t stream);
 hipError_t launch_dgrad_f32(bool dh, int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream);
 hipError_t launch_wgrad_bf16(const WgradArgs& a, hipStream_t stream);
 hipError_t launch_wgrad_f32(const WgradArgs& a, hipStream_t stream);

@@ -232,6 +232,7 @@ FFN_CASES = [
     # weight gradients' in each
     dict(T=2060, d=64, E=4, k=1, F=12288, cap=300),
     dict(T=2060, d=64, E=4, k=1, F=6144),
+    dict(T=1600, d=64, E=8, k=1, F=3200, cap=100),
     dict(T=640, d=64, E=64, k=1, F=2048, drop=0.1),
     dict(T=1500, d=64, E=8, k=1, F=4096, dtype="f32"),
     dict(T=2060, d=12288, E=4, k=1, F=64),

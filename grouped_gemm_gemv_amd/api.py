@@ -36,6 +36,10 @@ class Shape:
         return MoeShape(self.T, self.d, self.E, self.k, self.F, self.capacity, _DT[self.dtype], self.tile_rows,
                         self.weight_layout)
 
+    def __getstate__(self):
+        """The fields alone: the C struct that _c keeps here can be neither pickled nor copied."""
+        return {f.name: getattr(self, f.name) for f in dataclasses.fields(self)}
+
 
 def _p(t: Optional[torch.Tensor]) -> Optional[int]:
     if t is None:
@@ -306,6 +310,8 @@ def _call(name: str, device, stream, *args):
     """One entry point on the tensors' device, on `stream` or that device's current stream."""
     if device.type != "cuda":
         raise ValueError("libmoe takes device tensors")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, expected {device}")
     s = stream if stream is not None else torch.cuda.current_stream(device)
     fn = getattr(lib(), name)
     if device.index == torch.cuda.current_device():

@@ -219,3 +219,26 @@ def test_python_checks_shapes_before_the_library():
         M.api._in(x, "x", (4, 64), s.dtype, x.device)
     with pytest.raises(ValueError, match="is on"):
         M.api._in(x, "x", (4, 64), s.dtype, torch.device("cuda", 0))
+
+
+@built
+def test_a_shape_that_was_used_still_copies():
+    import copy
+    import pickle
+
+    import grouped_gemm_gemv_amd as M
+    s = M.Shape(3, 64, 4, 2, 64, capacity=1)
+    n = M.backward_workspace_size(s)
+    for c in (copy.copy(s), copy.deepcopy(s), pickle.loads(pickle.dumps(s))):
+        assert c == s and hash(c) == hash(s) and M.backward_workspace_size(c) == n
+
+
+def test_a_stream_of_another_device_is_refused():
+    import types
+
+    import torch
+
+    from grouped_gemm_gemv_amd import api
+    other = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    with pytest.raises(ValueError, match="stream"):
+        api._call("moe_permute_backward", torch.device("cuda", 0), other)

@@ -518,7 +518,8 @@ struct BackPlan {
   int steps, ranges, range_steps;  // K steps of the router's weight gradient, its token ranges, steps of one
   size_t dz, dense_hi, dense_lo, sums, part, route_ws;
   int mean, dot_ld;
-  size_t x_perm, dout_perm, dg, du, hw, wrow, dot, ffn_ws;  // from the start of the experts' part
+  int64_t k_steps;  // of the weight gradients, at most
+  size_t x_steps, dout_steps, dout_perm, dg, du, hw, wrow, dot, ffn_ws;  // from the start of the experts' part
   size_t dx_perm, backward_ws;
 };
 
@@ -554,7 +555,10 @@ BackPlan back_plan(const moe_shape_t& s) {
   b.mean = (int)mean_rows(s);
   b.dot_ld = s.F / moe::dgrad_dot_cols(s.dtype, b.mean);
   o = 0;
-  b.x_perm = take(R * s.d * eb);
+  const int KS = 64 / (int)eb;
+  b.k_steps = pass_max_tiles(s, KS, 0) + pass_max_tiles(s, KS, 1);
+  b.x_steps = take((size_t)b.k_steps * s.d * 64);
+  b.dout_steps = take((size_t)b.k_steps * s.d * 64);
   b.dout_perm = take(R * s.d * eb);
   b.dg = take(R * s.F * eb);
   b.du = take(R * s.F * eb);
@@ -589,22 +593,32 @@ moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const
                                   const float* topk_w, const void* w_gate, const void* w_up, const void* w_down,
                                   const moe_dispatch_t& d, const moe_saved8_t& saved, void* dx_perm, float* dtopk_w,
                                   void* dw_gate, void* dw_up, void* dw_down, char* ws, hipStream_t st) {
-  const int64_t row_bytes = (int64_t)s.d * elt_bytes(s);
-  float* wrow = reinterpret_cast<float*>(ws + b.wrow);
-  if (moe::launch_gather_backward(x, dout, topk_w, d.token_of, d.row_of, row_space(s), s.k, row_bytes, ws + b.x_perm,
-                                  ws + b.dout_perm, wrow, st) != hipSuccess)
-    return MOE_ERR_HIP;
+  moe::GatherArgs r{};
+  r.rows = grad_rows(s, d);
+  r.x = x;
+  r.dout = dout;
+  r.topk_w = topk_w;
+  r.token_of = d.token_of;
+  r.row_of = d.row_of;
+  r.k = s.k;
+  r.d = s.d;
+  r.panel = (size_t)row_space(s) * 64;
+  r.x_steps = dw_gate != nullptr ? ws + b.x_steps : nullptr;
+  r.dout_steps = dw_down != nullptr ? ws + b.dout_steps : nullptr;
+  r.dout_panels = ws + b.dout_perm;
+  r.wrow = reinterpret_cast<float*>(ws + b.wrow);
+  if (moe::launch_gather_backward(s.dtype, r, b.k_steps, st) != hipSuccess) return MOE_ERR_HIP;
   const int BM = moe::dgrad_tile_rows(s.dtype, b.mean);
   const int64_t tiles = pass_max_tiles(s, BM, 0) + pass_max_tiles(s, BM, 1);
   moe::DgradArgs a{};
-  a.rows = grad_rows(s, d);
+  a.rows = r.rows;
   a.blocked16 = s.weight_layout == MOE_LAYOUT_BLOCKED16 ? 1 : 0;
-  a.panel = (size_t)row_space(s) * 64;
+  a.panel = r.panel;
   a.a0 = ws + b.dout_perm;
   a.b0 = w_down;
   a.K = s.d;
   a.N = s.F;
-  a.wrow = wrow;
+  a.wrow = r.wrow;
   a.g8 = saved.gate;
   a.u8 = saved.up;
   a.gx = saved.gate_exp;
@@ -630,18 +644,19 @@ moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const
   g.rows = a.rows;
   g.blocked16 = a.blocked16;
   g.panel = a.panel;
-  auto add = [&](const void* P, const void* Q, void* out, int M, int N) {
+  g.M = s.d;
+  g.N = s.F;
+  auto add = [&](const void* P, const void* Q, void* out, int swap) {
     moe::WgradProduct& w = g.prod[g.n++];
     w.P = P;
     w.Q = Q;
     w.out = out;
-    w.M = M;
-    w.N = N;
+    w.swap = swap;
   };
-  if (dw_down != nullptr) add(ws + b.dout_perm, ws + b.hw, dw_down, s.d, s.F);
+  if (dw_down != nullptr) add(r.dout_steps, ws + b.hw, dw_down, 0);
   if (dw_gate != nullptr) {
-    add(ws + b.dg, ws + b.x_perm, dw_gate, s.F, s.d);
-    add(ws + b.du, ws + b.x_perm, dw_up, s.F, s.d);
+    add(r.x_steps, ws + b.dg, dw_gate, 1);
+    add(r.x_steps, ws + b.du, dw_up, 1);
   }
   return g.n > 0 ? hip_status(moe::launch_wgrad(s.dtype, g, st)) : MOE_OK;
 }

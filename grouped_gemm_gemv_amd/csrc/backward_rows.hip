@@ -1,8 +1,7 @@
 // Row kernels of the backward pass: the gradients of the weighted combine and
 // of the sorted dispatch, the router's gradient apart from its matrix product,
-// the gather in front of the experts' backward GEMMs, and the values of the
-// 8-bit projections.  All of them move whole rows once and are bound by that;
-// every sum is fp32 in a fixed order.
+// and the values of the 8-bit projections.  All of them move whole rows once and
+// are bound by that; every sum is fp32 in a fixed order.
 #include <algorithm>
 
 #include "device_common.hpp"
@@ -235,58 +234,6 @@ __global__ __launch_bounds__(256) void route_dz_kernel(const int32_t* __restrict
   }
 }
 
-// Rows of x and dout in expert order, in panels, and the routing weight of each
-// row: a wavefront takes 16 rows and blockIdx.y a share of their columns.  It
-// reads 128 bytes of 8 rows at a time and writes 8 rows of 64 bytes, one run, to
-// each of two panels.  Bound by memory: 52 us for 8192 rows of 4096 bf16 (5.2
-// TB/s read and written); 5 us, latency, for the smallest.
-__global__ __launch_bounds__(256) void gather_backward_kernel(const char* __restrict__ x,
-                                                              const char* __restrict__ dout,
-                                                              const float* __restrict__ topk_w,
-                                                              const int32_t* __restrict__ token_of,
-                                                              const int32_t* __restrict__ row_of, int64_t rows, int k,
-                                                              int64_t row_bytes, char* __restrict__ x_panels,
-                                                              char* __restrict__ dout_panels,
-                                                              float* __restrict__ wrow) {
-  const int lane = threadIdx.x & 63;
-  const int64_t r0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 16;
-  if (r0 >= rows) return;
-  if (blockIdx.y == 0 && lane < 16 && r0 + lane < rows) {
-    const int t = token_of[r0 + lane];
-    if (t >= 0)
-      for (int j = 0; j < k; ++j)
-        if (row_of[(int64_t)t * k + j] == r0 + lane) wrow[r0 + lane] = topk_w[(int64_t)t * k + j];
-  }
-  const int64_t panel = rows * 64;
-  const int byte = (lane & 7) * 16;
-  const int64_t c0 = row_bytes / 128 * blockIdx.y / gridDim.y * 128;
-  const int64_t c1 = row_bytes / 128 * (blockIdx.y + 1) / gridDim.y * 128;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t r = r0 + h * 8 + (lane >> 3);
-    const int t = r < rows ? token_of[r] : -1;
-    if (t < 0) continue;
-    const char* sx = x + t * row_bytes + byte;
-    const char* sd = dout + t * row_bytes + byte;
-    const int64_t at = (byte >> 6) * panel + r * 64 + (byte & 63);
-    for (int64_t c = c0; c < c1; c += 256) {
-      uint4 a[2], b[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        if (c + 128 * u < c1) {
-          a[u] = *reinterpret_cast<const uint4*>(sx + c + 128 * u);
-          b[u] = *reinterpret_cast<const uint4*>(sd + c + 128 * u);
-        }
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        if (c + 128 * u < c1) {
-          *reinterpret_cast<uint4*>(x_panels + (c / 64 + 2 * u) * panel + at) = a[u];
-          *reinterpret_cast<uint4*>(dout_panels + (c / 64 + 2 * u) * panel + at) = b[u];
-        }
-    }
-  }
-}
-
 // Values of one projection's codes (blockIdx.y: gate, up): a thread turns one
 // block of 16 into bf16, which holds every such value exactly.  Bound by memory:
 // 18 us for 1024 rows of 14336 (5 TB/s).
@@ -359,18 +306,6 @@ hipError_t launch_route_dz(int dtype, const int32_t* ids, const float* w, const 
   else
     hipLaunchKernelGGL(route_dz_kernel<TF32>, grid, block, lds, stream, ids, w, dw, T, k, E, dz,
                        static_cast<float*>(dense_hi), static_cast<float*>(nullptr), sums);
-  return hipGetLastError();
-}
-
-hipError_t launch_gather_backward(const void* x, const void* dout, const float* topk_w, const int32_t* token_of,
-                                  const int32_t* row_of, int64_t rows, int k, int64_t row_bytes, void* x_panels,
-                                  void* dout_panels, float* wrow, hipStream_t stream) {
-  // about four workgroups for each of the 256 compute units, as far as the columns go
-  const int64_t groups = (rows + 63) / 64;
-  const int64_t shares = std::max<int64_t>(1, std::min<int64_t>(row_bytes / 512, 1024 / groups));
-  hipLaunchKernelGGL(gather_backward_kernel, dim3((unsigned)groups, (unsigned)shares), dim3(256), 0, stream,
-                     static_cast<const char*>(x), static_cast<const char*>(dout), topk_w, token_of, row_of, rows, k,
-                     row_bytes, static_cast<char*>(x_panels), static_cast<char*>(dout_panels), wrow);
   return hipGetLastError();
 }
 

@@ -53,6 +53,7 @@
 //    where a fill reaches 6.8: a tile's rows are 512-byte pieces).
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -277,6 +278,7 @@ struct Step {
 // How an operand lies in memory and LDS.
 enum Operand {
   kPanelK,  // panels, K along the columns: a step is one panel
+  kSteps,   // [step][columns of the tile's matrix][64 bytes of K]: turned by the gather
   kPanelR,  // panels, K along the rows: a step is KS rows of every panel of the tile
   kRows     // a matrix (or blocked weights), K along its rows: a step is KS rows
 };
@@ -293,18 +295,20 @@ struct Tile {
   static constexpr int MBYTES = 64 * BM, STAGE = 64 * (BM + BN);
   // 1 KB LDS-direct loads per stage and operand, and per wavefront (the last
   // ones repeat an operand's final load, so every wavefront issues NL)
+  static constexpr bool DEALT = MOP == kPanelK;
+  static constexpr int M_STEP = DEALT ? 16 * WM : 16;  // rows between a wavefront's blocks
   static constexpr int QM = BM / 16, QN = BN / 16;
   static constexpr int LM = (QM + NW - 1) / NW, LN = (QN + NW - 1) / NW, NL = LM + LN;
   static constexpr int PL = EB == 2 ? 2 : 1;  // loads per panel of KS rows (kPanelR)
   static_assert(MOP != kRows && NOP != kPanelK, "the M operand comes in panels, the N operand has K along the rows");
   static_assert(TM % 16 == 0 && TN % 16 == 0, "wavefront tile");
+  static_assert(MOP != kPanelR, "K along the rows is the N operand's");
   static_assert(NOP != kRows || BN * EB % 256 == 0, "rows are swizzled within 256 bytes");
-  static_assert(MOP != kPanelR || (QM % NW == 0 && NW % 2 == 0 && TM * EB % 64 == 0), "panels of the M operand");
   static_assert(NOP != kPanelR || (QN % NW == 0 && NW % 2 == 0 && TN * EB % 64 == 0), "panels of the N operand");
   static_assert(S >= 3 && (S - 2) * NL + MI * NI * EB / 4 < 64, "ring");
 
   // LDS layouts, each free of bank conflicts:
-  //  kPanelK: rows of 64 bytes; chunk c (16 bytes) of row r sits at c ^ (r / 2 & 3),
+  //  kPanelK, kSteps: rows of 64 bytes; chunk c (16 bytes) of row r sits at c ^ (r / 2 & 3),
   //    so the 8 rows that eight lanes of a 16-byte read take cover 128 bytes of
   //    banks twice over (with r / 4 & 3 the reads took 40 % more cycles);
   //  kPanelR: the tile's panels in turn, KS rows of 64 bytes each.  bf16: a
@@ -328,7 +332,7 @@ struct Tile {
   template <Operand OP>
   __device__ __forceinline__ static int panel_offset(int q, int lane) {
     const int s = lane >> 2, c = lane & 3;
-    if constexpr (OP == kPanelK) {
+    if constexpr (OP == kPanelK || OP == kSteps) {
       const int r = q * 16 + s;
       return r * 64 + ((c ^ swz_c(r)) << 4);
     } else if constexpr (EB == 2) {
@@ -352,15 +356,15 @@ struct Tile {
     return blocked16 ? (k >> 4) * 16 * ld + (byte >> 6) * 1024 + (k & 15) * 64 + (byte & 63) : k * ld + byte;
   }
 
-  // Operand of the 16 columns (or rows) number sub of the wavefront's part:
-  // columns in one run, rows of kPanelK dealt to the WM wavefront rows in turn,
-  // so that a tile that is not full loads them evenly.  Lane group g = lane / 16
+  // Operand of the 16 columns (or rows) number sub of the wavefront's part: in one
+  // run, but rows of kPanelK dealt to the WM wavefront rows in turn, so that a
+  // tile that is not full loads them evenly.  Lane group g = lane / 16
   // holds K elements 8g..8g+7 (bf16) or 4g..4g+3 (fp32), whatever the layout.
   // lane0: lane part of the LDS address, from frag_lane.
   template <Operand OP>
   __device__ __forceinline__ static int frag_lane(int lane, int first) {
     const int g = lane >> 4, i = lane & 15;
-    if constexpr (OP == kPanelK) {
+    if constexpr (OP == kPanelK || OP == kSteps) {
       const int r = first + i;
       return r * 64 + ((g ^ swz_c(r)) << 4);
     } else if constexpr (OP == kPanelR) {
@@ -378,8 +382,8 @@ struct Tile {
   }
   template <Operand OP>
   __device__ __forceinline__ static uint4 frag(const char* st, int lane0, int sub) {
-    if constexpr (OP == kPanelK) {
-      return *reinterpret_cast<const uint4*>(st + lane0 + sub * WM * 1024);
+    if constexpr (OP == kPanelK || OP == kSteps) {
+      return *reinterpret_cast<const uint4*>(st + lane0 + sub * M_STEP * 64);
     } else if constexpr (EB == 2) {
       // kRows: 16 columns are 32 bytes, and column blocks differ by an exclusive
       // or in the address (the swizzle stays within 256 bytes)
@@ -395,12 +399,10 @@ struct Tile {
     }
   }
 
-  static constexpr bool MKS = MOP == kPanelR;
-  static __device__ __forceinline__ int m_first(int wave) { return MKS ? (wave / WN) * TM : (wave / WN) * 16; }
-  static constexpr int M_STEP = MKS ? 16 : 16 * WM;  // rows between a wavefront's blocks
+  static __device__ __forceinline__ int m_first(int wave) { return DEALT ? (wave / WN) * 16 : (wave / WN) * TM; }
   // Row (or column) of the tile that accumulator block mi of this lane holds.
   static __device__ __forceinline__ int m_of(int wave, int mi, int lane) {
-    return MKS ? (wave / WN) * TM + mi * 16 + (lane & 15) : (mi * WM + wave / WN) * 16 + (lane & 15);
+    return m_first(wave) + mi * M_STEP + (lane & 15);
   }
   static __device__ __forceinline__ int n_of(int wave, int ni, int lane) {
     return (wave % WN) * TN + ni * 16 + (lane >> 4) * 4;
@@ -479,8 +481,7 @@ struct Tile {
       for (int i = 0; i < NL; ++i) {
         const int in = i < LM ? 0 : i - LM;
         if (i < LM)
-          load_lds(MOP == kPanelR ? panel_desc(ld.m, ld.mbytes, i, lt.mpanels) : m, moff[i < LM ? i : 0],
-                   at + mq(wave, i) * 1024);
+          load_lds(m, moff[i < LM ? i : 0], at + mq(wave, i) * 1024);
         else
           load_lds(NOP == kPanelR ? panel_desc(ld.n, ld.nbytes, in, lt.npanels) : n, noff[in],
                    at + MBYTES + nq(wave, in) * 1024);
@@ -511,25 +512,28 @@ struct Tile {
       });
       cs = cs == S - 1 ? 0 : cs + 1;
     }
-    template <int MB>
+    // SWAP: the other operand is the MFMA's first, and a lane ends with 4
+    // consecutive m of one n.
+    template <int MB, bool SWAP>
     __device__ __forceinline__ void multiply() {
 #pragma unroll
       for (int mi = 0; mi < MB; ++mi)
 #pragma unroll
-        for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = mma16<Tr>(nf[ni], mf[mi], acc[mi][ni]);
+        for (int ni = 0; ni < NI; ++ni)
+          acc[mi][ni] = SWAP ? mma16<Tr>(mf[mi], nf[ni], acc[mi][ni]) : mma16<Tr>(nf[ni], mf[mi], acc[mi][ni]);
     }
 
     // One step.  This wavefront's loads of the step have landed (those of the
     // S - 2 after it may be in flight); after the barrier everyone's have, and
     // everyone is done with the stage of the step before, which takes the step
     // S - 1 ahead.
-    template <int MB>
+    template <int MB, bool SWAP>
     __device__ __forceinline__ void step() {
       wait_step();
       barrier();
       move<MB>();
       advance();
-      multiply<MB>();
+      multiply<MB, SWAP>();
       turn();
     }
 
@@ -542,14 +546,14 @@ struct Tile {
     // have landed (both halves wait so before the first one reads that stage).
     // Where the next loads lie is worked out between the multiplications: with
     // it in the data phase, that phase was the longer one and set the pace.
-    template <int MB>
+    template <int MB, bool SWAP>
     __device__ __forceinline__ void step_pp() {
       move<MB>();
       wait_step();
       wait_lds();
       barrier();
       advance();
-      multiply<MB>();
+      multiply<MB, SWAP>();
 #pragma unroll
       for (int i = 0; i < MB * NI; ++i) {  // one MFMA, then up to two scalar instructions in its shadow
         __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
@@ -575,14 +579,14 @@ struct Tile {
 
     // The steps of a unit, for its first MB blocks of 16 rows per wavefront, and
     // the empty ones behind them, which keep the ring going and nothing else.
-    template <int MB>
+    template <int MB, bool SWAP>
     __device__ __forceinline__ void steps(int n) {
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
         if constexpr (PP)
-          step_pp<MB>();
+          step_pp<MB, SWAP>();
         else
-          step<MB>();
+          step<MB, SWAP>();
       }
     }
     __device__ __forceinline__ void empty_steps(int n) {
@@ -633,11 +637,18 @@ struct Tile {
         for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
           for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        // a tile of at most half the rows multiplies half the blocks
-        if (!MKS && MI % 2 == 0 && ct.rows <= BM / 2)
-          steps<(MI + 1) / 2>(ct.steps);
-        else
-          steps<MI>(ct.steps);
+        if constexpr (MOP == kSteps) {
+          if (ct.swap)
+            steps<MI, true>(ct.steps);
+          else
+            steps<MI, false>(ct.steps);
+        } else {
+          // a tile of at most half the rows multiplies half the blocks
+          if (MI % 2 == 0 && ct.rows <= BM / 2)
+            steps<(MI + 1) / 2, false>(ct.steps);
+          else
+            steps<MI, false>(ct.steps);
+        }
         empty_steps(padded(ct) - ct.steps);
         // both halves store at the same time: in turn, each would wait for the
         // other's stores.  (Kept in registers and stored a few at a time in the
@@ -731,7 +742,7 @@ struct DgradJob {
     int steps, row0, rows, nbase, e;
     const char *a0, *a1, *b0, *b1;  // operands of the tile's rows and expert
     size_t panel;                   // bytes of a panel of activations
-    int mpanels, npanels;
+    int npanels;
   };
   const DgradArgs& p;
   const ExpertTable& tab;
@@ -938,20 +949,94 @@ __global__ __launch_bounds__(T::NTH) void dgrad_kernel(DgradArgs p) {
 
 // ---- weight gradients ---------------------------------------------------------
 
-// out[e][m][n] = sum over the rows r of expert e of P[r][m] Q[r][n]: up to three
-// such products in one launch.  An expert without rows gets zeros.
+// Rows of x and dout in expert order for the GEMMs, and the routing weight of
+// each row.  A workgroup takes one K step of the weight gradients (KS rows of
+// one run of an expert) and a share of the columns.  The steps of x and dout are
+// turned, [step][d][64 bytes], with zeros behind a run's last row: through LDS
+// in the layout and with the reads of an operand in panels, so that what a
+// lane reads there are the 16 bytes it writes.  dout goes to panels as well, for
+// the first data gradient.  x_steps and dout_steps may be null: not wanted.
+// Bound by memory.
+template <class Tr, class T>
+__global__ __launch_bounds__(256) void gather_backward_kernel(GatherArgs p) {
+  constexpr int KS = T::KS, EB = T::EB, LD = KS / 16;  // 16-byte loads of 256 columns' bytes per thread and tensor
+  __shared__ __attribute__((aligned(1024))) char st[2][4 * KS * 64];
+  __shared__ ExpertTable tab;
+  fill_table<KS>(p.rows, tab);
+  const int step = blockIdx.x;
+  if (step >= tab.tiles[256]) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int e = 0;
+  for (int b = 0; b < p.rows.E; b += 64)
+    e += __popcll(__ballot(b + lane < p.rows.E && tab.tiles[b + lane + 1] <= step));
+  const ExpertRows x = tab.rows[e];
+  const int j = step - tab.tiles[e], t0 = tiles_of(x.n0, KS);
+  const int first = (j < t0 ? j : j - t0) * KS, row0 = (j < t0 ? x.r0 : x.r1) + first;
+  const int n = min(KS, (j < t0 ? x.n0 : x.n1) - first);
+  if (blockIdx.y == 0 && (int)threadIdx.x < n) {
+    const int r = row0 + threadIdx.x, t = p.token_of[r];
+    for (int i = 0; i < p.k; ++i)
+      if (t >= 0 && p.row_of[(size_t)t * p.k + i] == r) p.wrow[r] = p.topk_w[(size_t)t * p.k + i];
+  }
+  const int row_bytes = p.d * EB, panels = row_bytes / 64;
+  const int c0 = (int)((int64_t)((panels + 3) / 4) * blockIdx.y / gridDim.y) * 4;
+  const int c1 = min(panels, (int)((int64_t)((panels + 3) / 4) * (blockIdx.y + 1) / gridDim.y) * 4);
+  const int c = threadIdx.x & 15;  // 16 lanes read 256 bytes of a row
+  int tok[LD];
+#pragma unroll
+  for (int u = 0; u < LD; ++u) {
+    const int r = u * 16 + (threadIdx.x >> 4);
+    tok[u] = r < n ? p.token_of[row0 + r] : -1;
+  }
+  const int fl = T::template frag_lane<kPanelR>(lane, 0);
+  for (int q = c0; q < c1; q += 4) {
+    const int at = q + (c >> 2);  // this thread's panel
+#pragma unroll
+    for (int u = 0; u < LD; ++u) {
+      const int r = u * 16 + (threadIdx.x >> 4);
+      uint4 a = make_uint4(0, 0, 0, 0), b = a;
+      if (tok[u] >= 0 && at < c1) {
+        const size_t o = (size_t)tok[u] * row_bytes + (size_t)q * 64 + c * 16;
+        if (p.x_steps != nullptr) a = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.x) + o);
+        b = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.dout) + o);
+        *reinterpret_cast<uint4*>(p.dout_panels + at * p.panel + (size_t)(row0 + r) * 64 + (c & 3) * 16) = b;
+      }
+      const int slot = EB == 2 ? r * 64 + (((c & 3) ^ ((r >> 2) & 2)) << 4)
+                               : ((r >> 2) | (r & 3) << 2) * 64 + ((c & 3) << 4);
+      *reinterpret_cast<uint4*>(st[0] + (c >> 2) * KS * 64 + slot) = a;
+      *reinterpret_cast<uint4*>(st[1] + (c >> 2) * KS * 64 + slot) = b;
+    }
+    __syncthreads();
+    if (q + wave < c1) {  // a wavefront turns one panel
+#pragma unroll
+      for (int s = 0; s < 2 / (EB / 2); ++s) {
+        const int i = lane & 15, g = lane >> 4;
+        const size_t o = ((size_t)step * p.d + (q + wave) * KS + s * 16 + i) * 64 + g * 16;
+        if (p.x_steps != nullptr)
+          *reinterpret_cast<uint4*>(p.x_steps + o) = T::template frag<kPanelR>(st[0] + wave * KS * 64, fl, s);
+        if (p.dout_steps != nullptr)
+          *reinterpret_cast<uint4*>(p.dout_steps + o) = T::template frag<kPanelR>(st[1] + wave * KS * 64, fl, s);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Sums over the rows r of expert e, up to three in one launch: out[m][n] =
+// sum P[r][m] Q[r][n] with m over d and n over F, or (swap) out[n][m] the same
+// value.  P in steps, Q in panels.  An expert without rows gets zeros.
 template <class Tr, class T>
 struct WgradJob {
   static constexpr int EB = T::EB;
   struct Info {
-    int steps, rows, steps0, e, w, mbase, nbase;
+    int steps, rows, steps0, e, w, mbase, nbase, swap;
     int n0, n1;
     size_t panel;
-    int mpanels, npanels;           // panels of either operand from the tile's first on
-    const char *p0, *q0, *p1, *q1;  // the operands' first rows of either run
+    int npanels;               // panels of Q from the tile's first on
+    const char *p0, *q0, *q1;  // the first step of P, the first rows of Q's either run
   };
   const WgradArgs& p;
-  const ExpertTable& tab;
+  const ExpertTable& tab;  // of KS rows: tiles[e] is expert e's first step
   __device__ __forceinline__ WgradJob(const WgradArgs& p_, const ExpertTable& t) : p(p_), tab(t) {}
 
   __device__ __forceinline__ Info decode(int L) const {
@@ -961,63 +1046,85 @@ struct WgradJob {
     i.w = (p.n > 1 && L >= p.prod[1].first ? 1 : 0) + (p.n > 2 && L >= p.prod[2].first ? 1 : 0);
     const WgradProduct& w = p.prod[i.w];
     L -= w.first;
-    // bands of kBand row tiles by all column tiles: the tiles that an XCD works at
-    // a time share both operands in L2 and store long runs of each output row
-    // (bands of 2 against 8 row tiles, the Mixtral shape: 599 against 618 us with 16
-    // rows in all, 2985 against 3011 us with 8192)
+    // bands of kBand tiles of out's rows by all tiles of its columns: the tiles that
+    // an XCD works at a time share both operands in L2 and store long runs of
+    // each row (bands of 2 against 8 tiles, the Mixtral shape: 599 against 618 us
+    // with 16 rows in all, 2985 against 3011 us with 8192)
     const int band = quotient(L, w.band), in = L - band * (int)w.band.d;
-    const bool whole = (band + 1) * kBand <= w.MT;
-    const int nt = whole ? in / kBand : quotient(in, w.last);
-    i.mbase = (band * kBand + in - nt * (whole ? kBand : (int)w.last.d)) * T::BM;
-    i.nbase = nt * T::BN;
-    i.rows = T::BM;
+    const bool whole = (band + 1) * kBand <= w.RT;
+    const int ct = whole ? in / kBand : quotient(in, w.last);
+    const int rt = band * kBand + in - ct * (whole ? kBand : (int)w.last.d);
+    i.swap = w.swap;
+    i.mbase = (w.swap ? ct : rt) * T::BM;
+    i.nbase = (w.swap ? rt : ct) * T::BN;
+    i.rows = min(T::BM, p.M - i.mbase);
     const int r0 = __builtin_amdgcn_readfirstlane(tab.rows[i.e].r0);
     i.n0 = __builtin_amdgcn_readfirstlane(tab.rows[i.e].n0);
     const int r1 = __builtin_amdgcn_readfirstlane(tab.rows[i.e].r1);
     i.n1 = __builtin_amdgcn_readfirstlane(tab.rows[i.e].n1);
+    const int step = __builtin_amdgcn_readfirstlane(tab.tiles[i.e]);
     i.panel = p.panel;
-    i.mpanels = (w.M - i.mbase) / T::KS;  // (M and N are multiples of 64)
-    i.npanels = (w.N - i.nbase) / T::KS;
-    const char* P = static_cast<const char*>(w.P) + (size_t)(i.mbase / T::KS) * p.panel;
+    i.npanels = (p.N - i.nbase) / T::KS;  // (N is a multiple of 64)
+    i.p0 = static_cast<const char*>(w.P) + ((size_t)step * p.M + i.mbase) * 64;
     const char* Q = static_cast<const char*>(w.Q) + (size_t)(i.nbase / T::KS) * p.panel;
-    i.p0 = P + (size_t)r0 * 64;
     i.q0 = Q + (size_t)r0 * 64;
-    i.p1 = P + (size_t)r1 * 64;
     i.q1 = Q + (size_t)r1 * 64;
     i.steps0 = (i.n0 + T::KS - 1) / T::KS;
     i.steps = i.steps0 + (i.n1 + T::KS - 1) / T::KS;
     return i;
   }
   __device__ __forceinline__ Step first(const Info& t) const {
-    const int left = t.steps > 0 ? min(T::KS, t.n0 > 0 ? t.n0 : t.n1) * 64 : 0;
-    return Step{t.n0 > 0 ? t.p0 : t.p1, t.n0 > 0 ? t.q0 : t.q1, left, left};
+    const bool in = t.steps > 0;
+    return Step{t.p0, t.n0 > 0 ? t.q0 : t.q1, in ? t.rows * 64 : 0,
+                in ? min(T::KS, t.n0 > 0 ? t.n0 : t.n1) * 64 : 0};
   }
   // Step j: KS rows on; the rows behind the capacity follow those in front of it.
   __device__ __forceinline__ void next(const Info& t, int j, Step& s) const {
-    const bool second = j >= t.steps0;
-    s.m = j == t.steps0 ? t.p1 : s.m + T::KS * 64;
+    const bool second = j >= t.steps0, in = j < t.steps;
+    s.m += (size_t)p.M * 64;
     s.n = j == t.steps0 ? t.q1 : s.n + T::KS * 64;
     const int left = max(0, min(T::KS, second ? t.n1 - (j - t.steps0) * T::KS : t.n0 - j * T::KS));
-    s.mbytes = s.nbytes = j < t.steps ? left * 64 : 0;
+    s.mbytes = in ? t.rows * 64 : 0;
+    s.nbytes = in ? left * 64 : 0;
   }
   __device__ __forceinline__ bool store(const Info& t, int wave, int lane, f32x4_t (&acc)[T::MI][T::NI]) const {
-    const WgradProduct& w = p.prod[t.w];
-    const int M = w.M, N = w.N;
-    const int n0 = t.nbase + (wave % T::WN) * T::TN;  // as in DgradJob: all in or all out
-    if (n0 >= N) return false;
-    // M is a multiple of 64, so whole groups of 16 rows are in or out
-    const int ld = N * EB;
-    const OutTile<Tr> out =
-        OutTile<Tr>::matrix(static_cast<const char*>(w.out) + ((size_t)t.e * M + t.mbase) * ld,
-                            min(T::BM, M - t.mbase), ld, T::m_first(wave), n0, lane, p.blocked16, T::TN * EB >= 128);
+    const int M = p.M, N = p.N, m0 = T::m_first(wave), n0 = (wave % T::WN) * T::TN;
+    const char* base = static_cast<const char*>(p.prod[t.w].out) + (size_t)t.e * M * N * EB;
+    // M and N are multiples of 64, so whole groups of 16 rows are in or out, and so
+    // are the columns of a wavefront (64 or 32) or of a part of it (64)
+    if (!t.swap) {
+      if (t.nbase + n0 >= N) return false;
+      const int ld = N * EB;
+      const OutTile<Tr> out = OutTile<Tr>::matrix(base + (size_t)t.mbase * ld, t.rows, ld, m0, t.nbase + n0, lane,
+                                                  p.blocked16, T::TN * EB >= 128);
 #pragma unroll
-    for (int mi = 0; mi < T::MI; ++mi) {
-      float v[T::NI][4];
+      for (int mi = 0; mi < T::MI; ++mi) {
+        float v[T::NI][4];
 #pragma unroll
-      for (int ni = 0; ni < T::NI; ++ni)
+        for (int ni = 0; ni < T::NI; ++ni)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[ni][r] = acc[mi][ni][r];
-      out.template put<T::NI>(mi * T::M_STEP, v);
+          for (int r = 0; r < 4; ++r) v[ni][r] = acc[mi][ni][r];
+        out.template put<T::NI>(mi * 16, v);
+      }
+      return true;
+    }
+    constexpr int PART = T::MI < 4 ? T::MI : 4, PARTS = T::MI / PART;  // blocks of 16 columns in a part
+    const int ld = M * EB, rows = min(T::BN, N - t.nbase);
+#pragma unroll
+    for (int h = 0; h < PARTS; ++h) {
+      const int col = t.mbase + m0 + h * PART * 16;
+      if (col >= M) return false;
+      const OutTile<Tr> out = OutTile<Tr>::matrix(base + (size_t)t.nbase * ld, rows, ld, n0, col, lane, p.blocked16,
+                                                  PART * 16 * EB >= 128);
+#pragma unroll
+      for (int ni = 0; ni < T::NI; ++ni) {
+        float v[PART][4];
+#pragma unroll
+        for (int mi = 0; mi < PART; ++mi)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[mi][r] = acc[h * PART + mi][ni][r];
+        out.template put<PART>(ni * 16, v);
+      }
     }
     return true;
   }
@@ -1027,7 +1134,7 @@ template <class Tr, class T>
 __global__ __launch_bounds__(T::NTH) void wgrad_kernel(WgradArgs p) {
   MOE_GRAD_RING;
   __shared__ ExpertTable tab;
-  fill_table<T::BM>(p.rows, tab);
+  fill_table<T::KS>(p.rows, tab);
   WgradJob<Tr, T> job(p, tab);
   const Units u = my_units(p.units);
   typename T::template Runner<WgradJob<Tr, T>>(job, ring, ring_at, u.first, u.stride, u.end, lane, wave).run();
@@ -1047,7 +1154,7 @@ struct RouteJob {
   struct Info {
     int steps, rows;
     size_t panel;
-    int mpanels, npanels;
+    int npanels;
   };
   const RouteWgradArgs& p;
   const int nbase, mbase, rows, j0, per;
@@ -1055,7 +1162,7 @@ struct RouteJob {
       : p(p_), nbase(blockIdx.x * T::BN), mbase(blockIdx.y * T::BM), rows(min(T::BM, p_.E - mbase)),
         j0(min((p_.T + T::KS - 1) / T::KS, (int)blockIdx.z * p_.steps)),
         per(min((p_.T + T::KS - 1) / T::KS - j0, p_.steps)) {}
-  __device__ __forceinline__ Info decode(int) const { return Info{per * (p.dz_lo != nullptr ? 2 : 1), rows, 0, 0, 0}; }
+  __device__ __forceinline__ Info decode(int) const { return Info{per * (p.dz_lo != nullptr ? 2 : 1), rows, 0, 0}; }
   __device__ __forceinline__ int rows_offset(const Info&, int q, int lane) const {
     return T::rows_offset(q, lane, nbase, p.d, p.d * EB, 0);
   }
@@ -1121,22 +1228,30 @@ hipError_t launch_dgrad_cfg(const DgradArgs& a, long long max_tiles, hipStream_t
 
 template <class Tr, class T>
 hipError_t launch_wgrad_cfg(WgradArgs a, hipStream_t stream) {
-  long long per_e = 0;
+  const long long MT = (a.M + T::BM - 1) / T::BM, NT = (a.N + T::BN - 1) / T::BN;
+  if (kBand * MT * NT > 0x7fffff00LL || a.n * MT * NT * a.rows.E > 0x7fffff00LL) return hipErrorInvalidValue;
   for (int w = 0; w < a.n; ++w) {
     WgradProduct& p = a.prod[w];
-    const long long NT = (p.N + T::BN - 1) / T::BN;
-    p.MT = (p.M + T::BM - 1) / T::BM;
-    p.first = (int)per_e;
-    if (p.MT == 0 || kBand * NT * p.MT > 0x7fffff00LL) return hipErrorInvalidValue;
-    p.band = divisor((unsigned)(kBand * NT));
-    p.last = divisor(p.MT % kBand != 0 ? p.MT % kBand : kBand);
-    per_e += NT * p.MT;
+    p.first = (int)(w * MT * NT);
+    p.RT = (int)(p.swap ? NT : MT);
+    p.band = divisor((unsigned)(kBand * (p.swap ? MT : NT)));
+    p.last = divisor(p.RT % kBand != 0 ? p.RT % kBand : kBand);
   }
-  if (per_e == 0) return hipSuccess;
-  if (per_e * a.rows.E > 0x7fffff00LL) return hipErrorInvalidValue;
-  a.units = (int)(per_e * a.rows.E);
-  a.per_e = divisor((unsigned)per_e);
+  a.units = (int)(a.n * MT * NT * a.rows.E);
+  a.per_e = divisor((unsigned)(a.n * MT * NT));
+  if (a.units == 0) return hipSuccess;
   hipLaunchKernelGGL((wgrad_kernel<Tr, T>), dim3(grid_of<T>(a.units)), dim3(T::NTH), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <class Tr, class T>
+hipError_t launch_gather_cfg(const GatherArgs& a, long long max_steps, hipStream_t stream) {
+  // about four workgroups for each compute unit, as far as the columns go
+  const long long quads = ((long long)a.d * T::EB + 255) / 256;
+  const long long shares = std::max(1LL, std::min(quads, 4LL * kComputeUnits / std::max(1LL, max_steps)));
+  if (max_steps > 0x7fffffLL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((gather_backward_kernel<Tr, T>), dim3((unsigned)max_steps, (unsigned)shares), dim3(256), 0,
+                     stream, a);
   return hipGetLastError();
 }
 

@@ -11,7 +11,7 @@ using D64 = Tile<TBF16, 64, 128, 1, 4, kPanelK, kRows, 4, 3, false>;
 // weight gradients, whatever the rows: with 16 rows per expert, when the stores of
 // the gradients are all there is, 128 x 128 tiles (two workgroups for each compute
 // unit) took 904 us at the Mixtral shape and 956 against 747 us with 64 rows
-using W256 = Tile<TBF16, 256, 256, 2, 4, kPanelR, kPanelR, 4, 1, true>;
+using W256 = Tile<TBF16, 256, 256, 2, 4, kSteps, kPanelR, 4, 1, true>;
 // router weight gradient: experts by columns
 using R64 = Tile<TBF16, 64, 128, 1, 4, kPanelK, kRows, 4, 3, false>;
 
@@ -42,6 +42,10 @@ hipError_t launch_dgrad_bf16(bool dh, int BM, int mean, const DgradArgs& a, long
 
 hipError_t launch_wgrad_bf16(const WgradArgs& a, hipStream_t stream) {
   return launch_wgrad_cfg<TBF16, W256>(a, stream);
+}
+
+hipError_t launch_gather_backward_bf16(const GatherArgs& a, long long max_steps, hipStream_t stream) {
+  return launch_gather_cfg<TBF16, W256>(a, max_steps, stream);
 }
 
 hipError_t launch_route_wgrad_bf16(const RouteWgradArgs& a, int ranges, hipStream_t stream) {

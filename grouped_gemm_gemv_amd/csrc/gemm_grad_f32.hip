@@ -7,7 +7,7 @@ using namespace grad;
 // fp32 MFMAs run at a sixteenth of the bf16 rate, so small tiles keep up (a ring
 // of 8 stages gained nothing at the tiny layer, 64 tokens of 128 columns)
 using D64 = Tile<TF32, 64, 64, 2, 2, kPanelK, kRows, 4, 4, false>;
-using W64 = Tile<TF32, 64, 64, 2, 2, kPanelR, kPanelR, 4, 4, false>;
+using W64 = Tile<TF32, 64, 64, 2, 2, kSteps, kPanelR, 4, 4, false>;
 }  // namespace
 
 hipError_t launch_dgrad_f32(bool dh, int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
@@ -18,6 +18,10 @@ hipError_t launch_dgrad_f32(bool dh, int BM, const DgradArgs& a, long long max_t
 
 hipError_t launch_wgrad_f32(const WgradArgs& a, hipStream_t stream) {
   return launch_wgrad_cfg<TF32, W64>(a, stream);
+}
+
+hipError_t launch_gather_backward_f32(const GatherArgs& a, long long max_steps, hipStream_t stream) {
+  return launch_gather_cfg<TF32, W64>(a, max_steps, stream);
 }
 
 hipError_t launch_route_wgrad_f32(const RouteWgradArgs& a, int ranges, hipStream_t stream) {
@@ -43,6 +47,11 @@ hipError_t launch_dgrad(int dtype, bool dh, int mean, const DgradArgs& a, long l
   const int BM = dgrad_tile_rows(dtype, mean);
   return dtype == 1 ? launch_dgrad_bf16(dh, BM, mean, a, max_tiles, stream)
                     : launch_dgrad_f32(dh, BM, a, max_tiles, stream);
+}
+
+hipError_t launch_gather_backward(int dtype, const GatherArgs& a, long long max_steps, hipStream_t stream) {
+  return dtype == 1 ? launch_gather_backward_bf16(a, max_steps, stream)
+                    : launch_gather_backward_f32(a, max_steps, stream);
 }
 
 hipError_t launch_wgrad(int dtype, const WgradArgs& a, hipStream_t stream) {

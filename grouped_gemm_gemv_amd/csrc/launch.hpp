@@ -200,13 +200,6 @@ constexpr int kRouteGradCols[2] = {64, 128};
 hipError_t launch_route_wgrad_bf16(const RouteWgradArgs& a, int ranges, hipStream_t stream);
 hipError_t launch_route_wgrad_f32(const RouteWgradArgs& a, int ranges, hipStream_t stream);
 
-// x and dout in expert order for the backward GEMMs (bit copies), in panels
-// [row_bytes / 64][R][64 bytes], and the routing weight of each row.  Rows without
-// a token are left as they are.
-hipError_t launch_gather_backward(const void* x, const void* dout, const float* topk_w, const int32_t* token_of,
-                                  const int32_t* row_of, int64_t rows, int k, int64_t row_bytes, void* x_panels,
-                                  void* dout_panels, float* wrow, hipStream_t stream);
-
 // Values of the 8-bit projections of every live row (bf16 holds each exactly).
 hipError_t launch_saved8_unpack(const int8_t* g8, const int8_t* u8, const uint8_t* gx, const uint8_t* ux,
                                 const int32_t* token_of, int64_t rows, int F, void* gate, void* up,
@@ -254,28 +247,51 @@ struct Divisor {
 };
 inline Divisor divisor(unsigned d) { return Divisor{d, 0xffffffffu / d}; }
 
-// One weight gradient out[E][M][N] = P^T Q by expert (panels of M and N columns).
+// One weight gradient, by expert P^T Q: [E][M][N], or with swap [E][N][M].
 struct WgradProduct {
-  const void* P;
-  const void* Q;
+  const void* P;  // [steps][M][64 bytes]
+  const void* Q;  // panels of N columns
   void* out;
-  int M, N;
-  // set by the launcher: the product's first unit inside an expert, its row tiles,
-  // the units of a band of kBand row tiles, the row tiles of the last band
-  int first, MT;
+  int swap;
+  // set by the launcher: the product's first unit inside an expert, its tiles down
+  // out's rows, the units of a band of kBand of them, those of the last band
+  int first, RT;
   Divisor band, last;
 };
 
 constexpr int kBand = 2;
 struct WgradArgs {
   GradRows rows;
-  int n;         // products
+  int n;          // products
   WgradProduct prod[3];
-  size_t panel;  // bytes of a panel
+  int M, N;
+  size_t panel;   // bytes of a panel
   Divisor per_e;  // units of an expert (set by the launcher, as the next)
   int units;
   int blocked16;
 };
+
+// x and dout in expert order, dout in panels ([row bytes / 64][R][64 bytes]) and
+// both, unless null, in K steps of the weight gradients ([steps][d][64 bytes], an
+// expert's rows from a step of its own on, either run of them), and the
+// routing weight of each row.  Rows without a token are left as they are.
+struct GatherArgs {
+  GradRows rows;
+  const void* x;  // [T][d]
+  const void* dout;
+  const float* topk_w;
+  const int32_t* token_of;
+  const int32_t* row_of;
+  int k, d;
+  size_t panel;
+  char* x_steps;
+  char* dout_steps;
+  char* dout_panels;
+  float* wrow;
+};
+hipError_t launch_gather_backward(int dtype, const GatherArgs& a, long long max_steps, hipStream_t stream);
+hipError_t launch_gather_backward_bf16(const GatherArgs& a, long long max_steps, hipStream_t stream);
+hipError_t launch_gather_backward_f32(const GatherArgs& a, long long max_steps, hipStream_t stream);
 
 // Columns of one partial sum of <D, h>, and rows of a tile, of the data
 // gradients: both go by the mean row count of an expert.

@@ -608,8 +608,6 @@ moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const
   r.dout_panels = ws + b.dout_perm;
   r.wrow = reinterpret_cast<float*>(ws + b.wrow);
   if (moe::launch_gather_backward(s.dtype, r, b.k_steps, st) != hipSuccess) return MOE_ERR_HIP;
-  const int BM = moe::dgrad_tile_rows(s.dtype, b.mean);
-  const int64_t tiles = pass_max_tiles(s, BM, 0) + pass_max_tiles(s, BM, 1);
   moe::DgradArgs a{};
   a.rows = r.rows;
   a.blocked16 = s.weight_layout == MOE_LAYOUT_BLOCKED16 ? 1 : 0;
@@ -628,7 +626,11 @@ moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const
   a.hw = dw_down != nullptr ? ws + b.hw : nullptr;
   a.dot = reinterpret_cast<float*>(ws + b.dot);
   a.dot_ld = b.dot_ld;
-  if (moe::launch_dgrad(s.dtype, true, b.mean, a, tiles, st) != hipSuccess) return MOE_ERR_HIP;
+  auto dgrad = [&](bool dh) {
+    const moe::DgradTile t = moe::dgrad_tile(s.dtype, b.mean, s.E, a.N);
+    return moe::launch_dgrad(s.dtype, dh, t, a, pass_max_tiles(s, t.rows, 0) + pass_max_tiles(s, t.rows, 1), st);
+  };
+  if (dgrad(true) != hipSuccess) return MOE_ERR_HIP;
   a.a0 = ws + b.dg;
   a.a1 = ws + b.du;
   a.b0 = w_gate;
@@ -639,7 +641,7 @@ moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const
   a.row_of = d.row_of;
   a.entries = s.T * s.k;
   a.dw = dtopk_w;
-  if (moe::launch_dgrad(s.dtype, false, b.mean, a, tiles, st) != hipSuccess) return MOE_ERR_HIP;
+  if (dgrad(false) != hipSuccess) return MOE_ERR_HIP;
   moe::WgradArgs g{};
   g.rows = a.rows;
   g.blocked16 = a.blocked16;

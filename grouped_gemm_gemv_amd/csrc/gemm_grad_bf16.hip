@@ -6,6 +6,7 @@ namespace {
 using namespace grad;
 // data gradients, by rows and columns of a tile
 using D256 = Tile<TBF16, 256, 256, 2, 4, kPanelK, kRows, 4, 1, true>;
+using D192 = Tile<TBF16, 192, 256, 2, 4, kPanelK, kRows, 5, 1, true>;
 using D256N = Tile<TBF16, 256, 128, 4, 2, kPanelK, kRows, 5, 1, true>;
 using D64 = Tile<TBF16, 64, 128, 1, 4, kPanelK, kRows, 4, 3, false>;
 // weight gradients, whatever the rows: with 16 rows per expert, when the stores of
@@ -15,29 +16,18 @@ using W256 = Tile<TBF16, 256, 256, 2, 4, kSteps, kPanelR, 4, 1, true>;
 // router weight gradient: experts by columns
 using R64 = Tile<TBF16, 64, 128, 1, 4, kPanelK, kRows, 4, 3, false>;
 
-// 256-row tiles: narrow ones (128 columns) where, with the experts' mean row
-// count and half a tile more each, they make one round of the compute units at
-// most.  Wide against narrow, us: second data gradient at the Mixtral shape 448
-// against 409 with 512 rows, 537 against 466 with 1024, and with the 384 tiles of
-// 2048 rows 600 against 823; 16 experts of d = 3584, F = 2560 with 1024 rows
-// (320 narrow tiles in the first data gradient, 448 in the second) 93 against
-// 126 and 109 against 162.
-bool narrow_tiles(int mean, int E, int N) {
-  const long long tiles = (long long)E * (mean > 128 ? mean + 128 : 256) / 256;
-  return tiles * ((N + 127) / 128) <= kComputeUnits;
-}
-
 template <bool DH>
-hipError_t dgrad_tiles(int BM, int mean, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
-  if (BM == D64::BM) return launch_dgrad_cfg<TBF16, D64, DH>(a, max_tiles, stream);
-  if (BM != D256::BM) return hipErrorInvalidValue;
-  return narrow_tiles(mean, a.rows.E, a.N) ? launch_dgrad_cfg<TBF16, D256N, DH>(a, max_tiles, stream)
-                                           : launch_dgrad_cfg<TBF16, D256, DH>(a, max_tiles, stream);
+hipError_t dgrad_tiles(DgradTile t, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
+  if (t.rows == D64::BM) return launch_dgrad_cfg<TBF16, D64, DH>(a, max_tiles, stream);
+  if (t.rows == D192::BM) return launch_dgrad_cfg<TBF16, D192, DH>(a, max_tiles, stream);
+  if (t.rows != D256::BM) return hipErrorInvalidValue;
+  return t.cols == D256N::BN ? launch_dgrad_cfg<TBF16, D256N, DH>(a, max_tiles, stream)
+                             : launch_dgrad_cfg<TBF16, D256, DH>(a, max_tiles, stream);
 }
 }  // namespace
 
-hipError_t launch_dgrad_bf16(bool dh, int BM, int mean, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
-  return dh ? dgrad_tiles<true>(BM, mean, a, max_tiles, stream) : dgrad_tiles<false>(BM, mean, a, max_tiles, stream);
+hipError_t launch_dgrad_bf16(bool dh, DgradTile tile, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
+  return dh ? dgrad_tiles<true>(tile, a, max_tiles, stream) : dgrad_tiles<false>(tile, a, max_tiles, stream);
 }
 
 hipError_t launch_wgrad_bf16(const WgradArgs& a, hipStream_t stream) {

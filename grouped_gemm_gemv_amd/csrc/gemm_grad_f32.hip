@@ -10,8 +10,8 @@ using D64 = Tile<TF32, 64, 64, 2, 2, kPanelK, kRows, 4, 4, false>;
 using W64 = Tile<TF32, 64, 64, 2, 2, kSteps, kPanelR, 4, 4, false>;
 }  // namespace
 
-hipError_t launch_dgrad_f32(bool dh, int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
-  if (BM != D64::BM) return hipErrorInvalidValue;
+hipError_t launch_dgrad_f32(bool dh, DgradTile tile, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
+  if (tile.rows != D64::BM) return hipErrorInvalidValue;
   return dh ? launch_dgrad_cfg<TF32, D64, true>(a, max_tiles, stream)
             : launch_dgrad_cfg<TF32, D64, false>(a, max_tiles, stream);
 }
@@ -31,22 +31,43 @@ hipError_t launch_route_wgrad_f32(const RouteWgradArgs& a, int ranges, hipStream
   return hipGetLastError();
 }
 
-// Rows of a data gradient's tile.  bf16: 64 rows (three workgroups for each
-// compute unit) where an expert's rows fit one such tile; past 48 rows on
-// average many do not, and their weights would be read twice.  Both data
-// gradients, 64- against 256-row tiles, us: the Mixtral shape with 32 rows for each
-// expert 202 + 307 against 193 + 387, with 64 rows 269 + 497 against 205 + 402; 64
-// experts of d = 2048, F = 1408 with 48 rows 96 + 162 against 121 + 138, of
-// d = 3584, F = 2560 with 64 rows 331 + 589 against 291 + 446.
-int dgrad_tile_rows(int dtype, int mean) { return dtype == 1 && mean > 48 ? 256 : 64; }
+// The tile of a data gradient.  bf16, us of kernel time on each side:
+//  * 64 x 128 (three workgroups for each compute unit) where an expert's rows fit
+//    one such tile; past 48 rows on average many do not, and their weights would
+//    be read twice.  Both data gradients, 64- against 256-row tiles: the Mixtral
+//    shape with 32 rows for each expert 202 + 307 against 193 + 387, with 64 rows
+//    269 + 497 against 205 + 402; 64 experts of d = 2048, F = 1408 with 48 rows
+//    96 + 162 against 121 + 138, of d = 3584, F = 2560 with 64 rows 331 + 589
+//    against 291 + 446;
+//  * 256 x 128 where these make one round of the compute units at most (an
+//    expert takes its mean row count and half a tile more).  256 x 256 against
+//    256 x 128: second data gradient at the Mixtral shape 448 against 409 with 512
+//    rows, 537 against 466 with 1024, but 600 against 823 with 2048; 16 experts of
+//    d = 3584, F = 2560 with 1024 rows (more than one round) 93 against 126 and 109
+//    against 162;
+//  * else 192 or 256 rows by 256, whichever takes fewer rounds times rows; 192
+//    only from an eighth less on, as the lower tile does less with each byte it
+//    loads.  256 against 192 rows, second data gradient at the Mixtral shape with 8192
+//    rows (3 rounds either way) 1787 against 1611, with 4096 1133 against 1019;
+//    first with 8192 rows (8 rounds against 11) 931 against 1018.
+DgradTile dgrad_tile(int dtype, int mean, int E, int N) {
+  if (dtype != 1) return DgradTile{64, 64};
+  if (mean <= 48) return DgradTile{64, 128};
+  auto tiles = [&](int rows) { return (long long)E * std::max(mean + rows / 2, rows) / rows; };
+  if (tiles(256) * ((N + 127) / 128) <= kComputeUnits) return DgradTile{256, 128};
+  auto cost = [&](int rows) {
+    return (tiles(rows) * ((N + 255) / 256) + kComputeUnits - 1) / kComputeUnits * rows;
+  };
+  return DgradTile{9 * cost(192) < 8 * cost(256) ? 192 : 256, 256};
+}
 
 // one partial sum per wavefront column
-int dgrad_dot_cols(int dtype, int mean) { return dgrad_tile_rows(dtype, mean) == 256 ? 64 : 32; }
+int dgrad_dot_cols(int dtype, int mean) { return dtype == 1 && mean > 48 ? 64 : 32; }
 
-hipError_t launch_dgrad(int dtype, bool dh, int mean, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
-  const int BM = dgrad_tile_rows(dtype, mean);
-  return dtype == 1 ? launch_dgrad_bf16(dh, BM, mean, a, max_tiles, stream)
-                    : launch_dgrad_f32(dh, BM, a, max_tiles, stream);
+hipError_t launch_dgrad(int dtype, bool dh, DgradTile tile, const DgradArgs& a, long long max_tiles,
+                        hipStream_t stream) {
+  return dtype == 1 ? launch_dgrad_bf16(dh, tile, a, max_tiles, stream)
+                    : launch_dgrad_f32(dh, tile, a, max_tiles, stream);
 }
 
 hipError_t launch_gather_backward(int dtype, const GatherArgs& a, long long max_steps, hipStream_t stream) {

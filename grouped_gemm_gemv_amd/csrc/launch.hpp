@@ -293,14 +293,19 @@ hipError_t launch_gather_backward(int dtype, const GatherArgs& a, long long max_
 hipError_t launch_gather_backward_bf16(const GatherArgs& a, long long max_steps, hipStream_t stream);
 hipError_t launch_gather_backward_f32(const GatherArgs& a, long long max_steps, hipStream_t stream);
 
-// Columns of one partial sum of <D, h>, and rows of a tile, of the data
-// gradients: both go by the mean row count of an expert.
+// Columns of one partial sum of <D, h>, by the mean row count of an expert, and
+// the tile of a data gradient with N columns.
 int dgrad_dot_cols(int dtype, int mean);
-int dgrad_tile_rows(int dtype, int mean);
-hipError_t launch_dgrad(int dtype, bool dh, int mean, const DgradArgs& a, long long max_tiles, hipStream_t stream);
+struct DgradTile {
+  int rows, cols;
+};
+DgradTile dgrad_tile(int dtype, int mean, int E, int N);
+// max_tiles: row tiles of tile.rows at most, over all experts
+hipError_t launch_dgrad(int dtype, bool dh, DgradTile tile, const DgradArgs& a, long long max_tiles,
+                        hipStream_t stream);
 hipError_t launch_wgrad(int dtype, const WgradArgs& a, hipStream_t stream);
-hipError_t launch_dgrad_bf16(bool dh, int BM, int mean, const DgradArgs& a, long long max_tiles, hipStream_t stream);
-hipError_t launch_dgrad_f32(bool dh, int BM, const DgradArgs& a, long long max_tiles, hipStream_t stream);
+hipError_t launch_dgrad_bf16(bool dh, DgradTile tile, const DgradArgs& a, long long max_tiles, hipStream_t stream);
+hipError_t launch_dgrad_f32(bool dh, DgradTile tile, const DgradArgs& a, long long max_tiles, hipStream_t stream);
 hipError_t launch_wgrad_bf16(const WgradArgs& a, hipStream_t stream);
 hipError_t launch_wgrad_f32(const WgradArgs& a, hipStream_t stream);
 

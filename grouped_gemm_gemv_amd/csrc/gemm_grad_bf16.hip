@@ -8,6 +8,7 @@ using namespace grad;
 using D256 = Tile<TBF16, 256, 256, 2, 4, kPanelK, kRows, 4, 1, true>;
 using D192 = Tile<TBF16, 192, 256, 2, 4, kPanelK, kRows, 5, 1, true>;
 using D256N = Tile<TBF16, 256, 128, 4, 2, kPanelK, kRows, 5, 1, true>;
+using D128 = Tile<TBF16, 128, 128, 2, 2, kPanelK, kRows, 4, 2, false>;
 using D64 = Tile<TBF16, 64, 128, 1, 4, kPanelK, kRows, 4, 3, false>;
 // weight gradients, whatever the rows: with 16 rows per expert, when the stores of
 // the gradients are all there is, 128 x 128 tiles (two workgroups for each compute
@@ -19,6 +20,7 @@ using R64 = Tile<TBF16, 64, 128, 1, 4, kPanelK, kRows, 4, 3, false>;
 template <bool DH>
 hipError_t dgrad_tiles(DgradTile t, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
   if (t.rows == D64::BM) return launch_dgrad_cfg<TBF16, D64, DH>(a, max_tiles, stream);
+  if (t.rows == D128::BM) return launch_dgrad_cfg<TBF16, D128, DH>(a, max_tiles, stream);
   if (t.rows == D192::BM) return launch_dgrad_cfg<TBF16, D192, DH>(a, max_tiles, stream);
   if (t.rows != D256::BM) return hipErrorInvalidValue;
   return t.cols == D256N::BN ? launch_dgrad_cfg<TBF16, D256N, DH>(a, max_tiles, stream)

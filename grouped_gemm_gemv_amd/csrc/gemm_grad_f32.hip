@@ -44,7 +44,9 @@ hipError_t launch_route_wgrad_f32(const RouteWgradArgs& a, int ranges, hipStream
 //    256 x 128: second data gradient at the Mixtral shape 448 against 409 with 512
 //    rows, 537 against 466 with 1024, but 600 against 823 with 2048; 16 experts of
 //    d = 3584, F = 2560 with 1024 rows (more than one round) 93 against 126 and 109
-//    against 162;
+//    against 162.  Up to 96 rows on average 128 x 128 instead, whose 4 wavefronts
+//    need no turns (346 against 411 with 64 rows for each expert; with 128, when
+//    half of the experts take two such tiles, 649 against 478);
 //  * else 192 or 256 rows by 256, whichever takes fewer rounds times rows; 192
 //    only from an eighth less on, as the lower tile does less with each byte it
 //    loads.  256 against 192 rows, second data gradient at the Mixtral shape with 8192
@@ -54,7 +56,7 @@ DgradTile dgrad_tile(int dtype, int mean, int E, int N) {
   if (dtype != 1) return DgradTile{64, 64};
   if (mean <= 48) return DgradTile{64, 128};
   auto tiles = [&](int rows) { return (long long)E * std::max(mean + rows / 2, rows) / rows; };
-  if (tiles(256) * ((N + 127) / 128) <= kComputeUnits) return DgradTile{256, 128};
+  if (tiles(256) * ((N + 127) / 128) <= kComputeUnits) return DgradTile{mean <= 96 ? 128 : 256, 128};
   auto cost = [&](int rows) {
     return (tiles(rows) * ((N + 255) / 256) + kComputeUnits - 1) / kComputeUnits * rows;
   };

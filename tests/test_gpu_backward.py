@@ -240,6 +240,8 @@ FFN_CASES = [
     # tiles of 192 rows, in the first data gradient and in the second
     dict(T=2060, d=64, E=4, k=1, F=9216), dict(T=1300, d=64, E=4, k=1, F=12480, cap=260, layout=1),
     dict(T=1000, d=12288, E=6, k=1, F=64),
+    # of 128
+    dict(T=560, d=320, E=8, k=1, F=448, layout=1), dict(T=1150, d=64, E=12, k=1, F=2688, cap=60, drop=0.1),
 ]
 
 

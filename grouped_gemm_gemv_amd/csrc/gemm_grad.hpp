@@ -1110,22 +1110,24 @@ struct WgradJob {
     }
     constexpr int PART = T::MI < 4 ? T::MI : 4, PARTS = T::MI / PART;  // blocks of 16 columns in a part
     const int ld = M * EB, rows = min(T::BN, N - t.nbase);
+    OutTile<Tr> out[PARTS];
 #pragma unroll
     for (int h = 0; h < PARTS; ++h) {
       const int col = t.mbase + m0 + h * PART * 16;
-      if (col >= M) return false;
-      const OutTile<Tr> out = OutTile<Tr>::matrix(base + (size_t)t.nbase * ld, rows, ld, n0, col, lane, p.blocked16,
-                                                  PART * 16 * EB >= 128);
+      out[h] = OutTile<Tr>::matrix(base + (size_t)t.nbase * ld, col < M ? rows : 0, ld, n0, col, lane, p.blocked16,
+                                   PART * 16 * EB >= 128);
+    }
 #pragma unroll
-      for (int ni = 0; ni < T::NI; ++ni) {
+    for (int ni = 0; ni < T::NI; ++ni)
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h) {
         float v[PART][4];
 #pragma unroll
         for (int mi = 0; mi < PART; ++mi)
 #pragma unroll
           for (int r = 0; r < 4; ++r) v[mi][r] = acc[h * PART + mi][ni][r];
-        out.template put<PART>(ni * 16, v);
+        out[h].template put<PART>(ni * 16, v);
       }
-    }
     return true;
   }
 };

@@ -567,7 +567,7 @@ BackPlan back_plan(const moe_shape_t& s) {
   b.dot = take(4 * R * b.dot_ld);
   b.ffn_ws = o;
   o = b.route_ws + b.ffn_ws;
-  b.dx_perm = take(R * s.d * eb);
+  b.dx_perm = take(R * s.d * 4);  // fp32
   b.backward_ws = o;
   return b;
 }
@@ -588,11 +588,13 @@ moe::GradRows grad_rows(const moe_shape_t& s, const moe_dispatch_t& d) {
 }
 
 // The experts' gradients: rows into expert order, the two data gradients, then
-// every weight gradient in one launch, and the routing weights' gradient.
+// every weight gradient in one launch.  The second also forms the routing
+// weights' gradient.  dx_f32: dx_perm is fp32 whatever the type.
 moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const void* x, const void* dout,
                                   const float* topk_w, const void* w_gate, const void* w_up, const void* w_down,
-                                  const moe_dispatch_t& d, const moe_saved8_t& saved, void* dx_perm, float* dtopk_w,
-                                  void* dw_gate, void* dw_up, void* dw_down, char* ws, hipStream_t st) {
+                                  const moe_dispatch_t& d, const moe_saved8_t& saved, void* dx_perm, bool dx_f32,
+                                  float* dtopk_w, void* dw_gate, void* dw_up, void* dw_down, char* ws,
+                                  hipStream_t st) {
   moe::GatherArgs r{};
   r.rows = grad_rows(s, d);
   r.x = x;
@@ -638,6 +640,7 @@ moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const
   a.K = s.F;
   a.N = s.d;
   a.out = dx_perm;
+  a.out_f32 = dx_f32 ? 1 : 0;
   a.row_of = d.row_of;
   a.entries = s.T * s.k;
   a.dw = dtopk_w;
@@ -693,7 +696,7 @@ moe_status_t enqueue_route_backward(const moe_shape_t& s, const BackPlan& b, con
   fin.ranges = b.ranges;
   fin.steps = b.steps;
   return hip_status(
-      moe::launch_token_backward(s.dtype, dx_perm, row_of, dz, ids, w_router, s.T, s.k, s.d, s.E, dx, fin, st));
+      moe::launch_token_backward(s.dtype, dx_perm, true, row_of, dz, ids, w_router, s.T, s.k, s.d, s.E, dx, fin, st));
 }
 
 }  // namespace
@@ -974,8 +977,8 @@ moe_status_t moe_permute_backward(const moe_shape_t* s, const void* dx_perm, con
   if (st != MOE_OK) return st;
   if (!dx_perm || !dx || !disp || !disp->row_of) return MOE_ERR_NULL_PTR;
   if (!aligned({dx_perm, dx}, 16)) return MOE_ERR_INVALID_ARG;
-  return hip_status(moe::launch_token_backward(s->dtype, dx_perm, disp->row_of, nullptr, nullptr, nullptr, s->T, s->k,
-                                               s->d, s->E, dx, moe::RouteFinish{}, stream));
+  return hip_status(moe::launch_token_backward(s->dtype, dx_perm, false, disp->row_of, nullptr, nullptr, nullptr, s->T,
+                                               s->k, s->d, s->E, dx, moe::RouteFinish{}, stream));
 }
 
 moe_status_t moe_route_backward(const moe_shape_t* s, const void* x, const void* w_router, const int32_t* topk_ids,
@@ -1010,8 +1013,8 @@ moe_status_t moe_grouped_ffn_backward(const moe_shape_t* s, const void* x, const
   if (!aligned({x, dout, w_gate, w_up, w_down, dx_perm, dw_gate, dw_up, dw_down}, 16) ||
       !aligned({topk_w, dtopk_w}, 4) || !aligned({workspace}, kAlign))
     return MOE_ERR_INVALID_ARG;
-  return enqueue_ffn_backward(*s, b, x, dout, topk_w, w_gate, w_up, w_down, *disp, *saved, dx_perm, dtopk_w, dw_gate,
-                              dw_up, dw_down, static_cast<char*>(workspace), stream);
+  return enqueue_ffn_backward(*s, b, x, dout, topk_w, w_gate, w_up, w_down, *disp, *saved, dx_perm, false, dtopk_w,
+                              dw_gate, dw_up, dw_down, static_cast<char*>(workspace), stream);
 }
 
 moe_status_t moe_forward_save8(const moe_shape_t* s, const void* x, const void* w_router, const float* bias,
@@ -1055,11 +1058,11 @@ moe_status_t moe_backward(const moe_shape_t* s, const void* x, const void* w_rou
     return MOE_ERR_INVALID_ARG;
   char* ws = static_cast<char*>(workspace);
   void* dx_perm = ws + b.dx_perm;
-  if ((st = enqueue_ffn_backward(*s, b, x, dout, topk_w, w_gate, w_up, w_down, *disp, *saved, dx_perm, dtopk_w,
+  if ((st = enqueue_ffn_backward(*s, b, x, dout, topk_w, w_gate, w_up, w_down, *disp, *saved, dx_perm, true, dtopk_w,
                                  dw_gate, dw_up, dw_down, ws + b.route_ws, stream)) != MOE_OK)
     return st;
   if (w_router == nullptr)
-    return hip_status(moe::launch_token_backward(s->dtype, dx_perm, disp->row_of, nullptr, nullptr, nullptr, s->T,
+    return hip_status(moe::launch_token_backward(s->dtype, dx_perm, true, disp->row_of, nullptr, nullptr, nullptr, s->T,
                                                  s->k, s->d, s->E, dx, moe::RouteFinish{}, stream));
   return enqueue_route_backward(*s, b, x, w_router, topk_ids, topk_w, dtopk_w, dx_perm, disp->row_of, dx, dw_router,
                                 dbias, ws, stream);

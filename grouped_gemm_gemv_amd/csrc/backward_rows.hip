@@ -109,13 +109,14 @@ __device__ __forceinline__ void route_finish(const RouteFinish& p, int E, int d)
 
 // dx_t = sum_j dx_perm[row_j] + sum_j dz_j w_router[id_j]: fp32, the rows in
 // slot order and then the router's part, one rounding.  Either sum may be
-// absent (row_of or dz null).  The router's rows stay in L2.  `lanes` threads
+// absent (row_of or dz null).  dx_perm has In's type: fp32 inside moe_backward, whose
+// dx is then rounded once.  The router's rows stay in L2.  `lanes` threads
 // (64 or 256) work on a token.  The first fin.blocks workgroups finish the
 // router's other gradients instead (nothing here needs them, and they would be
 // a launch of their own).  Bound by memory: the sum of 8 rows of 3584 bf16 for
 // 4096 tokens takes 39 us (6.6 TB/s); the router's part for 4096 tokens of 2048
 // with 64 experts, 6 chosen, 15 us with the finish (6 us as its own launch).
-template <class Tr>
+template <class Tr, class In>
 __global__ __launch_bounds__(256) void token_backward_kernel(const char* __restrict__ dx_perm,
                                                              const int32_t* __restrict__ row_of,
                                                              const float* __restrict__ dz,
@@ -128,7 +129,7 @@ __global__ __launch_bounds__(256) void token_backward_kernel(const char* __restr
     route_finish<Tr>(fin, E, d);
     return;
   }
-  constexpr int EPC = Tr::EPC;
+  constexpr int EPC = Tr::EPC, PER = EPC / In::EPC;  // 16-byte loads of dx_perm for 16 bytes of dx
   const size_t row_bytes = (size_t)d * sizeof(Elt);
   const int nchunk = d / EPC;
   const int per = 256 / lanes;
@@ -141,20 +142,23 @@ __global__ __launch_bounds__(256) void token_backward_kernel(const char* __restr
     for (int i = 0; i < EPC; ++i) acc[i] = 0.f;
     if (row_of != nullptr) {
       for (int j0 = 0; j0 < k; j0 += kSlots) {
-        uint4 ch[kSlots];
+        uint4 ch[kSlots][PER];
         bool ok[kSlots];
 #pragma unroll
         for (int u = 0; u < kSlots; ++u) {
           const int row = j0 + u < k ? row_of[t * k + j0 + u] : -1;
           ok[u] = row >= 0;
-          ch[u] = ok[u] ? *reinterpret_cast<const uint4*>(dx_perm + (size_t)row * row_bytes + o)
-                        : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < PER; ++i)
+            ch[u][i] = ok[u] ? *reinterpret_cast<const uint4*>(dx_perm + (size_t)row * row_bytes * PER + o * PER + i * 16)
+                             : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int u = 0; u < kSlots; ++u) {
           if (!ok[u]) continue;
           float v[EPC];
-          widen<Tr>(ch[u], v);
+#pragma unroll
+          for (int i = 0; i < PER; ++i) widen<In>(ch[u][i], v + i * In::EPC);
 #pragma unroll
           for (int i = 0; i < EPC; ++i) acc[i] += v[i];
         }
@@ -277,21 +281,23 @@ hipError_t launch_combine_backward(int dtype, const void* dout, const void* y, c
   return hipGetLastError();
 }
 
-hipError_t launch_token_backward(int dtype, const void* dx_perm, const int32_t* row_of, const float* dz,
+hipError_t launch_token_backward(int dtype, const void* dx_perm, bool f32, const int32_t* row_of, const float* dz,
                                  const int32_t* ids, const void* w_router, int T, int k, int d, int E, void* dx,
                                  RouteFinish fin, hipStream_t stream) {
   const int lanes = row_threads(dtype, d), per = 256 / lanes;
   fin.sum_blocks = fin.part != nullptr ? (int)(((int64_t)E * d / 4 + 255) / 256) : 0;
   fin.blocks = fin.sum_blocks + (fin.dbias != nullptr ? E : 0);
   const dim3 grid((unsigned)fin.blocks + ((unsigned)T + per - 1) / per), block(256);
-  if (dtype == 1)
-    hipLaunchKernelGGL(token_backward_kernel<TBF16>, grid, block, 0, stream, static_cast<const char*>(dx_perm),
-                       row_of, dz, ids, static_cast<const char*>(w_router), T, k, d, E, lanes,
-                       static_cast<char*>(dx), fin);
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, static_cast<const char*>(dx_perm), row_of, dz, ids,
+                       static_cast<const char*>(w_router), T, k, d, E, lanes, static_cast<char*>(dx), fin);
+  };
+  if (dtype != 1)
+    launch(token_backward_kernel<TF32, TF32>);
+  else if (f32)
+    launch(token_backward_kernel<TBF16, TF32>);
   else
-    hipLaunchKernelGGL(token_backward_kernel<TF32>, grid, block, 0, stream, static_cast<const char*>(dx_perm),
-                       row_of, dz, ids, static_cast<const char*>(w_router), T, k, d, E, lanes,
-                       static_cast<char*>(dx), fin);
+    launch(token_backward_kernel<TBF16, TBF16>);
   return hipGetLastError();
 }
 

@@ -735,7 +735,9 @@ __device__ __forceinline__ Units my_units(int total) {
 
 // out tile = act rows x weights (DH: with the SwiGLU's gradient in the epilogue).
 // A unit's steps go over K, a1 x b1 behind a0 x b0 into the same accumulators.
-template <class Tr, class T, bool DH>
+// Out: type of the results (a choice at run time cost the main loop 8 %, in
+// registers).
+template <class Tr, class T, bool DH, class Out>
 struct DgradJob {
   static constexpr int EB = T::EB;
   struct Info {
@@ -850,10 +852,11 @@ struct DgradJob {
     if (n0 >= p.N) return false;
     const int m0 = T::m_first(wave);
     if constexpr (!DH) {
-      const int ld = p.N * EB;
-      const OutTile<Tr> out =
-          OutTile<Tr>::matrix(static_cast<const char*>(p.out) + (size_t)t.row0 * ld, t.rows, ld, m0, n0, lane, 0,
-                              T::TN * EB >= 128);
+      constexpr int OB = sizeof(typename Out::T);
+      const int ld = p.N * OB;
+      const OutTile<Out> out =
+          OutTile<Out>::matrix(static_cast<const char*>(p.out) + (size_t)t.row0 * ld, t.rows, ld, m0, n0, lane, 0,
+                               T::TN * OB >= 128);
 #pragma unroll
       for (int mi = 0; mi < T::MI; ++mi) {
         float v[T::NI][4];
@@ -925,7 +928,7 @@ struct DgradJob {
   const int lane = threadIdx.x & 63;                                                                   \
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)
 
-template <class Tr, class T, bool DH>
+template <class Tr, class T, bool DH, class Out>
 __global__ __launch_bounds__(T::NTH) void dgrad_kernel(DgradArgs p) {
   MOE_GRAD_RING;
   __shared__ ExpertTable tab;
@@ -942,9 +945,9 @@ __global__ __launch_bounds__(T::NTH) void dgrad_kernel(DgradArgs p) {
     }
   }
   fill_table<T::BM>(p.rows, tab);
-  DgradJob<Tr, T, DH> job(p, tab);
+  DgradJob<Tr, T, DH, Out> job(p, tab);
   const Units u = my_units(job.units());
-  typename T::template Runner<DgradJob<Tr, T, DH>>(job, ring, ring_at, u.first, u.stride, u.end, lane, wave).run();
+  typename T::template Runner<DgradJob<Tr, T, DH, Out>>(job, ring, ring_at, u.first, u.stride, u.end, lane, wave).run();
 }
 
 // ---- weight gradients ---------------------------------------------------------
@@ -1224,7 +1227,13 @@ hipError_t launch_dgrad_cfg(const DgradArgs& a, long long max_tiles, hipStream_t
   const long long units = max_tiles * ((a.N + T::BN - 1) / T::BN);
   if (units == 0) return hipSuccess;
   if (units > 0x7fffff00LL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((dgrad_kernel<Tr, T, DH>), dim3(grid_of<T>(units)), dim3(T::NTH), 0, stream, a);
+  if constexpr (!DH && sizeof(typename Tr::T) == 2) {
+    if (a.out_f32 != 0) {
+      hipLaunchKernelGGL((dgrad_kernel<Tr, T, DH, TF32>), dim3(grid_of<T>(units)), dim3(T::NTH), 0, stream, a);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((dgrad_kernel<Tr, T, DH, Tr>), dim3(grid_of<T>(units)), dim3(T::NTH), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -176,8 +176,9 @@ struct RouteFinish {
 };
 
 // dx[t] = sum_j dx_perm[row_of[t k + j]], plus, with dz set, sum_j dz[t k + j]
-// w_router[ids[t k + j]] (dx_perm may then be null); and fin's work.
-hipError_t launch_token_backward(int dtype, const void* dx_perm, const int32_t* row_of, const float* dz,
+// w_router[ids[t k + j]] (dx_perm may then be null); and fin's work.  f32: dx_perm
+// is fp32 whatever the type.
+hipError_t launch_token_backward(int dtype, const void* dx_perm, bool f32, const int32_t* row_of, const float* dz,
                                  const int32_t* ids, const void* w_router, int T, int k, int d, int E, void* dx,
                                  RouteFinish fin, hipStream_t stream);
 
@@ -222,7 +223,8 @@ struct DgradArgs {
   const void* b0;  // [E][K][N]
   const void* b1;
   int K, N, blocked16;
-  void* out;  // [R][N]
+  void* out;   // [R][N]
+  int out_f32;  // whether out is fp32 whatever the type
   // with the SwiGLU's gradient (out unused): a0 = dout, K = d, N = F
   const float* wrow;
   const int8_t* g8;

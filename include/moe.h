@@ -429,7 +429,8 @@ moe_status_t moe_forward_save8(const moe_shape_t* s, const void* x, const void* 
  * weights, topk_ids and topk_w: moe_grouped_ffn_backward, then the router's
  * gradient (w_router not NULL) and
  *   dx[t] = sum_j dx_perm[row_of[t k + j]] + sum_j dz[t k + j] w_router[topk_ids[t,j]]
- * in fp32 with one rounding.  dout, dx [T,d]; dtopk_w [T,k] is always written.
+ * in fp32 with one rounding (dx_perm is kept in fp32 here, in the workspace).
+ * dout, dx [T,d]; dtopk_w [T,k] is always written.
  * With w_router NULL (the routing is the caller's) dw_router and dbias must be
  * NULL; else dw_router is required and dbias may be NULL.  workspace of >=
  * backward_ws_bytes (256-byte aligned). */

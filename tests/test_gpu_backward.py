@@ -338,6 +338,7 @@ def _kit(c):
     dict(T=1, d=64, E=8, k=2, F=128), dict(T=12, d=256, E=8, k=2, F=192), dict(T=200, d=256, E=8, k=2, F=320),
     dict(T=300, d=128, E=16, k=4, F=192, cap=40, layout=1), dict(T=64, d=128, E=8, k=2, F=256, dtype="f32"),
     dict(T=900, d=128, E=2, k=1, F=192),
+    dict(T=1000, d=12288, E=6, k=1, F=64), dict(T=2060, d=12288, E=4, k=1, F=64),  # the tall tiles, into fp32
 ], ids=str)
 def test_layer_forward_then_backward(kw, router):
     """out is bitwise moe_forward's; the gradients follow, in float64, from the codes that the forward pass left."""
@@ -373,10 +374,10 @@ def test_layer_forward_then_backward(kw, router):
         close(n, c.unweight(o[n]), *want[n])
     dw, e_dw = (z.reshape(c.T, c.k) for z in want["dw"])
     close("dw", host64(o["dw"]), dw, e_dw)
-    # dx: rows of dx_perm within their bound, summed and rounded; the router's part from the GPU's own dw
+    # dx: rows of dx_perm, here without their own rounding, summed and rounded; the router's part from the GPU's own dw
     dx, e = B.permute_backward(want["dx_perm"][0], row_of, c.T, c.k, c.dtype)
     for f, r in enumerate(row_of):
-        e[f // c.k] += want["dx_perm"][1][r]
+        e[f // c.k] += want["dx_perm"][1][r] - B.U[c.dtype] * np.abs(want["dx_perm"][0][r])
     if router:
         (dxr, er), (dwr, ew), (db, eb) = B.route_backward(x, host64(c.wr), ids, w, host64(o["dw"]), c.dtype)
         e += er + B.U[c.dtype] * np.abs(dxr) + 4 * c.k * B.U32 * (np.abs(dx) + np.abs(dxr))

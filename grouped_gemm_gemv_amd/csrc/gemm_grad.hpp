@@ -20,13 +20,16 @@
 // WM x WN wavefronts of TM x TN each.  N is the MFMA "A" operand, so a lane ends
 // with 4 consecutive n of one m, as the outputs lie in memory.
 //
-// Activations between the products (x and dout in expert order, dg, du, w_r h)
-// are kept in panels: [columns of 64 bytes][R rows][64 bytes].  A K step of the
-// data gradients (64 bytes of every row of a tile) and 16 K rows of 64 bytes of
-// the weight gradients are then both one run of memory, whatever the width of
-// a row: with rows of 28 KB, a multiple of 4 KB apart, the second data gradient
-// took 2049 instead of 1722 us (8192 rows, d = 4096, F = 14336).  Weights are
-// read as the caller keeps them.
+// Activations between the products (dout in expert order, dg, du, w_r h) are
+// kept in panels: [columns of 64 bytes][R rows][64 bytes].  A K step of the data
+// gradients (64 bytes of every row of a tile) and 16 K rows of 64 bytes of the
+// weight gradients are then both one run of memory, whatever the width of a
+// row: with rows of 28 KB, a multiple of 4 KB apart, the second data gradient
+// took 2049 instead of 1722 us (8192 rows, d = 4096, F = 14336).  The weight
+// gradients' other operand, x and dout, is turned once by the gather in front
+// (gather_backward_kernel) and read at the full rate of LDS, twice that of the
+// transposing read (2769 instead of 2923 us).  Weights are read as the caller
+// keeps them.
 //
 // A K step is 64 bytes of a K-contiguous row (32 bf16 or 16 fp32), so each
 // operand takes 64 bytes of LDS per tile row or column whatever its
@@ -41,13 +44,11 @@
 // multiplied and its results are stored.
 //
 // What bounds them, at d = 4096, F = 14336 with 8 experts (bf16):
-//  * many rows: the matrix cores.  8192 rows take 940 us (first data gradient,
-//    1.02 PF/s), 1800 (second, 1.07) and 2980 (weight gradients, 0.97), where a
+//  * many rows: the matrix cores.  8192 rows take 926 us (first data gradient,
+//    1.04 PF/s), 1617 (second, 1.19) and 2836 (weight gradients, 1.02), where a
 //    library product of 8192 cubed reaches 1.24, or 1.10 with a transposed
-//    operand.  The second loses a quarter of its last round of tiles (2.3 tiles
-//    for each workgroup); a step of the weight gradients takes 1640 cycles, of
-//    which 1024 are MFMAs, because both operands come through the transposing
-//    LDS read, at half the rate of the plain one;
+//    operand; the clock falls to 2.0 GHz.  What is left: the codes and the
+//    epilogue of the first, the stores between the tiles of the last;
 //  * few rows: memory.  32 rows take 181 and 290 us (0.94 and 1.88 GB of
 //    weights, 5.2 and 6.5 TB/s) and 610 (2.8 GB of weight gradients, 4.6 TB/s
 //    where a fill reaches 6.8: a tile's rows are 512-byte pieces).
@@ -959,7 +960,8 @@ __global__ __launch_bounds__(T::NTH) void dgrad_kernel(DgradArgs p) {
 // in the layout and with the reads of an operand in panels, so that what a
 // lane reads there are the 16 bytes it writes.  dout goes to panels as well, for
 // the first data gradient.  x_steps and dout_steps may be null: not wanted.
-// Bound by memory.
+// Bound by memory: 54 us for 8192 rows of 4096 bf16 (336 MB read and written,
+// 6.2 TB/s); by latency for the smallest, 4 us.
 template <class Tr, class T>
 __global__ __launch_bounds__(256) void gather_backward_kernel(GatherArgs p) {
   constexpr int KS = T::KS, EB = T::EB, LD = KS / 16;  // 16-byte loads of 256 columns' bytes per thread and tensor

@@ -516,7 +516,7 @@ moe_status_t forward_impl(const moe_shape_t* s, const void* x, const void* w_rou
 struct BackPlan {
   size_t saved_bytes, saved_up, saved_gate_exp, saved_up_exp;
   int steps, ranges, range_steps;  // K steps of the router's weight gradient, its token ranges, steps of one
-  size_t dz, dense_hi, dense_lo, sums, part, route_ws;
+  size_t dz, dense_hi, dense_lo, sums, taken, part, route_ws;
   int mean, dot_ld;
   int64_t k_steps;  // of the weight gradients, at most
   size_t x_steps, dout_steps, dout_perm, dg, du, hw, wrow, dot, ffn_ws;  // from the start of the experts' part
@@ -550,6 +550,7 @@ BackPlan back_plan(const moe_shape_t& s) {
   b.dense_hi = take((size_t)steps * s.E * 64);
   b.dense_lo = s.dtype == MOE_BF16 ? take((size_t)steps * s.E * 64) : 0;
   b.sums = take(4 * (size_t)steps * s.E);
+  b.taken = take(4 * (size_t)steps);
   b.part = take(4 * (size_t)b.ranges * s.E * s.d);
   b.route_ws = o;
   b.mean = (int)mean_rows(s);
@@ -674,11 +675,14 @@ moe_status_t enqueue_route_backward(const moe_shape_t& s, const BackPlan& b, con
   float* dz = reinterpret_cast<float*>(ws + b.dz);
   char* lo = s.dtype == MOE_BF16 ? ws + b.dense_lo : nullptr;
   float* sums = reinterpret_cast<float*>(ws + b.sums);
-  if (moe::launch_route_dz(s.dtype, ids, w, dw, s.T, s.k, s.E, dz, ws + b.dense_hi, lo, sums, st) != hipSuccess)
+  unsigned* taken = reinterpret_cast<unsigned*>(ws + b.taken);
+  if (moe::launch_route_dz(s.dtype, ids, w, dw, s.T, s.k, s.E, dz, ws + b.dense_hi, lo, sums, taken, st) !=
+      hipSuccess)
     return MOE_ERR_HIP;
   moe::RouteWgradArgs a{};
   a.dz_hi = ws + b.dense_hi;
   a.dz_lo = lo;
+  a.taken = taken;
   a.x = x;
   a.part = reinterpret_cast<float*>(ws + b.part);
   a.T = s.T;

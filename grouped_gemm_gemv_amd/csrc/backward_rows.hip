@@ -201,12 +201,14 @@ template <class Tr>
 __global__ __launch_bounds__(256) void route_dz_kernel(const int32_t* __restrict__ ids, const float* __restrict__ w,
                                                        const float* __restrict__ dw, int T, int k, int E,
                                                        float* __restrict__ dz, typename Tr::T* __restrict__ hi,
-                                                       typename Tr::T* __restrict__ lo, float* __restrict__ sums) {
+                                                       typename Tr::T* __restrict__ lo, float* __restrict__ sums,
+                                                       unsigned* __restrict__ taken) {
   constexpr int KS = 64 / sizeof(typename Tr::T);
   extern __shared__ float dense[];  // [E][KS]
   for (int i = threadIdx.x; i < E * KS; i += 256) dense[i] = 0.f;
   __syncthreads();
   const int64_t t = (int64_t)blockIdx.x * KS + threadIdx.x;
+  bool any = false;
   if (threadIdx.x < KS && t < T) {
     const float* wt = w + t * k;
     const float* dt = dw + t * k;
@@ -216,9 +218,11 @@ __global__ __launch_bounds__(256) void route_dz_kernel(const int32_t* __restrict
       const float z = wt[j] * (dt[j] - s);
       dz[t * k + j] = z;
       const int id = ids[t * k + j];
-      if (id >= 0 && id < E) dense[id * KS + threadIdx.x] += z;
+      if (id >= 0 && id < E) dense[id * KS + threadIdx.x] += z, any = true;
     }
   }
+  const uint64_t bits = __ballot(any);
+  if (threadIdx.x == 0) taken[blockIdx.x] = (unsigned)bits;
   __syncthreads();
   const size_t base = (size_t)blockIdx.x * E * KS;
   for (int i = threadIdx.x; i < E * KS; i += 256) {
@@ -302,16 +306,17 @@ hipError_t launch_token_backward(int dtype, const void* dx_perm, bool f32, const
 }
 
 hipError_t launch_route_dz(int dtype, const int32_t* ids, const float* w, const float* dw, int T, int k, int E,
-                           float* dz, void* dense_hi, void* dense_lo, float* sums, hipStream_t stream) {
+                           float* dz, void* dense_hi, void* dense_lo, float* sums, unsigned* taken,
+                           hipStream_t stream) {
   const int KS = dtype == 1 ? 32 : 16;
   const dim3 grid((unsigned)(((int64_t)T + KS - 1) / KS)), block(256);
   const size_t lds = (size_t)E * KS * sizeof(float);
   if (dtype == 1)
     hipLaunchKernelGGL(route_dz_kernel<TBF16>, grid, block, lds, stream, ids, w, dw, T, k, E, dz,
-                       static_cast<uint16_t*>(dense_hi), static_cast<uint16_t*>(dense_lo), sums);
+                       static_cast<uint16_t*>(dense_hi), static_cast<uint16_t*>(dense_lo), sums, taken);
   else
     hipLaunchKernelGGL(route_dz_kernel<TF32>, grid, block, lds, stream, ids, w, dw, T, k, E, dz,
-                       static_cast<float*>(dense_hi), static_cast<float*>(nullptr), sums);
+                       static_cast<float*>(dense_hi), static_cast<float*>(nullptr), sums, taken);
   return hipGetLastError();
 }
 

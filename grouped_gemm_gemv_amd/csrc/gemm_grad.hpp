@@ -342,6 +342,8 @@ struct Tile {
       return ((s >> 2) | (s & 3) << 2) * 64 + (c << 4);
     }
   }
+  // kRows: K row of this lane's slot in load q.
+  __device__ __forceinline__ static int k_row(int q, int lane) { return (q * 64 + lane) / (BN * EB / 16); }
   // kRows: byte offset inside the step of this lane's slot in load q, for a tile
   // from column col0 on of rows of `cols` elements (ld bytes each).  blocked16: the
   // rows are in groups of 16, each stored as 1024-byte blocks of 64 bytes from
@@ -423,6 +425,7 @@ struct Tile {
     int ls, cs;       // stages of the next load and of the next step
     Info lt, ct;      // the unit being loaded, the unit being multiplied
     Step ld;          // the next loads
+    unsigned mask;    // MASKED: which of their K rows are read, a bit each; the others are zeros
     int stores;       // steps left for which this wavefront's ST stores of the unit before may be in flight
     int moff[LM], noff[LN];
     uint4 nf[NI], mf[MI];
@@ -445,6 +448,7 @@ struct Tile {
           for (int i = 0; i < LN; ++i) noff[i] = job.rows_offset(lt, nq(wave, i), lane);
         }
       }
+      if constexpr (Job::MASKED) mask = job.mask(0);
       // (selects, not an else branch: stores of two branches merged into one
       // through a pointer would keep the state in scratch memory)
       lt.steps = in ? lt.steps : 0;
@@ -458,6 +462,7 @@ struct Tile {
       ls = ls == S - 1 ? 0 : ls + 1;
       ++lj;
       job.next(lt, lj, ld);
+      if constexpr (Job::MASKED) mask = job.mask(lj);
     }
     __device__ __forceinline__ void turn() {
       if (lj == lpad) {
@@ -484,7 +489,8 @@ struct Tile {
         if (i < LM)
           load_lds(m, moff[i < LM ? i : 0], at + mq(wave, i) * 1024);
         else
-          load_lds(NOP == kPanelR ? panel_desc(ld.n, ld.nbytes, in, lt.npanels) : n, noff[in],
+          load_lds(NOP == kPanelR ? panel_desc(ld.n, ld.nbytes, in, lt.npanels) : n,
+                   !Job::MASKED || (mask >> k_row(nq(wave, in), lane) & 1) != 0 ? noff[in] : kOutside,
                    at + MBYTES + nq(wave, in) * 1024);
         between(i);
       }
@@ -741,6 +747,7 @@ __device__ __forceinline__ Units my_units(int total) {
 template <class Tr, class T, bool DH, class Out>
 struct DgradJob {
   static constexpr int EB = T::EB;
+  static constexpr bool MASKED = false;
   struct Info {
     int steps, row0, rows, nbase, e;
     const char *a0, *a1, *b0, *b1;  // operands of the tile's rows and expert
@@ -1033,6 +1040,7 @@ __global__ __launch_bounds__(256) void gather_backward_kernel(GatherArgs p) {
 template <class Tr, class T>
 struct WgradJob {
   static constexpr int EB = T::EB;
+  static constexpr bool MASKED = false;
   struct Info {
     int steps, rows, steps0, e, w, mbase, nbase, swap;
     int n0, n1;
@@ -1152,12 +1160,15 @@ __global__ __launch_bounds__(T::NTH) void wgrad_kernel(WgradArgs p) {
 // part[z][e][i] = sum over tokens t of range z of dz[e][t] x[t][i] (fp32 partial
 // sums).  dz is dense with zeros where expert e did not take token t, laid out
 // by K step: [step][E][64 bytes].  bf16 carries it as two terms (high and low
-// part), which keeps 16 bits of its significand.  One tile per workgroup, over
-// enough token ranges for two on each compute unit: 12.6 us for 4096 tokens of
+// part), which keeps 16 bits of its significand.  A token with experts and a
+// NaN or an infinity in x reaches all of them, the zeros being multiplied too.
+// One tile per workgroup, over
+// enough token ranges for two on each compute unit: 14 us for 4096 tokens of
 // 2048 bf16 and 64 experts, most of it the latency of a range's 8 to 16 steps.
 template <class Tr, class T>
 struct RouteJob {
   static constexpr int EB = T::EB;
+  static constexpr bool MASKED = true;
   struct Info {
     int steps, rows;
     size_t panel;
@@ -1172,6 +1183,18 @@ struct RouteJob {
   __device__ __forceinline__ Info decode(int) const { return Info{per * (p.dz_lo != nullptr ? 2 : 1), rows, 0, 0}; }
   __device__ __forceinline__ int rows_offset(const Info&, int q, int lane) const {
     return T::rows_offset(q, lane, nbase, p.d, p.d * EB, 0);
+  }
+  // Tokens of step j that any expert took.  The rows of x of the others, which
+  // may hold anything, are not read: zero times a NaN there would reach every
+  // expert.  (A scalar load: the wait for a vector load would drain the ring.)
+  __device__ __forceinline__ unsigned mask(int j) const {
+#ifdef __HIP_DEVICE_COMPILE__
+    const bool second = j >= per;
+    const int q = j < per * (p.dz_lo != nullptr ? 2 : 1) ? j0 + (second ? j - per : j) : 0;
+    return ((const __attribute__((address_space(4))) unsigned*)(uintptr_t)p.taken)[q];
+#else
+    return 0;
+#endif
   }
   __device__ __forceinline__ Step first(const Info& t) const {
     Step s{};

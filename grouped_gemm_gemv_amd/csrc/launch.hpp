@@ -184,14 +184,17 @@ hipError_t launch_token_backward(int dtype, const void* dx_perm, bool f32, const
 
 // dz_f = w_f (dw_f - sum_i w_i dw_i), and its dense form by K step for the
 // router's weight gradient (hi, and with bf16 lo: [ceil(T / KS)][E][KS]) with
-// its sums over each step's tokens ([ceil(T / KS)][E]).
+// its sums over each step's tokens ([ceil(T / KS)][E]) and which of these have an
+// expert at all ([ceil(T / KS)], a bit each).
 hipError_t launch_route_dz(int dtype, const int32_t* ids, const float* w, const float* dw, int T, int k, int E,
-                           float* dz, void* dense_hi, void* dense_lo, float* sums, hipStream_t stream);
+                           float* dz, void* dense_hi, void* dense_lo, float* sums, unsigned* taken,
+                           hipStream_t stream);
 
 struct RouteWgradArgs {
   const void* dz_hi;  // [steps of all tokens][E][64 bytes]
   const void* dz_lo;  // the same, or null (fp32)
   const void* x;      // [T][d]
+  const unsigned* taken;  // [steps of all tokens]: which of a step's tokens have an expert, a bit each
   float* part;        // [ranges][E][d]
   int T, E, d;
   int steps;          // K steps of one range of tokens

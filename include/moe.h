@@ -334,7 +334,10 @@ moe_status_t moe_forward_fp8(const moe_shape_t* s, const void* x, const void* w_
  * aligned (topk arrays, their gradients, dbias and counts 4-byte; else
  * MOE_ERR_INVALID_ARG); output buffers must not overlap inputs.  Rows that hold no
  * token are neither read nor written.  Entries without a row (an id outside
- * [0, E)) get gradient 0 for their routing weight and contribute nothing. */
+ * [0, E)) get gradient 0 for their routing weight and contribute nothing; of a
+ * token without any (padding) x and dout are not read and dx is 0.  A NaN or an
+ * infinity in x or dout of a token with rows reaches that token's dx and the
+ * gradients of its experts, and in x the router's gradients of every expert. */
 
 /* Sizes for a shape (host values). */
 typedef struct moe_backward_sizes {

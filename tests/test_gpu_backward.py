@@ -275,6 +275,45 @@ def test_grouped_ffn_backward(kw):
         assert np.array_equal(bits(o[n]), bits(again[n])), n
 
 
+@pytest.mark.parametrize("kw", [
+    dict(T=100, d=192, E=8, k=1, F=320), dict(T=300, d=64, E=4, k=2, F=192, cap=90, layout=1),
+    dict(T=90, d=64, E=4, k=2, F=128, dtype="f32"), dict(T=2060, d=64, E=4, k=1, F=9216),
+], ids=str)
+def test_padding_may_hold_anything(kw):
+    """Tokens without an expert: whatever x, dout and the weights hold there, every gradient is bitwise the same."""
+    _need_gpu()
+    print(f"\n[gpu] padding {kw}", flush=True)
+    c = Case(**kw, drop=0.0)
+    pad = np.zeros(c.T, dtype=bool)
+    pad[[1, 2, c.T // 2]] = True
+    pad[-7:] = True
+    m = torch.from_numpy(pad).cuda()
+    c.ids[m] = -1
+    M = c.M
+    xp = torch.empty(c.R, c.d, dtype=c.dt, device="cuda")
+    M.moe_permute(c.shape, c.x, c.ids, c.disp, xp, M.workspace(M.query(c.shape).permute_ws_bytes))
+    saved, _, _ = c.saved()
+    ws = M.workspace(M.backward_workspace_size(c.shape))
+    wts = [c.weight(w) for w in (c.wg, c.wu, c.wd)]
+    dw_in = torch.randn(c.T, c.k, device="cuda")
+    runs = []
+    for v in (0.0, float("nan"), float("inf")):
+        c.x[m], c.dout[m], c.w[m], dw_in[m] = v, v, v, v
+        o = _ffn(c, saved)
+        r = {"dx": c.empty(c.T, c.d), "dwr": c.empty(c.E, c.d), "db": c.empty(c.E, dt=torch.float32)}
+        M.moe_route_backward(c.shape, c.x, c.wr, c.ids, c.w, dw_in, r["dx"], r["dwr"], r["db"], ws)
+        a = {"dx": c.empty(c.T, c.d), "dw": c.empty(c.T, c.k, dt=torch.float32), "dwr": c.empty(c.E, c.d),
+             "db": c.empty(c.E, dt=torch.float32), **{n: torch.empty_like(o[n]) for n in ("dwg", "dwu", "dwd")}}
+        M.moe_backward(c.shape, c.x, c.wr, c.ids, c.w, *wts, c.disp, saved, c.dout, a["dx"], a["dw"], a["dwr"],
+                       a["db"], a["dwg"], a["dwu"], a["dwd"], ws)
+        for n in ("dwr", "db", "dx"):
+            assert torch.isfinite(r[n]).all() and torch.isfinite(a[n]).all(), (n, v)
+        assert (r["dx"][m] == 0).all() and (a["dx"][m] == 0).all() and (a["dw"][m] == 0).all()
+        runs.append([bits(t) for t in (*o.values(), *r.values(), *a.values())])
+    for other in runs[1:]:
+        assert all(np.array_equal(p, q) for p, q in zip(runs[0], other))
+
+
 def test_gradients_that_are_not_asked_for():
     _need_gpu()
     c = Case(T=60, d=128, E=4, k=2, F=192)

@@ -1160,11 +1160,11 @@ __global__ __launch_bounds__(T::NTH) void wgrad_kernel(WgradArgs p) {
 // part[z][e][i] = sum over tokens t of range z of dz[e][t] x[t][i] (fp32 partial
 // sums).  dz is dense with zeros where expert e did not take token t, laid out
 // by K step: [step][E][64 bytes].  bf16 carries it as two terms (high and low
-// part), which keeps 16 bits of its significand.  A token with experts and a
-// NaN or an infinity in x reaches all of them, the zeros being multiplied too.
-// One tile per workgroup, over
-// enough token ranges for two on each compute unit: 14 us for 4096 tokens of
-// 2048 bf16 and 64 experts, most of it the latency of a range's 8 to 16 steps.
+// part), which keeps 16 bits of its significand.  A NaN or an infinity in x of a
+// token with experts reaches all of them, the zeros being multiplied too.  One
+// tile per workgroup, over enough token ranges for two on each compute unit: 14 us
+// for 4096 tokens of 2048 bf16 and 64 experts, most of it the latency of a
+// range's 8 to 16 steps.
 template <class Tr, class T>
 struct RouteJob {
   static constexpr int EB = T::EB;

@@ -630,7 +630,7 @@ moe_status_t enqueue_ffn_backward(const moe_shape_t& s, const BackPlan& b, const
   a.dot = reinterpret_cast<float*>(ws + b.dot);
   a.dot_ld = b.dot_ld;
   auto dgrad = [&](bool dh) {
-    const moe::DgradTile t = moe::dgrad_tile(s.dtype, b.mean, s.E, a.N);
+    const moe::DgradTile t = moe::dgrad_tile(s.dtype, dh, b.mean, s.E, a.N);
     return moe::launch_dgrad(s.dtype, dh, t, a, pass_max_tiles(s, t.rows, 0) + pass_max_tiles(s, t.rows, 1), st);
   };
   if (dgrad(true) != hipSuccess) return MOE_ERR_HIP;

@@ -7,10 +7,12 @@ using namespace grad;
 // fp32 MFMAs run at a sixteenth of the bf16 rate, so small tiles keep up (a ring
 // of 8 stages gained nothing at the tiny layer, 64 tokens of 128 columns)
 using D64 = Tile<TF32, 64, 64, 2, 2, kPanelK, kRows, 4, 4, false>;
+using D32 = Tile<TF32, 32, 64, 1, 4, kPanelK, kRows, 4, 4, false>;
 using W64 = Tile<TF32, 64, 64, 2, 2, kSteps, kPanelR, 4, 4, false>;
 }  // namespace
 
 hipError_t launch_dgrad_f32(bool dh, DgradTile tile, const DgradArgs& a, long long max_tiles, hipStream_t stream) {
+  if (tile.rows == D32::BM && !dh) return launch_dgrad_cfg<TF32, D32, false>(a, max_tiles, stream);
   if (tile.rows != D64::BM) return hipErrorInvalidValue;
   return dh ? launch_dgrad_cfg<TF32, D64, true>(a, max_tiles, stream)
             : launch_dgrad_cfg<TF32, D64, false>(a, max_tiles, stream);
@@ -31,7 +33,11 @@ hipError_t launch_route_wgrad_f32(const RouteWgradArgs& a, int ranges, hipStream
   return hipGetLastError();
 }
 
-// The tile of a data gradient.  bf16, us of kernel time on each side:
+// The tile of a data gradient.  fp32: 64 x 64, but the second one (dh false) of up
+// to 32 rows on average 32 x 64 with the four wavefronts side by side, each with
+// half the MFMAs in a step: 246 against 334 us for 39 experts of d = 448, F = 6528
+// with 7 rows, 13.7 against 14.6 for 8 of d = 128, F = 256 with 16, 76.3 against 76.5
+// for 8 of d = 1024, F = 2048 with 25.  bf16, us of kernel time on each side:
 //  * 64 x 128 (three workgroups for each compute unit) where an expert's rows fit
 //    one such tile; past 48 rows on average many do not, and their weights would
 //    be read twice.  Both data gradients, 64- against 256-row tiles: the Mixtral
@@ -52,8 +58,8 @@ hipError_t launch_route_wgrad_f32(const RouteWgradArgs& a, int ranges, hipStream
 //    loads.  256 against 192 rows, second data gradient at the Mixtral shape with 8192
 //    rows (3 rounds either way) 1787 against 1611, with 4096 1133 against 1019;
 //    first with 8192 rows (8 rounds against 11) 931 against 1018.
-DgradTile dgrad_tile(int dtype, int mean, int E, int N) {
-  if (dtype != 1) return DgradTile{64, 64};
+DgradTile dgrad_tile(int dtype, bool dh, int mean, int E, int N) {
+  if (dtype != 1) return DgradTile{!dh && mean <= 32 ? 32 : 64, 64};
   if (mean <= 48) return DgradTile{64, 128};
   auto tiles = [&](int rows) { return (long long)E * std::max(mean + rows / 2, rows) / rows; };
   if (tiles(256) * ((N + 127) / 128) <= kComputeUnits) return DgradTile{mean <= 96 ? 128 : 256, 128};

@@ -299,12 +299,12 @@ hipError_t launch_gather_backward_bf16(const GatherArgs& a, long long max_steps,
 hipError_t launch_gather_backward_f32(const GatherArgs& a, long long max_steps, hipStream_t stream);
 
 // Columns of one partial sum of <D, h>, by the mean row count of an expert, and
-// the tile of a data gradient with N columns.
+// the tile of the first (dh) or second data gradient with N columns.
 int dgrad_dot_cols(int dtype, int mean);
 struct DgradTile {
   int rows, cols;
 };
-DgradTile dgrad_tile(int dtype, int mean, int E, int N);
+DgradTile dgrad_tile(int dtype, bool dh, int mean, int E, int N);
 // max_tiles: row tiles of tile.rows at most, over all experts
 hipError_t launch_dgrad(int dtype, bool dh, DgradTile tile, const DgradArgs& a, long long max_tiles,
                         hipStream_t stream);

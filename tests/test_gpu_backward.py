@@ -237,6 +237,7 @@ FFN_CASES = [
     dict(T=1500, d=64, E=8, k=1, F=4096, dtype="f32"),
     dict(T=2060, d=12288, E=4, k=1, F=64),
     dict(T=600, d=192, E=16, k=1, F=1536, cap=30, layout=1),
+    dict(T=160, d=8192, E=16, k=1, F=64, dtype="f32"),
     # tiles of 192 rows, in the first data gradient and in the second
     dict(T=2060, d=64, E=4, k=1, F=9216), dict(T=1300, d=64, E=4, k=1, F=12480, cap=260, layout=1),
     dict(T=1000, d=12288, E=6, k=1, F=64),

@@ -165,21 +165,34 @@ def moe_ffn_gate_up_fp8(shape: Shape, x, w_gate, w_up, s_gate, s_up, disp: Dispa
         pass_idx, _p(h), _stream(stream)))
 
 
+def _down_disp(disp: Dispatch, shape: Shape):
+    """The C dispatch of a down GEMM call.  Where the call splits K, its partial sums [2][R][d] go to the
+    dispatch's own buffer, whose size the library does not know: one carved for fewer or narrower rows is refused."""
+    mine = disp.shape
+    if (disp.c.kpart and shape.dtype is torch.bfloat16 and shape.F >= 128
+            and _rows(mine) * mine.d < _rows(shape) * shape.d):
+        raise ValueError(f"disp was made for {mine}: its partial sums of the down GEMM are too small for {shape}")
+    return ctypes.byref(disp.c)
+
+
 def moe_ffn_down_fp8(shape: Shape, h, w_down, s_down, disp: Dispatch, pass_idx: int, y_perm, stream=None):
     """Down projection with E4M3 weight codes (uint8 [E,d,F]) and per-channel fp32 scales [E,d]."""
+    d = _down_disp(disp, shape)
     check("moe_ffn_down_fp8", lib().moe_ffn_down_fp8(ctypes.byref(shape.c()), _p(h), _p(w_down), _p(s_down),
-                                                     ctypes.byref(disp.c), pass_idx, _p(y_perm),
+                                                     d, pass_idx, _p(y_perm),
                                                      _stream(stream)))
 
 
 def moe_ffn_down(shape: Shape, h, w_down, disp: Dispatch, pass_idx: int, y_perm, stream=None):
-    check("moe_ffn_down", lib().moe_ffn_down(ctypes.byref(shape.c()), _p(h), _p(w_down), ctypes.byref(disp.c),
+    d = _down_disp(disp, shape)
+    check("moe_ffn_down", lib().moe_ffn_down(ctypes.byref(shape.c()), _p(h), _p(w_down), d,
                                              pass_idx, _p(y_perm), _stream(stream)))
 
 
 def moe_grouped_ffn(shape: Shape, x_perm, w_gate, w_up, w_down, disp: Dispatch, h, y_perm, stream=None):
+    d = _down_disp(disp, shape)
     check("moe_grouped_ffn", lib().moe_grouped_ffn(ctypes.byref(shape.c()), _p(x_perm), _p(w_gate), _p(w_up),
-                                                   _p(w_down), ctypes.byref(disp.c), _p(h), _p(y_perm),
+                                                   _p(w_down), d, _p(h), _p(y_perm),
                                                    _stream(stream)))
 
 
@@ -284,7 +297,8 @@ def _rows(s: Shape) -> int:
 
 
 def _disp(disp: Dispatch, shape: Shape, device):
-    """The C dispatch of a Dispatch that was made for this shape (its storage order and tile height aside)."""
+    """The C dispatch of a Dispatch that was made for this shape (d, F, storage order and tile height aside).
+    None of the calls behind it writes the dispatch's partial sums, the only array whose size depends on d."""
     mine, other = disp.shape, shape
     if (mine.T, mine.E, mine.k, mine.capacity) != (other.T, other.E, other.k, other.capacity):
         raise ValueError(f"disp was made for {mine}")

@@ -107,6 +107,13 @@ bool split_down(const moe_shape_t& s, int BM) {
   return BM == 160 && s.dtype == MOE_BF16 && mean_rows(s) >= kSplitMinRows && (int64_t)s.F * 2 >= 256;
 }
 
+// Whether a down GEMM on dispatch d splits K.  check_dispatch refuses a dispatch
+// without planes where the split needs them; moe_forward_save8 hands on its own
+// planes, or none.
+bool splits_down(const moe_shape_t& s, const moe_dispatch_t& d) {
+  return d.kpart != nullptr && split_down(s, d.tile_rows);
+}
+
 // moe_forward folds the combine into the down GEMM for a batch of at most
 // two (token, slot) entries on the 16-row tile map, one pass: each down
 // workgroup computes its column slice of y for every tile and then the output
@@ -422,7 +429,7 @@ moe_status_t enqueue_down(const moe_shape_t& s, const void* h, const void* wd, c
     a.comb_T = s.T;
     a.comb_k = s.k;
   }
-  const bool split = split_down(s, d.tile_rows);
+  const bool split = splits_down(s, d);
   if (split) {
     a.kpart = d.kpart;
     a.kplane = (size_t)row_space(s) * s.d;
@@ -466,7 +473,7 @@ moe_status_t enqueue_layer(const moe_shape_t& s, const Plan& p, const void* x, c
   const int ps = s.capacity > 0 ? kBothPasses : 0;
   if ((st = enqueue_gate_up(s, nullptr, w_gate, w_up, disp, ps, h, stream, x, s_gate, s_up, saved)) != MOE_OK)
     return st;
-  const bool split = split_down(s, disp.tile_rows);
+  const bool split = splits_down(s, disp);
   if (fused_down_combine(s, disp.tile_rows))  // a decode batch: the combine inside the down GEMM
     return enqueue_down(s, h, w_down, disp, ps, y, stream, s_down, true, out, w);
   if ((st = enqueue_down(s, h, w_down, disp, ps, y, stream, s_down, !split)) != MOE_OK) return st;
@@ -1037,8 +1044,14 @@ moe_status_t moe_forward_save8(const moe_shape_t* s, const void* x, const void* 
       !aligned({workspace}, kAlign))
     return MOE_ERR_INVALID_ARG;
   char* ws = static_cast<char*>(workspace);
+  // The down GEMM's partial sums go to the place that the workspace has for them:
+  // a caller's dispatch may serve layers of several widths, and its own planes,
+  // [2][R][d] of the shape it was carved for, may be too small for this one.  A
+  // dispatch on 160-row tiles where this shape would take others runs unsplit.
+  moe_dispatch_t d = *disp;
+  d.kpart = p.ksplit ? reinterpret_cast<float*>(ws + p.ws_disp + p.dl.kpart) : nullptr;
   return enqueue_layer(*s, p, x, w_router, bias, topk_ids, topk_w, w_gate, w_up, w_down, nullptr, nullptr, nullptr, out,
-                       *disp, ws + p.ws_h, ws + p.ws_y, ws + p.ws_perm, saved, stream);
+                       d, ws + p.ws_h, ws + p.ws_y, ws + p.ws_perm, saved, stream);
 }
 
 moe_status_t moe_backward(const moe_shape_t* s, const void* x, const void* w_router, const int32_t* topk_ids,

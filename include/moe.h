@@ -131,7 +131,9 @@ typedef struct moe_dispatch {
   uint32_t* err_flags;     /* [1]      bit 0: an id outside [0, E) was skipped   */
   float* kpart;            /* [2][R][d] fp32: the down GEMM's partial sums over the
                               two halves of its K loop, when the shape splits it
-                              (bf16, 160-row tiles, >= 80 rows per expert), else NULL */
+                              (bf16, 160-row tiles, >= 80 rows per expert), else NULL.
+                              R and d are those of the carved shape: the down GEMM
+                              calls need planes of at least their own R x d   */
   int32_t tile_rows;       /* BM the tile map was built for                      */
   int32_t max_tiles;       /* entries reserved per pass in tile_map              */
 } moe_dispatch_t;
@@ -421,8 +423,9 @@ moe_status_t moe_grouped_ffn_backward(const moe_shape_t* s, const void* x, const
 /* moe_forward for training: `out` is bitwise that of moe_forward, and what the
  * backward pass needs is left in the caller's buffers: topk_ids and topk_w
  * [T,k] (computed where w_router is not NULL, else read), disp (from
- * moe_dispatch_carve) and saved (from moe_saved8_carve).  workspace as for
- * moe_forward; it may be reused as soon as the call's work is done. */
+ * moe_dispatch_carve; its kpart is not used, so layers that differ only in d, F
+ * or weight_layout may share it) and saved (from moe_saved8_carve).  workspace as
+ * for moe_forward; it may be reused as soon as the call's work is done. */
 moe_status_t moe_forward_save8(const moe_shape_t* s, const void* x, const void* w_router, const float* bias,
                                int32_t* topk_ids, float* topk_w, const void* w_gate, const void* w_up,
                                const void* w_down, void* out, const moe_dispatch_t* disp, const moe_saved8_t* saved,

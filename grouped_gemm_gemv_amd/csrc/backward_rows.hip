@@ -195,7 +195,9 @@ __global__ __launch_bounds__(256) void token_backward_kernel(const char* __restr
 // dw_i), and its dense form for the router's weight gradient: workgroup b
 // holds the KS tokens of one K step, one thread each, and writes [E][KS]
 // (bf16: the rounded value, and the rounded rest) and each expert's sum over
-// the step, the first half of dbias.  Bound by latency: 6 us for 4096 tokens and
+// the step, the first half of dbias.  Slots without an expert are left out of
+// the sum: their weight and its gradient may hold anything, and zero times a NaN
+// would reach the token's other slots.  Bound by latency: 6 us for 4096 tokens and
 // 64 experts.
 template <class Tr>
 __global__ __launch_bounds__(256) void route_dz_kernel(const int32_t* __restrict__ ids, const float* __restrict__ w,
@@ -212,13 +214,15 @@ __global__ __launch_bounds__(256) void route_dz_kernel(const int32_t* __restrict
   if (threadIdx.x < KS && t < T) {
     const float* wt = w + t * k;
     const float* dt = dw + t * k;
+    const int* it = ids + t * k;
+    const auto live = [&](int j) { return it[j] >= 0 && it[j] < E; };
     float s = 0.f;
-    for (int j = 0; j < k; ++j) s = fmaf(wt[j], dt[j], s);
+    for (int j = 0; j < k; ++j)
+      if (live(j)) s = fmaf(wt[j], dt[j], s);
     for (int j = 0; j < k; ++j) {
-      const float z = wt[j] * (dt[j] - s);
+      const float z = live(j) ? wt[j] * (dt[j] - s) : 0.f;
       dz[t * k + j] = z;
-      const int id = ids[t * k + j];
-      if (id >= 0 && id < E) dense[id * KS + threadIdx.x] += z, any = true;
+      if (live(j)) dense[it[j] * KS + threadIdx.x] += z, any = true;
     }
   }
   const uint64_t bits = __ballot(any);

@@ -389,6 +389,8 @@ moe_status_t moe_permute_backward(const moe_shape_t* s, const void* dx_perm, con
 /* Gradient of moe_route for given topk_ids and topk_w [T,k].  The weights are
  * the softmax over a token's chosen logits, so with dtopk_w [T,k] fp32
  *   dz[f] = topk_w[f] (dtopk_w[f] - sum_i topk_w[t,i] dtopk_w[t,i])
+ * (the sum without slots whose id is outside [0, E): what their topk_w and
+ * dtopk_w hold is not looked at)
  *   dx[t] = sum_j dz[t k + j] w_router[topk_ids[t,j]]
  *   dw_router[e] = sum over entries f of expert e of dz[f] x[f / k]
  *   dbias[e] = sum over entries f of expert e of dz[f]

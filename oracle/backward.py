@@ -63,9 +63,11 @@ def permute_backward(dx_perm, row_of, T, k, dtype):
 
 
 def route_backward(x, wr, ids, w, dw, dtype):
-    """dx, dw_router, dbias with bounds.  dz = w (dw - <w, dw>)."""
+    """dx, dw_router, dbias with bounds.  dz = w (dw - <w, dw>) over the slots that have an expert."""
     T, k = w.shape
     E, d = wr.shape
+    live = (ids >= 0) & (ids < E)
+    w, dw = np.where(live, w, 0.0), np.where(live, dw, 0.0)
     dz = w * (dw - (w * dw).sum(axis=1, keepdims=True))
     e_dz = (k + 4) * U32 * np.abs(w) * (np.abs(dw) + (np.abs(w) * np.abs(dw)).sum(axis=1, keepdims=True))
     dense, e_dense, n = np.zeros((T, E)), np.zeros((T, E)), np.zeros(E)

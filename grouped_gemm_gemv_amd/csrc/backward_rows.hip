@@ -14,9 +14,9 @@ constexpr int kSlots = 4;  // slots of a token worked at a time
 
 // Gradient of out_t = sum_j w_j y_j for slots 4 blockIdx.y .. + 3 of token
 // blockIdx.x: dy_j = w_j dout_t (one rounding) and dw_j = <dout_t, y_j>.  dout_t
-// is read once for the four slots.  dw: thread partials over its chunks, then
-// lanes, then wavefronts in order.  Bound by memory: 4096 tokens of 2048 bf16
-// with 6 experts each take 37 us (5.9 TB/s).
+// is read once for the four slots, and not at all if none of them has a row.  dw:
+// thread partials over its chunks, then lanes, then wavefronts in order.  Bound by
+// memory: 4096 tokens of 2048 bf16 with 6 experts each take 37 us (5.9 TB/s).
 template <class Tr>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const char* __restrict__ dout,
                                                                const char* __restrict__ y,
@@ -32,7 +32,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const char* __res
   const int j0 = blockIdx.y * kSlots;
   size_t at[kSlots];
   float w[kSlots], acc[kSlots];
-  bool ok[kSlots];
+  bool ok[kSlots], any = false;
 #pragma unroll
   for (int u = 0; u < kSlots; ++u) {
     const int row = j0 + u < k ? row_of[t * k + j0 + u] : -1;
@@ -40,9 +40,10 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const char* __res
     w[u] = ok[u] ? topk_w[t * k + j0 + u] : 0.f;
     at[u] = ok[u] ? (size_t)row * row_bytes : 0;
     acc[u] = 0.f;
+    any = any || ok[u];
   }
   const char* dt = dout + t * row_bytes;
-  for (int c = threadIdx.x; c < nchunk; c += blockDim.x) {
+  for (int c = threadIdx.x; any && c < nchunk; c += blockDim.x) {
     const size_t o = (size_t)c * 16;
     float g[EPC];
     const uint4 gc = *reinterpret_cast<const uint4*>(dt + o);

@@ -85,3 +85,38 @@ def test_router_gradient_does_not_look_at_dropped_slots(kw):
         runs.append([bits(t) for t in (*r.values(), *a.values())])
     for other in runs[1:]:
         assert all(np.array_equal(p, q) for p, q in zip(runs[0], other))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", [dict(T=40, d=576, E=16, k=9, F=64), dict(T=21, d=64, E=12, k=5, F=64, dtype="f32")],
+                         ids=str)
+def test_combine_gradient_where_groups_of_slots_have_no_row(kw):
+    """The kernel works four slots at a time: whole groups of them without a row, and tokens without any, whose dout
+    and weights hold NaN."""
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from tests.gpu_helpers import host64
+    from tests.test_gpu_backward import Case, _t, close
+    print(f"\n[gpu] combine gradient, groups without a row {kw}", flush=True)
+    c = Case(**kw)
+    rng = np.random.default_rng(8)
+    drop = np.zeros((c.T, c.k), dtype=bool)
+    drop[::3, :4], drop[1::3, 4:], drop[[2, 5, c.T - 1]] = True, True, True
+    pad = drop.all(axis=1)
+    ids = np.where(drop, -1, c.ids_np).astype(np.int32)
+    c.ids.copy_(torch.from_numpy(ids))
+    c.M.moe_permute(c.shape, c.x, c.ids, c.disp, c.empty(c.R, c.d),
+                    c.M.workspace(c.M.query(c.shape).permute_ws_bytes))
+    y = _t(rng.standard_normal((c.R, c.d)), c.dt)
+    want, e, dww, ew = B.combine_backward(host64(c.dout), host64(y), host64(c.w),
+                                          c.disp.arrays()["row_of"].cpu().numpy(), c.dtype)
+    c.dout[torch.from_numpy(pad).cuda()] = float("nan")
+    c.w[torch.from_numpy(drop).cuda()] = float("nan")
+    dy, dw = c.empty(c.R, c.d), c.empty(c.T, c.k, dt=torch.float32)
+    c.M.moe_combine_backward(c.shape, c.dout, y, c.w, c.disp, dy, dw)
+    live = c.disp.arrays()["token_of"].cpu().numpy() >= 0
+    close("dy", host64(dy)[live], want[live], e[live])
+    assert np.isnan(host64(dy)[~live]).all()  # rows without a token stay as they were
+    close("dw", host64(dw), dww, ew)
+    assert (host64(dw)[drop] == 0).all()

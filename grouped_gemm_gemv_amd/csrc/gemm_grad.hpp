@@ -1243,6 +1243,8 @@ constexpr int kComputeUnits = 256;
 // admit), in whole rounds of the XCDs, no more than there are units.
 template <class T>
 inline unsigned grid_of(long long units) {
+  static_assert(T::OCC * (T::S * T::STAGE + sizeof(ExpertTable) + 4 * sizeof(int)) <= 160 * 1024,
+                "ring and table of the workgroups that share a compute unit");
   const long long most = (long long)kComputeUnits * T::OCC;
   return (unsigned)((units < most ? (units + 7) / 8 * 8 : most));
 }

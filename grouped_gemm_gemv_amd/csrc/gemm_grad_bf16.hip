@@ -9,7 +9,7 @@ using D256 = Tile<TBF16, 256, 256, 2, 4, kPanelK, kRows, 4, 1, true>;
 using D192 = Tile<TBF16, 192, 256, 2, 4, kPanelK, kRows, 5, 1, true>;
 using D256N = Tile<TBF16, 256, 128, 4, 2, kPanelK, kRows, 5, 1, true>;
 using D128 = Tile<TBF16, 128, 128, 2, 2, kPanelK, kRows, 4, 2, false>;
-using D64 = Tile<TBF16, 64, 128, 1, 4, kPanelK, kRows, 4, 3, false>;
+using D64 = Tile<TBF16, 64, 128, 1, 4, kPanelK, kRows, 4, 2, false>;
 // weight gradients, whatever the rows: with 16 rows per expert, when the stores of
 // the gradients are all there is, 128 x 128 tiles (two workgroups for each compute
 // unit) took 904 us at the Mixtral shape and 956 against 747 us with 64 rows

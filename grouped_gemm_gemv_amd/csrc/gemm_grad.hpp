@@ -39,7 +39,7 @@
 // matrix and steps past the last.
 //
 // The workgroups are persistent: each takes every so-many-th unit (tile) of
-// its XCD's range, and the ring runs on across units, so the first steps of
+// its XCD's range or of the whole, and the ring runs on across units, so the first steps of
 // the next tile are on their way while the last ones of this one are
 // multiplied and its results are stored.
 //
@@ -740,6 +740,22 @@ __device__ __forceinline__ Units my_units(int total) {
   return Units{x * J + ((int)blockIdx.x >> 3), (int)gridDim.x >> 3, min(total, (x + 1) * J)};
 }
 
+// The weight gradients' units, whose cost is their expert's rows: dealt to the XCDs in
+// runs of one unit for each of their workgroups, so that every XCD takes part in
+// every expert and units at work at a time in one L2 are still neighbours.  With a
+// contiguous eighth for each XCD, as above (with 8 experts just one of them), the hot
+// expert's XCD set the pace.  Contiguous against dealt, us of the launch:
+//  * Zipf 1.2 routing, the Mixtral shape with 1024 rows 1207 against 802, with 8192 6300
+//    against 2881; 64 experts of d = 3584, F = 2560 with 32768 rows 3928 against 2310 (Zipf 2.0:
+//    4085 against 2403); fp32, 8 experts of d = 1024, F = 4096 with 2048 rows 1347 against 584;
+//  * uniform routing, the Mixtral shape with 128, 512, 1024, 4096, 8192 rows 617, 767, 887,
+//    1700, 2785 against 614, 726, 875, 1666, 2795; 64 experts of d = 3584, F = 2560 with 4096 and
+//    32768 rows 903 and 2151 against 880 and 2218; fp32 as above 573 against 575.
+__device__ __forceinline__ Units dealt_units(int total) {
+  const int per = (int)gridDim.x >> 3;
+  return Units{((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3), (int)gridDim.x, total};
+}
+
 // out tile = act rows x weights (DH: with the SwiGLU's gradient in the epilogue).
 // A unit's steps go over K, a1 x b1 behind a0 x b0 into the same accumulators.
 // Out: type of the results (a choice at run time cost the main loop 8 %, in
@@ -1151,7 +1167,7 @@ __global__ __launch_bounds__(T::NTH) void wgrad_kernel(WgradArgs p) {
   __shared__ ExpertTable tab;
   fill_table<T::KS>(p.rows, tab);
   WgradJob<Tr, T> job(p, tab);
-  const Units u = my_units(p.units);
+  const Units u = dealt_units(p.units);
   typename T::template Runner<WgradJob<Tr, T>>(job, ring, ring_at, u.first, u.stride, u.end, lane, wave).run();
 }
 
@@ -1267,7 +1283,8 @@ hipError_t launch_dgrad_cfg(const DgradArgs& a, long long max_tiles, hipStream_t
 template <class Tr, class T>
 hipError_t launch_wgrad_cfg(WgradArgs a, hipStream_t stream) {
   const long long MT = (a.M + T::BM - 1) / T::BM, NT = (a.N + T::BN - 1) / T::BN;
-  if (kBand * MT * NT > 0x7fffff00LL || a.n * MT * NT * a.rows.E > 0x7fffff00LL) return hipErrorInvalidValue;
+  // (a unit number plus the grid still fits 32 bits)
+  if (kBand * MT * NT > 0x7fff0000LL || a.n * MT * NT * a.rows.E > 0x7fff0000LL) return hipErrorInvalidValue;
   for (int w = 0; w < a.n; ++w) {
     WgradProduct& p = a.prod[w];
     p.first = (int)(w * MT * NT);

@@ -115,8 +115,8 @@ __device__ __forceinline__ void route_finish(const RouteFinish& p, int E, int d)
 // (64 or 256) work on a token.  The first fin.blocks workgroups finish the
 // router's other gradients instead (nothing here needs them, and they would be
 // a launch of their own).  Bound by memory: the sum of 8 rows of 3584 bf16 for
-// 4096 tokens takes 39 us (6.6 TB/s); the router's part for 4096 tokens of 2048
-// with 64 experts, 6 chosen, 15 us with the finish (6 us as its own launch).
+// 4096 tokens takes 39 us (6.8 TB/s); the router's part for 4096 tokens of 2048
+// with 64 experts, 6 chosen, 14 us with the finish (6 us as its own launch).
 template <class Tr, class In>
 __global__ __launch_bounds__(256) void token_backward_kernel(const char* __restrict__ dx_perm,
                                                              const int32_t* __restrict__ row_of,
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(256) void token_backward_kernel(const char* __restr
 // (bf16: the rounded value, and the rounded rest) and each expert's sum over
 // the step, the first half of dbias.  Slots without an expert are left out of
 // the sum: their weight and its gradient may hold anything, and zero times a NaN
-// would reach the token's other slots.  Bound by latency: 6 us for 4096 tokens and
+// would reach the token's other slots.  Bound by latency: 7 us for 4096 tokens and
 // 64 experts.
 template <class Tr>
 __global__ __launch_bounds__(256) void route_dz_kernel(const int32_t* __restrict__ ids, const float* __restrict__ w,

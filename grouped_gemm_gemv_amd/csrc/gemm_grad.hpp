@@ -44,14 +44,14 @@
 // multiplied and its results are stored.
 //
 // What bounds them, at d = 4096, F = 14336 with 8 experts (bf16):
-//  * many rows: the matrix cores.  8192 rows take 926 us (first data gradient,
-//    1.04 PF/s), 1617 (second, 1.19) and 2836 (weight gradients, 1.02), where a
-//    library product of 8192 cubed reaches 1.24, or 1.10 with a transposed
+//  * many rows: the matrix cores.  8192 rows take 927 us (first data gradient,
+//    1.04 PF/s), 1584 (second, 1.21) and 2879 (weight gradients, 1.00), where a
+//    library product of 8192 cubed reaches 1.28, or 1.12 with a transposed
 //    operand; the clock falls to 2.0 GHz.  What is left: the codes and the
 //    epilogue of the first, the stores between the tiles of the last;
-//  * few rows: memory.  32 rows take 181 and 290 us (0.94 and 1.88 GB of
-//    weights, 5.2 and 6.5 TB/s) and 610 (2.8 GB of weight gradients, 4.6 TB/s
-//    where a fill reaches 6.8: a tile's rows are 512-byte pieces).
+//  * few rows: memory.  32 rows take 186 and 291 us (0.94 and 1.88 GB of
+//    weights, 5.1 and 6.5 TB/s) and 606 (2.8 GB of weight gradients, 4.7 TB/s
+//    where a fill reaches 6.9: a tile's rows are 512-byte pieces).
 #pragma once
 
 #include <algorithm>
@@ -1077,8 +1077,9 @@ struct WgradJob {
     L -= w.first;
     // bands of kBand tiles of out's rows by all tiles of its columns: the tiles that
     // an XCD works at a time share both operands in L2 and store long runs of
-    // each row (bands of 2 against 8 tiles, the Mixtral shape: 599 against 618 us
-    // with 16 rows in all, 2985 against 3011 us with 8192)
+    // each row (bands of 1, 2, 4, 8 tiles, the Mixtral shape: 599, 595, 609, 615 us
+    // with 16 rows in all, 2894, 2884, 2886, 2920 with 8192; 64 experts of d = 3584,
+    // F = 2560 with 32768 rows 2300, 2297, 2288, 2301)
     const int band = quotient(L, w.band), in = L - band * (int)w.band.d;
     const bool whole = (band + 1) * kBand <= w.RT;
     const int ct = whole ? in / kBand : quotient(in, w.last);

@@ -135,8 +135,8 @@ __device__ __forceinline__ uint4 widen_e4m3(unsigned lo, unsigned hi) {
 // backward pass (moe_saved8_t).  A 16-column block of a row is exactly one
 // MFMA subtile's column of accumulators (four lanes of four values), so the
 // shared exponent takes two lane exchanges and no LDS.  The weights bound it as
-// before: 342 us for 512 tokens at d = 4096, F = 14336, 8 experts of which 2 are
-// chosen (1.9 GB, 5.5 TB/s), 107 us for one token.
+// before: 337 us for 512 tokens at d = 4096, F = 14336, 8 experts of which 2 are
+// chosen (1.9 GB, 5.7 TB/s) against 318 without, 107 against 98 for one token.
 template <class Tr, int BM, int WTN, int WN, int WK, bool GATED, int PF, int NTMS, bool WQ, int WS = 0, int KS = 1,
           int PP = 0, bool SAVE = false>
 struct Gemm {

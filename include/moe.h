@@ -331,6 +331,11 @@ moe_status_t moe_forward_fp8(const moe_shape_t* s, const void* x, const void* w_
  * code is clamped; relative to the block's largest magnitude that is at most
  * 2^-7.  A block with a NaN or an infinity has b = 255 and reads as NaN in all
  * 16 columns.  Magnitudes below 2^-127 read as 0.  Every value is exact in bf16.
+ * What it costs: the backward pass is that of a layer whose projections are these
+ * values.  With normally distributed x, weights and dout its gradients differ from
+ * the unquantised layer's by 0.7-1.1 % in norm (dx 0.7-0.9, dw_gate and dw_up
+ * 0.7-1.1, dw_down and dtopk_w 0.9-1.1); projections kept in bf16 would give
+ * 0.2-0.3 %.
  *
  * Beyond the conventions above: the pointers of these calls must be 16-byte
  * aligned (topk arrays, their gradients, dbias and counts 4-byte; else

@@ -87,3 +87,32 @@ def test_forward_save8_leaves_a_shared_dispatchs_partial_sums_alone():
     ref = torch.empty_like(x)
     M.moe_forward(s, x, wr, None, None, None, wg, wu, wd, ref, ws)
     assert np.array_equal(bits(ref), res[0][2])
+
+
+@pytest.mark.gpu
+def test_forward_save8_on_a_taller_dispatch_than_the_shapes_own():
+    """The dispatch's 160-row tiles would split K, this shape's own 64-row ones do not, so the workspace has no place
+    for partial sums: the down GEMM runs unsplit, and the dispatch's planes stay as they are."""
+    import grouped_gemm_gemv_amd as M
+    from tests.gpu_helpers import TOL, host64, rel_err
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    print("\n[gpu] taller dispatch", flush=True)
+    s, tall = M.Shape(512, 64, 8, 2, 256), M.Shape(512, 64, 8, 2, 256, tile_rows=160)
+    assert M.query(s).tile_rows != 160
+    gen = torch.Generator(device="cuda").manual_seed(5)
+
+    def rnd(*n):
+        return (torch.randn(*n, generator=gen, device="cuda") / n[-1] ** 0.5).bfloat16()
+
+    x, wr = rnd(s.T, s.d) * 8, rnd(s.E, s.d)
+    wg, wu, wd = rnd(s.E, s.F, s.d), rnd(s.E, s.F, s.d), rnd(s.E, s.d, s.F)
+    disp, saved, ws = M.Dispatch(tall), M.Saved8(s), M.workspace(M.workspace_size(s))
+    disp.buf.fill_(0x5A)
+    ids, w = torch.empty(s.T, s.k, dtype=torch.int32, device="cuda"), torch.empty(s.T, s.k, device="cuda")
+    out, ref = torch.full_like(x, float("nan")), torch.empty_like(x)
+    M.moe_forward_save8(s, x, wr, None, ids, w, wg, wu, wd, out, disp, saved, ws)
+    M.moe_forward(s, x, wr, None, None, None, wg, wu, wd, ref, ws)
+    torch.cuda.synchronize()
+    assert disp.c.kpart and (disp.buf[disp.c.kpart - disp.buf.data_ptr():] == 0x5A).all()
+    assert rel_err(host64(out), host64(ref)) <= TOL["bf16"]

@@ -268,12 +268,13 @@ void carve(const moe_shape_t& s, const Plan& p, char* base, moe_dispatch_t* d) {
   (void)s;
 }
 
-moe_status_t check_dispatch(const moe_shape_t& s, const Plan& p, const moe_dispatch_t* d) {
+// `down`: the call runs a down GEMM on the dispatch's own planes of partial sums.
+moe_status_t check_dispatch(const moe_shape_t& s, const Plan& p, const moe_dispatch_t* d, bool down = false) {
   if (d == nullptr) return MOE_ERR_NULL_PTR;
   if (!d->counts || !d->offsets || !d->spill_counts || !d->spill_offsets || !d->row_of || !d->token_of ||
       !d->tile_off || !d->tile_map || !d->n_tiles || !d->err_flags)
     return MOE_ERR_NULL_PTR;
-  if (split_down(s, d->tile_rows) && d->kpart == nullptr) return MOE_ERR_NULL_PTR;
+  if (down && split_down(s, d->tile_rows) && d->kpart == nullptr) return MOE_ERR_NULL_PTR;
   if (!supported_tile_rows(d->tile_rows)) return MOE_ERR_UNSUPPORTED;
   const int64_t need = std::max(pass_max_tiles(s, d->tile_rows, 0), pass_max_tiles(s, d->tile_rows, 1));
   if (d->max_tiles < need || d->max_tiles < 1) return MOE_ERR_INVALID_ARG;
@@ -810,7 +811,7 @@ moe_status_t moe_ffn_down(const moe_shape_t* s, const void* h, const void* w_dow
   if (!h || !w_down || !y_perm) return MOE_ERR_NULL_PTR;
   if (pass < 0 || pass > kBothPasses) return MOE_ERR_INVALID_ARG;
   const Plan p = make_plan(*s);
-  if ((st = check_dispatch(*s, p, disp)) != MOE_OK) return st;
+  if ((st = check_dispatch(*s, p, disp, true)) != MOE_OK) return st;
   return enqueue_down(*s, h, w_down, *disp, pass, y_perm, stream);
 }
 
@@ -821,7 +822,7 @@ moe_status_t moe_grouped_ffn(const moe_shape_t* s, const void* x_perm, const voi
   if (st != MOE_OK) return st;
   if (!x_perm || !w_gate || !w_up || !w_down || !h || !y_perm) return MOE_ERR_NULL_PTR;
   const Plan p = make_plan(*s);
-  if ((st = check_dispatch(*s, p, disp)) != MOE_OK) return st;
+  if ((st = check_dispatch(*s, p, disp, true)) != MOE_OK) return st;
   const int passes = s->capacity > 0 ? 2 : 1;
   for (int ps = 0; ps < passes; ++ps) {
     if ((st = enqueue_gate_up(*s, x_perm, w_gate, w_up, *disp, ps, h, stream)) != MOE_OK) return st;
@@ -902,7 +903,7 @@ moe_status_t moe_ffn_down_fp8(const moe_shape_t* s, const void* h, const uint8_t
   if (!h || !w_down || !s_down || !y_perm) return MOE_ERR_NULL_PTR;
   if (pass < 0 || pass > kBothPasses) return MOE_ERR_INVALID_ARG;
   const Plan p = make_plan(*s);
-  if ((st = check_dispatch(*s, p, disp)) != MOE_OK) return st;
+  if ((st = check_dispatch(*s, p, disp, true)) != MOE_OK) return st;
   return enqueue_down(*s, h, w_down, *disp, pass, y_perm, stream, s_down);
 }
 

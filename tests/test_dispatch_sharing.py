@@ -43,6 +43,26 @@ def test_down_calls_refuse_a_dispatch_with_too_few_partial_sums(call):
             run(M.Dispatch(disp, device="cpu"), shape)
 
 
+def test_only_the_down_calls_ask_for_planes_of_partial_sums():
+    """A dispatch carved without planes (F = 64 does not split K) for a layer of the same routing that splits: the down
+    GEMM calls refuse it (a pointer is missing, 2), the calls that do not use the planes go on to their next check, here
+    a workspace or a pointer that is not aligned (1).  No address is used."""
+    import grouped_gemm_gemv_amd as M
+    from grouped_gemm_gemv_amd._lib import MoeSaved8, lib
+    _, wide = _shapes()
+    disp = M.Dispatch(M.Shape(512, 512, 8, 2, 64, tile_rows=160), device="cpu")
+    assert not disp.c.kpart and M.Dispatch(wide, device="cpu").c.kpart
+    S, D, V = ctypes.byref(wide.c()), ctypes.byref(disp.c), ctypes.byref(MoeSaved8(*[1 << 20] * 4))
+    A, big = 1 << 20, 1 << 50
+    assert lib().moe_ffn_down(S, A, A, D, 0, A, None) == 2
+    assert lib().moe_ffn_down_fp8(S, A, A, A, D, 0, A, None) == 2
+    assert lib().moe_grouped_ffn(S, A, A, A, A, D, A, A, None) == 2
+    assert lib().moe_ffn_gate_up_save8(S, A + 8, A, A, D, 0, A, V, None) == 1
+    assert lib().moe_forward_save8(S, A, A, A, A, A, A, A, A, A, D, V, A + 8, big, None) == 1
+    assert lib().moe_grouped_ffn_backward(S, *[A] * 6, D, V, *[A] * 5, A + 8, big, None) == 1
+    assert lib().moe_backward(S, *[A] * 7, D, V, *[A] * 8, A + 8, big, None) == 1
+
+
 @pytest.mark.gpu
 def test_forward_save8_leaves_a_shared_dispatchs_partial_sums_alone():
     """Two layers of different width share a dispatch: nothing behind its other arrays is written, out is bitwise
@@ -72,7 +92,9 @@ def test_forward_save8_leaves_a_shared_dispatchs_partial_sums_alone():
     assert c.kpart
     shared = M.Dispatch(narrow, c=c, owner=buf)
     res = []
-    for disp in (shared, M.Dispatch(s)):
+    none = M.Dispatch(M.Shape(s.T, s.d, s.E, s.k, 64, tile_rows=160))  # carved without planes
+    assert not none.c.kpart
+    for disp in (shared, M.Dispatch(s), none):
         ids = torch.empty(s.T, s.k, dtype=torch.int32, device="cuda")
         w, dw = (torch.empty(s.T, s.k, device="cuda") for _ in range(2))
         out, dx = torch.empty_like(x), torch.empty_like(x)
@@ -83,7 +105,8 @@ def test_forward_save8_leaves_a_shared_dispatchs_partial_sums_alone():
         res.append([bits(t) for t in (ids, w, out, dx, dw, *g)])
     torch.cuda.synchronize()
     assert (buf[c.kpart - buf.data_ptr():] == 0x5A).all()
-    assert all(np.array_equal(a, b) for a, b in zip(*res))
+    for other in res[1:]:
+        assert all(np.array_equal(a, b) for a, b in zip(res[0], other))
     ref = torch.empty_like(x)
     M.moe_forward(s, x, wr, None, None, None, wg, wu, wd, ref, ws)
     assert np.array_equal(bits(ref), res[0][2])

@@ -37,6 +37,8 @@ EXPORTED = [
     "moe_forward_noalloc",
     "moe_backward_query", "moe_saved8_carve", "moe_ffn_gate_up_save8", "moe_saved8_unpack", "moe_combine_backward",
     "moe_permute_backward", "moe_route_backward", "moe_grouped_ffn_backward", "moe_forward_save8", "moe_backward",
+    "moe_norm", "moe_norm_backward", "moe_residual", "moe_residual_workspace_size", "moe_residual_backward",
+    "moe_dropout", "moe_decode_workspace_size", "moe_decode", "moe_decode_fp8",
 ]
 
 
@@ -75,6 +77,13 @@ class MoeSaved8(ctypes.Structure):
     _fields_ = [(n, c_ptr) for n in SAVED8_ARRAYS]
 
 
+GATE_NONE, GATE_TOKEN, GATE_FULL = 0, 1, 2  # moe_gate_t
+
+
+class MoeResidual(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_float), ("scale", ctypes.c_float), ("dropout", ctypes.c_float), ("gate", c_i32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn: str, status: int, msg: str):
         super().__init__(f"{fn} failed: {msg}")
@@ -90,6 +99,8 @@ def _declare(lib):
     S = P(MoeShape)
     D = P(MoeDispatch)
     V = P(MoeSaved8)
+    R = P(MoeResidual)
+    F, N = ctypes.c_float, ctypes.c_size_t
     lib.moe_status_string.argtypes = [ctypes.c_int]
     lib.moe_status_string.restype = ctypes.c_char_p
     sig = {
@@ -122,6 +133,15 @@ def _declare(lib):
         "moe_grouped_ffn_backward": [S] + [c_ptr] * 6 + [D, V] + [c_ptr] * 6 + [ctypes.c_size_t, c_ptr],
         "moe_forward_save8": [S] + [c_ptr] * 9 + [D, V, c_ptr, ctypes.c_size_t, c_ptr],
         "moe_backward": [S] + [c_ptr] * 7 + [D, V] + [c_ptr] * 9 + [ctypes.c_size_t, c_ptr],
+        "moe_norm": [S, c_ptr, c_ptr, F, c_ptr, c_ptr],
+        "moe_norm_backward": [S, c_ptr, c_ptr, F] + [c_ptr] * 5 + [N, c_ptr],
+        "moe_residual": [S, R] + [c_ptr] * 9,
+        "moe_residual_workspace_size": [S, P(N)],
+        "moe_residual_backward": [S, R] + [c_ptr] * 14 + [N, c_ptr],
+        "moe_dropout": [c_ptr, ctypes.c_int64, ctypes.c_int, F, c_ptr, c_ptr, c_ptr],
+        "moe_decode_workspace_size": [S, P(N)],
+        "moe_decode": [S, c_ptr, c_ptr, F] + [c_ptr] * 8 + [F, c_ptr, c_ptr, N, c_ptr],
+        "moe_decode_fp8": [S, c_ptr, c_ptr, F] + [c_ptr] * 11 + [F, c_ptr, c_ptr, N, c_ptr],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)

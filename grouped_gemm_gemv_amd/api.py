@@ -14,7 +14,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import (MoeBackwardSizes, MoeDispatch, MoeForwardViews, MoeSaved8, MoeShape, MoeSizes, check, lib)
+from ._lib import (MoeBackwardSizes, MoeDispatch, MoeForwardViews, MoeResidual, MoeSaved8, MoeShape, MoeSizes, check, lib)
 
 _DT = {torch.float32: _lib.MOE_F32, torch.bfloat16: _lib.MOE_BF16}
 _TORCH_DT = {v: k for k, v in _DT.items()}
@@ -467,3 +467,133 @@ def moe_backward(shape: Shape, x, w_router, topk_ids, topk_w, w_gate, w_up, w_do
           _in(dx, "dx", (s.T, s.d), s.dtype, dev), _in(dtopk_w, "dtopk_w", tk, torch.float32, dev),
           _in(dw_router, "dw_router", (s.E, s.d), s.dtype, dev), _in(dbias, "dbias", (s.E,), torch.float32, dev),
           *_weights(s, "dw", dw_gate, dw_up, dw_down, dev), *_ws(ws, dev))
+
+
+# ---- the block around the layer ----
+
+
+@dataclasses.dataclass(frozen=True)
+class Residual:
+    """What moe_residual does beside its arrays: eps of the norms, the residual branch's scale, dropout's p."""
+    eps: float = 1e-6
+    scale: float = 1.0
+    dropout: float = 0.0
+
+    def c(self, gate: int) -> MoeResidual:
+        return MoeResidual(self.eps, self.scale, self.dropout, gate)
+
+
+def _gate(gate, s: Shape, name: str, device):
+    """moe_gate_t and the address of a gate [T] (one value a token) or [T, d], or None."""
+    if gate is None:
+        return _lib.GATE_NONE, None
+    full = gate.dim() != 1
+    want = (s.T, s.d) if full else (s.T,)
+    return _lib.GATE_FULL if full else _lib.GATE_TOKEN, _in(gate, name, want, s.dtype, device)
+
+
+def _rng(rng, device):
+    return _in(rng, "rng", (2,), torch.int64, device)
+
+
+def residual_workspace_size(shape: Shape) -> int:
+    """Bytes of workspace of moe_norm_backward and moe_residual_backward."""
+    n = ctypes.c_size_t()
+    check("moe_residual_workspace_size", lib().moe_residual_workspace_size(_c(shape), ctypes.byref(n)))
+    return n.value
+
+
+def moe_norm(shape: Shape, x, w, n, eps: float = 1e-6, stream=None):
+    """n = x / rms(x) w for every row of x [T, d]; w [d]."""
+    s, dev = shape, x.device
+    _call("moe_norm", dev, stream, _c(s), _in(x, "x", (s.T, s.d), s.dtype, dev), _in(w, "w", (s.d,), s.dtype, dev), eps,
+          _in(n, "n", (s.T, s.d), s.dtype, dev))
+
+
+def moe_norm_backward(shape: Shape, x, w, dn, dres, dx, dw, ws, eps: float = 1e-6, stream=None):
+    """Gradient of moe_norm: dx = dres + the norm's (dres may be None, and dx may be dres); dw [d], or None."""
+    s, dev = shape, x.device
+    Td = (s.T, s.d)
+    _call("moe_norm_backward", dev, stream, _c(s), _in(x, "x", Td, s.dtype, dev), _in(w, "w", (s.d,), s.dtype, dev), eps,
+          _in(dn, "dn", Td, s.dtype, dev), _in(dres, "dres", Td, s.dtype, dev), _in(dx, "dx", Td, s.dtype, dev),
+          _in(dw, "dw", (s.d,), s.dtype, dev), *_ws(ws, dev))
+
+
+def moe_residual(shape: Shape, r: Residual, res, y, post_w, gate, rng, next_w, out, n, stream=None):
+    """out = res + scale sigmoid(gate) dropout(y / rms(y) post_w) and n = out / rms(out) next_w.
+
+    post_w, gate ([T] or [T, d]) and next_w with n may be None; rng int64 [2] on the device (seed, step), None without
+    dropout; out may be res."""
+    s, dev = shape, y.device
+    Td = (s.T, s.d)
+    kind, g = _gate(gate, s, "gate", dev)
+    _call("moe_residual", dev, stream, _c(s), ctypes.byref(r.c(kind)), _in(res, "res", Td, s.dtype, dev),
+          _in(y, "y", Td, s.dtype, dev), _in(post_w, "post_w", (s.d,), s.dtype, dev), g, _rng(rng, dev),
+          _in(next_w, "next_w", (s.d,), s.dtype, dev), _in(out, "out", Td, s.dtype, dev), _in(n, "n", Td, s.dtype, dev))
+
+
+def moe_residual_backward(shape: Shape, r: Residual, out, y, post_w, gate, rng, next_w, dout, dn, dres, dy, dgate,
+                          dpost_w, dnext_w, ws, stream=None):
+    """Gradient of moe_residual from those of out (or None) and n (with next_w); `out` is what the forward call left.
+    dgate, dpost_w and dnext_w may be None: not computed.  dres may be dout."""
+    s, dev = shape, y.device
+    Td = (s.T, s.d)
+    kind, g = _gate(gate, s, "gate", dev)
+    if dgate is not None and (gate is None or dgate.shape != gate.shape):
+        raise ValueError("dgate must have the gate's shape")
+    _call("moe_residual_backward", dev, stream, _c(s), ctypes.byref(r.c(kind)), _in(out, "out", Td, s.dtype, dev),
+          _in(y, "y", Td, s.dtype, dev), _in(post_w, "post_w", (s.d,), s.dtype, dev), g, _rng(rng, dev),
+          _in(next_w, "next_w", (s.d,), s.dtype, dev), _in(dout, "dout", Td, s.dtype, dev),
+          _in(dn, "dn", Td, s.dtype, dev), _in(dres, "dres", Td, s.dtype, dev), _in(dy, "dy", Td, s.dtype, dev),
+          _gate(dgate, s, "dgate", dev)[1], _in(dpost_w, "dpost_w", (s.d,), s.dtype, dev),
+          _in(dnext_w, "dnext_w", (s.d,), s.dtype, dev), *_ws(ws, dev))
+
+
+def moe_dropout(x, p: float, rng, out, stream=None):
+    """out = x where kept, over 1 - p; any contiguous x of fp32 or bf16, and out like it (or x itself).  The same call
+    on a gradient is the gradient.  rng int64 [2] on the device: seed, step."""
+    if x.dtype not in _DT:
+        raise ValueError(f"x must be fp32 or bf16, got {x.dtype}")
+    dev = x.device
+    _call("moe_dropout", dev, stream, _in(x, "x", x.shape, x.dtype, dev), x.numel(), _DT[x.dtype], p, _rng(rng, dev),
+          _in(out, "out", x.shape, x.dtype, dev))
+
+
+# ---- the layer for a few tokens ----
+
+
+def decode_workspace_size(shape: Shape) -> int:
+    """Bytes of workspace of moe_decode and moe_decode_fp8."""
+    n = ctypes.c_size_t()
+    check("moe_decode_workspace_size", lib().moe_decode_workspace_size(_c(shape), ctypes.byref(n)))
+    return n.value
+
+
+def _decode(name, shape: Shape, x, norm_w, w_router, bias, topk_ids, topk_w, weights, res, out, ws, eps, scale, stream):
+    s, dev = shape, x.device
+    tk = (s.T, s.k)
+    _call(name, dev, stream, _c(s), _in(x, "x", (s.T, s.d), s.dtype, dev), _in(norm_w, "norm_w", (s.d,), s.dtype, dev),
+          eps, _in(w_router, "w_router", (s.E, s.d), s.dtype, dev), _in(bias, "bias", (s.E,), torch.float32, dev),
+          _in(topk_ids, "topk_ids", tk, torch.int32, dev), _in(topk_w, "topk_w", tk, torch.float32, dev), *weights,
+          _in(res, "res", (s.T, s.d), s.dtype, dev), scale, _in(out, "out", (s.T, s.d), s.dtype, dev), *_ws(ws, dev))
+
+
+def moe_decode(shape: Shape, x, norm_w, w_router, bias, topk_ids, topk_w, w_gate, w_up, w_down, res, out, ws,
+               eps: float = 1e-6, scale: float = 1.0, stream=None):
+    """The layer for up to 16 tokens, with the norm before it (norm_w) and the residual behind it (res; out may be
+    res): out = res + scale layer(x / rms(x) norm_w).  norm_w, bias and res may be None.  With w_router the routing is
+    computed, and written to topk_ids and topk_w [T, k] where they are given; without it they are read."""
+    weights = _weights(shape, "w", w_gate, w_up, w_down, x.device)
+    _decode("moe_decode", shape, x, norm_w, w_router, bias, topk_ids, topk_w, weights, res, out, ws, eps, scale, stream)
+
+
+def moe_decode_fp8(shape: Shape, x, norm_w, w_router, bias, topk_ids, topk_w, w_gate, w_up, w_down, s_gate, s_up, s_down,
+                   res, out, ws, eps: float = 1e-6, scale: float = 1.0, stream=None):
+    """moe_decode with E4M3 expert weight codes (uint8) and per-channel fp32 scales."""
+    s, dev = shape, x.device
+    up, down = (s.E, s.F, s.d), (s.E, s.d, s.F)
+    weights = [_in(w, n, sh, torch.uint8, dev)
+               for w, n, sh in ((w_gate, "w_gate", up), (w_up, "w_up", up), (w_down, "w_down", down))]
+    weights += [_in(v, n, sh, torch.float32, dev)
+                for v, n, sh in ((s_gate, "s_gate", up[:2]), (s_up, "s_up", up[:2]), (s_down, "s_down", down[:2]))]
+    _decode("moe_decode_fp8", s, x, norm_w, w_router, bias, topk_ids, topk_w, weights, res, out, ws, eps, scale, stream)

@@ -28,7 +28,7 @@ ARCH = "gfx950"
 SOURCES = ["api.cpp", "route.hip", "dispatch.hip", "gemm_bf16_gateup.hip", "gemm_bf16_down.hip",
            "gemm_f32_gateup.hip", "gemm_f32_down.hip", "gemm_fp8w_gateup.hip", "gemm_fp8w_down.hip", "layout.hip",
            "noalloc.hip", "gemm_bf16_gateup_save.hip", "gemm_f32_gateup_save.hip", "gemm_grad_bf16.hip",
-           "gemm_grad_f32.hip", "backward_rows.hip"]
+           "gemm_grad_f32.hip", "backward_rows.hip", "block_rows.hip", "decode.hip"]
 PEAKS_SOURCES = ["peaks.hip"]
 # recompiled with MOE_LOOP_PHASES for libmoe_phases.so (the other objects are shared)
 PHASES_SOURCES = ["gemm_bf16_gateup.hip", "gemm_bf16_down.hip"]

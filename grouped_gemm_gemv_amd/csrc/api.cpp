@@ -5,8 +5,10 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 
+#include "block.hpp"
 #include "launch.hpp"
 #include "moe.h"
 
@@ -711,6 +713,98 @@ moe_status_t enqueue_route_backward(const moe_shape_t& s, const BackPlan& b, con
       moe::launch_token_backward(s.dtype, dx_perm, true, row_of, dz, ids, w_router, s.T, s.k, s.d, s.E, dx, fin, st));
 }
 
+// ---- the block around the layer, and the layer for a few tokens ----
+
+// Dropout's limit on the 16-bit numbers and the factor of what is kept.
+unsigned dropout_threshold(float p) { return (unsigned)std::min(65535.0, std::floor((double)p * 65536.0 + 0.5)); }
+float dropout_scale(unsigned threshold) { return 65536.f / (float)(65536u - threshold); }
+
+moe_status_t validate_norm(const moe_shape_t* s, float eps) {
+  const moe_status_t st = validate(s);
+  if (st != MOE_OK) return st;
+  if (!(eps > 0.f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  return s->d <= moe::kNormMaxWidth ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+moe_status_t validate_residual(const moe_shape_t* s, const moe_residual_t* r, const void* gate, const uint64_t* rng) {
+  moe_status_t st = validate(s);
+  if (st != MOE_OK) return st;
+  if (r == nullptr) return MOE_ERR_NULL_PTR;
+  if ((st = validate_norm(s, r->eps)) != MOE_OK) return st;
+  if (!std::isfinite(r->scale) || !(r->dropout >= 0.f && r->dropout < 1.f)) return MOE_ERR_INVALID_ARG;
+  if (r->gate != MOE_GATE_NONE && r->gate != MOE_GATE_TOKEN && r->gate != MOE_GATE_FULL) return MOE_ERR_INVALID_ARG;
+  if (r->gate == MOE_GATE_NONE && gate != nullptr) return MOE_ERR_INVALID_ARG;
+  if (r->gate != MOE_GATE_NONE && gate == nullptr) return MOE_ERR_NULL_PTR;
+  if (r->dropout > 0.f && rng == nullptr) return MOE_ERR_NULL_PTR;
+  if (!aligned({rng}, 8)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// A gate's or its gradient's alignment: whole chunks, or single elements.
+bool gate_aligned(const moe_shape_t& s, const moe_residual_t& r, const void* gate) {
+  return aligned({gate}, r.gate == MOE_GATE_FULL ? 16 : elt_bytes(s));
+}
+
+size_t residual_ws(const moe_shape_t& s) {
+  return align_up((size_t)2 * moe::residual_backward_groups(s.T, s.d) * s.d * 4);
+}
+
+// Of the layer for a few tokens: the routing, then h of the experts that may be active.
+size_t decode_ws(const moe_shape_t& s) {
+  const size_t active = (size_t)std::min<int64_t>(s.E, (int64_t)s.T * s.k);
+  return align_up(sizeof(moe::DecodeTable)) + align_up(active * s.F * s.T * elt_bytes(s));
+}
+
+moe_status_t validate_decode(const moe_shape_t* s) {
+  const moe_status_t st = validate(s);
+  if (st != MOE_OK) return st;
+  if (s->T > moe::kDecodeTokens) return MOE_ERR_UNSUPPORTED;
+  return moe::decode_lds_bytes((int)elt_bytes(*s), s->T, s->d, s->E) <= moe::kDecodeLds ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+moe_status_t decode_impl(const moe_shape_t* s, const void* x, const void* norm_w, float eps, const void* w_router,
+                         const float* bias, int32_t* topk_ids, float* topk_w, const void* w_gate, const void* w_up,
+                         const void* w_down, const float* s_gate, const float* s_up, const float* s_down,
+                         const void* res, float scale, void* out, void* workspace, size_t ws_bytes,
+                         hipStream_t stream) {
+  const moe_status_t st = validate_decode(s);
+  if (st != MOE_OK) return st;
+  if (!x || !w_gate || !w_up || !w_down || !out || !workspace) return MOE_ERR_NULL_PTR;
+  if (w_router == nullptr && (topk_ids == nullptr || topk_w == nullptr)) return MOE_ERR_NULL_PTR;
+  if (w_router == nullptr && bias != nullptr) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || (norm_w != nullptr && (!(eps > 0.f) || !std::isfinite(eps)))) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < decode_ws(*s)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned({x, norm_w, w_router, w_gate, w_up, w_down, s_gate, s_up, s_down, res, out}, 16) ||
+      !aligned({bias, topk_ids, topk_w}, 4) || !aligned({workspace}, kAlign))
+    return MOE_ERR_INVALID_ARG;
+  moe::DecodeArgs a{};
+  a.x = x;
+  a.norm_w = norm_w;
+  a.w_router = w_router;
+  a.bias = bias;
+  a.ids = topk_ids;
+  a.w = topk_w;
+  a.w_gate = w_gate;
+  a.w_up = w_up;
+  a.w_down = w_down;
+  a.s_gate = s_gate;
+  a.s_up = s_up;
+  a.s_down = s_down;
+  a.res = res;
+  a.out = out;
+  a.table = static_cast<moe::DecodeTable*>(workspace);
+  a.h = static_cast<char*>(workspace) + align_up(sizeof(moe::DecodeTable));
+  a.T = s->T;
+  a.d = s->d;
+  a.E = s->E;
+  a.k = s->k;
+  a.F = s->F;
+  a.blocked16 = s->weight_layout == MOE_LAYOUT_BLOCKED16;
+  a.eps = eps;
+  a.scale = scale;
+  return hip_status(moe::launch_decode(s->dtype, a, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -1084,6 +1178,160 @@ moe_status_t moe_backward(const moe_shape_t* s, const void* x, const void* w_rou
                                                  s->k, s->d, s->E, dx, moe::RouteFinish{}, stream));
   return enqueue_route_backward(*s, b, x, w_router, topk_ids, topk_w, dtopk_w, dx_perm, disp->row_of, dx, dw_router,
                                 dbias, ws, stream);
+}
+
+moe_status_t moe_norm(const moe_shape_t* s, const void* x, const void* w, float eps, void* n, hipStream_t stream) {
+  const moe_status_t st = validate_norm(s, eps);
+  if (st != MOE_OK) return st;
+  if (!x || !w || !n) return MOE_ERR_NULL_PTR;
+  if (!aligned({x, w, n}, 16)) return MOE_ERR_INVALID_ARG;
+  moe::ResidualArgs a{};
+  a.res = x;
+  a.next_w = w;
+  a.n = n;
+  a.T = s->T;
+  a.d = s->d;
+  a.eps = eps;
+  return hip_status(moe::launch_residual(s->dtype, a, stream));
+}
+
+moe_status_t moe_norm_backward(const moe_shape_t* s, const void* x, const void* w, float eps, const void* dn,
+                               const void* dres, void* dx, void* dw, void* workspace, size_t ws_bytes,
+                               hipStream_t stream) {
+  const moe_status_t st = validate_norm(s, eps);
+  if (st != MOE_OK) return st;
+  if (!x || !w || !dn || !dx || !workspace) return MOE_ERR_NULL_PTR;
+  if (ws_bytes < residual_ws(*s)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned({x, w, dn, dres, dx, dw}, 16) || !aligned({workspace}, kAlign)) return MOE_ERR_INVALID_ARG;
+  moe::ResidualBackwardArgs a{};
+  a.x = x;
+  a.next_w = w;
+  a.dout = dres;
+  a.dn = dn;
+  a.dres = dx;
+  a.dnext_w = dw;
+  a.part = static_cast<float*>(workspace);
+  a.T = s->T;
+  a.d = s->d;
+  a.eps = eps;
+  return hip_status(moe::launch_residual_backward(s->dtype, a, stream));
+}
+
+moe_status_t moe_residual(const moe_shape_t* s, const moe_residual_t* r, const void* res, const void* y,
+                          const void* post_w, const void* gate, const uint64_t* rng, const void* next_w, void* out,
+                          void* n, hipStream_t stream) {
+  const moe_status_t st = validate_residual(s, r, gate, rng);
+  if (st != MOE_OK) return st;
+  if (!res || !y || !out) return MOE_ERR_NULL_PTR;
+  if ((next_w == nullptr) != (n == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!aligned({res, y, post_w, next_w, out, n}, 16) || !gate_aligned(*s, *r, gate)) return MOE_ERR_INVALID_ARG;
+  moe::ResidualArgs a{};
+  a.res = res;
+  a.y = y;
+  a.post_w = post_w;
+  a.gate = gate;
+  a.next_w = next_w;
+  a.out = out;
+  a.n = n;
+  a.T = s->T;
+  a.d = s->d;
+  a.gate_full = r->gate == MOE_GATE_FULL;
+  a.eps = r->eps;
+  a.scale = r->scale;
+  a.threshold = dropout_threshold(r->dropout);
+  a.keep_scale = dropout_scale(a.threshold);
+  a.rng = a.threshold != 0 ? rng : nullptr;
+  return hip_status(moe::launch_residual(s->dtype, a, stream));
+}
+
+moe_status_t moe_residual_workspace_size(const moe_shape_t* s, size_t* bytes) {
+  const moe_status_t st = validate_norm(s, 1.f);
+  if (st != MOE_OK) return st;
+  if (bytes == nullptr) return MOE_ERR_NULL_PTR;
+  *bytes = residual_ws(*s);
+  return MOE_OK;
+}
+
+moe_status_t moe_residual_backward(const moe_shape_t* s, const moe_residual_t* r, const void* out, const void* y,
+                                   const void* post_w, const void* gate, const uint64_t* rng, const void* next_w,
+                                   const void* dout, const void* dn, void* dres, void* dy, void* dgate,
+                                   void* dpost_w, void* dnext_w, void* workspace, size_t ws_bytes,
+                                   hipStream_t stream) {
+  const moe_status_t st = validate_residual(s, r, gate, rng);
+  if (st != MOE_OK) return st;
+  if (!y || !dres || !dy || !workspace) return MOE_ERR_NULL_PTR;
+  if ((next_w == nullptr) != (dn == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (next_w != nullptr && out == nullptr) return MOE_ERR_NULL_PTR;
+  if (next_w == nullptr && dout == nullptr) return MOE_ERR_NULL_PTR;
+  if ((dgate != nullptr && r->gate == MOE_GATE_NONE) || (dpost_w != nullptr && post_w == nullptr) ||
+      (dnext_w != nullptr && next_w == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < residual_ws(*s)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned({out, y, post_w, next_w, dout, dn, dres, dy, dpost_w, dnext_w}, 16) || !gate_aligned(*s, *r, gate) ||
+      !gate_aligned(*s, *r, dgate) || !aligned({workspace}, kAlign))
+    return MOE_ERR_INVALID_ARG;
+  moe::ResidualBackwardArgs a{};
+  a.x = out;
+  a.y = y;
+  a.post_w = post_w;
+  a.gate = gate;
+  a.next_w = next_w;
+  a.dout = dout;
+  a.dn = dn;
+  a.dres = dres;
+  a.dy = dy;
+  a.dgate = dgate;
+  a.dpost_w = dpost_w;
+  a.dnext_w = dnext_w;
+  a.part = static_cast<float*>(workspace);
+  a.T = s->T;
+  a.d = s->d;
+  a.gate_full = r->gate == MOE_GATE_FULL;
+  a.eps = r->eps;
+  a.scale = r->scale;
+  a.threshold = dropout_threshold(r->dropout);
+  a.keep_scale = dropout_scale(a.threshold);
+  a.rng = a.threshold != 0 ? rng : nullptr;
+  return hip_status(moe::launch_residual_backward(s->dtype, a, stream));
+}
+
+moe_status_t moe_dropout(const void* x, int64_t n, int dtype, float p, const uint64_t* rng, void* out,
+                         hipStream_t stream) {
+  if (n < 0 || (dtype != MOE_F32 && dtype != MOE_BF16) || !(p >= 0.f && p < 1.f)) return MOE_ERR_INVALID_ARG;
+  if (n == 0) return MOE_OK;
+  if (!x || !out || !rng) return MOE_ERR_NULL_PTR;
+  if (!aligned({x, out}, 16) || !aligned({rng}, 8)) return MOE_ERR_INVALID_ARG;
+  const unsigned t = dropout_threshold(p);
+  return hip_status(moe::launch_dropout(dtype, x, n, t, dropout_scale(t), rng, out, stream));
+}
+
+moe_status_t moe_decode_workspace_size(const moe_shape_t* s, size_t* bytes) {
+  const moe_status_t st = validate_decode(s);
+  if (st != MOE_OK) return st;
+  if (bytes == nullptr) return MOE_ERR_NULL_PTR;
+  *bytes = decode_ws(*s);
+  return MOE_OK;
+}
+
+moe_status_t moe_decode(const moe_shape_t* s, const void* x, const void* norm_w, float eps, const void* w_router,
+                        const float* bias, int32_t* topk_ids, float* topk_w, const void* w_gate, const void* w_up,
+                        const void* w_down, const void* res, float scale, void* out, void* workspace,
+                        size_t ws_bytes, hipStream_t stream) {
+  return decode_impl(s, x, norm_w, eps, w_router, bias, topk_ids, topk_w, w_gate, w_up, w_down, nullptr, nullptr,
+                     nullptr, res, scale, out, workspace, ws_bytes, stream);
+}
+
+moe_status_t moe_decode_fp8(const moe_shape_t* s, const void* x, const void* norm_w, float eps,
+                            const void* w_router, const float* bias, int32_t* topk_ids, float* topk_w,
+                            const uint8_t* w_gate, const uint8_t* w_up, const uint8_t* w_down, const float* s_gate,
+                            const float* s_up, const float* s_down, const void* res, float scale, void* out,
+                            void* workspace, size_t ws_bytes, hipStream_t stream) {
+  const moe_status_t st = validate_decode(s);
+  if (st != MOE_OK) return st;
+  if (s->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!s_gate || !s_up || !s_down) return MOE_ERR_NULL_PTR;
+  return decode_impl(s, x, norm_w, eps, w_router, bias, topk_ids, topk_w, w_gate, w_up, w_down, s_gate, s_up, s_down,
+                     res, scale, out, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -453,6 +453,115 @@ moe_status_t moe_backward(const moe_shape_t* s, const void* x, const void* w_rou
                           float* dtopk_w, void* dw_router, float* dbias, void* dw_gate, void* dw_up, void* dw_down,
                           void* workspace, size_t ws_bytes, hipStream_t stream);
 
+/* ---- the block around the layer -------------------------------------------
+ * What stands between two blocks of a model that holds the layer: the norm
+ * before a block, and behind it the norm, gate, dropout and residual scale of its
+ * output; forward and gradients.  With r(v) = 1 / sqrt(mean(v^2) + eps) over a row:
+ *   moe_norm:      n = x r(x) w
+ *   moe_residual:  v = y r(y) post_w  (or y without post_w)
+ *                  out = res + scale sigmoid(gate) drop(v)
+ *                  n = out r(out) next_w  (with next_w: the next block's input)
+ * All in fp32 with one rounding of each output; n comes from out before its
+ * rounding.  The pass over a row is bound by memory, so all of it is one kernel.
+ * The calls use the shape's T, d and dtype (the rest only has to be valid); d up to
+ * 16384 (else MOE_ERR_UNSUPPORTED).  Pointers must be 16-byte aligned (a gate for
+ * each token, to its element; rng 8-byte; else MOE_ERR_INVALID_ARG); outputs must not
+ * overlap inputs except where said.
+ *
+ * Dropout.  Element i (of the flat array, t d + column) is kept where its 16-bit
+ * number is at least t = floor(65536 p + 1/2) (65535 at most), and is then multiplied with
+ * 65536 / (65536 - t), so that the mean is kept exactly; a dropped element
+ * gives 0 whatever it holds.  The number comes from a counter-based generator, Philox 4x32
+ * with 10 rounds: key = seed, counter = {i / 8, step} (64 bits each, low word
+ * first), half i % 8 of the four words, low half first.  No mask is stored: the
+ * gradient makes the numbers again.  rng [2] (device, uint64): {seed, step}, read
+ * when the kernel runs, so a captured graph draws a new mask on a replay where the
+ * caller has advanced step; forward and gradient of one pass need the same values. */
+typedef enum moe_gate { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_FULL = 2 } moe_gate_t;
+typedef struct moe_residual {
+  float eps;      /* of both norms, > 0                                        */
+  float scale;    /* of the residual branch, finite                            */
+  float dropout;  /* p in [0, 1); 0: none, rng is not read and may be NULL     */
+  int32_t gate;   /* moe_gate_t: no gate, one value a token [T], or all [T,d]  */
+} moe_residual_t;
+
+/* n = x r(x) w.  x, n [T,d]; w [d]. */
+moe_status_t moe_norm(const moe_shape_t* s, const void* x, const void* w, float eps, void* n, hipStream_t stream);
+
+/* Gradient of moe_norm, added to the one that reaches x beside the norm (dres, or
+ * NULL):
+ *   dx = dres + r (z - x r^2 mean(z x)),  z = dn w;   dw = sum_t dn x r
+ * dx may be dres.  dw may be NULL: not computed.  workspace of >=
+ * moe_residual_workspace_size (256-byte aligned). */
+moe_status_t moe_norm_backward(const moe_shape_t* s, const void* x, const void* w, float eps, const void* dn,
+                               const void* dres, void* dx, void* dw, void* workspace, size_t ws_bytes,
+                               hipStream_t stream);
+
+/* out and, with next_w, n (both or neither) as above.  res, y, out, n [T,d];
+ * post_w, next_w [d] or NULL; gate as r->gate says, NULL without one.  out may be
+ * res. */
+moe_status_t moe_residual(const moe_shape_t* s, const moe_residual_t* r, const void* res, const void* y,
+                          const void* post_w, const void* gate, const uint64_t* rng, const void* next_w, void* out,
+                          void* n, hipStream_t stream);
+
+/* Bytes of workspace (host) of moe_norm_backward and moe_residual_backward: the
+ * workgroups' sums of the norms' weight gradients.  Host arithmetic only. */
+moe_status_t moe_residual_workspace_size(const moe_shape_t* s, size_t* bytes);
+
+/* Gradient of moe_residual from those of out (dout, or NULL: zero) and n (dn,
+ * with next_w); `out` is what the forward call left there (read with next_w).
+ *   D = dout + r(out) (z - out r(out)^2 mean(z out)),  z = dn next_w
+ *   dres = D,  q = scale keep / (1 - p) D
+ *   dgate = sigmoid(gate) sigmoid(-gate) q v  (summed over the row for one value a token)
+ *   c = sigmoid(gate) q post_w,  dy = r(y) (c - y r(y)^2 mean(c y))  (or sigmoid(gate) q)
+ *   dpost_w = sum_t sigmoid(gate) q y r(y),  dnext_w = sum_t dn out r(out)
+ * dres, dy [T,d]; dres may be dout.  dgate, dpost_w and dnext_w may be NULL: not
+ * computed; they must be NULL without what they are the gradient of. */
+moe_status_t moe_residual_backward(const moe_shape_t* s, const moe_residual_t* r, const void* out, const void* y,
+                                   const void* post_w, const void* gate, const uint64_t* rng, const void* next_w,
+                                   const void* dout, const void* dn, void* dres, void* dy, void* dgate,
+                                   void* dpost_w, void* dnext_w, void* workspace, size_t ws_bytes,
+                                   hipStream_t stream);
+
+/* Dropout of any array of n elements (n >= 0; dtype a moe_dtype_t), as above; the
+ * same call on a gradient is the gradient.  out may be x. */
+moe_status_t moe_dropout(const void* x, int64_t n, int dtype, float p, const uint64_t* rng, void* out,
+                         hipStream_t stream);
+
+/* ---- the layer for a few tokens ---------------------------------------------
+ * moe_forward for a serving step: a whole pre-norm block in two kernels.
+ *   m = x r(x) norm_w  (or x without norm_w)
+ *   routing of m as moe_route's (w_router not NULL), or topk_ids and topk_w
+ *   out = res + scale sum_j topk_w[t,j] (silu(m W_gate^T) (m W_up^T)) W_down^T
+ * (without res: the sum alone, scaled).  The logits have fp32's accuracy; m and h
+ * are rounded to dtype for the experts' products, everything else is fp32 with one
+ * rounding of out.  Capacity and tile_rows do not matter: no entry is dropped.
+ *  - T <= 16, and x must fit in a workgroup's LDS: T d element size + 8 T E <=
+ *    145408 bytes (16 tokens of 4096 bf16 with up to 112 experts, 8 of 7168 with
+ *    256); else MOE_ERR_UNSUPPORTED, and moe_forward takes the batch.
+ *  - With w_router, topk_ids and topk_w [T,k] receive the routing, or are NULL.
+ *    Equal logits: the lower index.  A NaN logit ranks below every other; an expert
+ *    with a bias of -inf is left out, and a token that has no other gets no expert.
+ *  - Without w_router they are read.  Ids outside [0, E) have no expert; an expert
+ *    given twice counts twice.  Experts that no token has a weight other than 0 of
+ *    are not read, and a token takes nothing from an expert that it has weight 0 of,
+ *    whatever the expert's weights hold.
+ *  - The two weight orders and, in moe_decode_fp8, E4M3 weights with scales as in
+ *    moe_forward_fp8.
+ * Pointers must be 16-byte aligned (topk arrays and bias 4-byte); out may be res or x,
+ * and otherwise overlaps no input.  workspace of >= moe_decode_workspace_size
+ * (256-byte aligned; the routing and h), used by one call at a time. */
+moe_status_t moe_decode_workspace_size(const moe_shape_t* s, size_t* bytes);
+moe_status_t moe_decode(const moe_shape_t* s, const void* x, const void* norm_w, float eps, const void* w_router,
+                        const float* bias, int32_t* topk_ids, float* topk_w, const void* w_gate, const void* w_up,
+                        const void* w_down, const void* res, float scale, void* out, void* workspace,
+                        size_t ws_bytes, hipStream_t stream);
+moe_status_t moe_decode_fp8(const moe_shape_t* s, const void* x, const void* norm_w, float eps,
+                            const void* w_router, const float* bias, int32_t* topk_ids, float* topk_w,
+                            const uint8_t* w_gate, const uint8_t* w_up, const uint8_t* w_down, const float* s_gate,
+                            const float* s_up, const float* s_down, const void* res, float scale, void* out,
+                            void* workspace, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

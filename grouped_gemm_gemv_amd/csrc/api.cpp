@@ -749,11 +749,29 @@ size_t residual_ws(const moe_shape_t& s) {
   return align_up((size_t)2 * moe::residual_backward_groups(s.T, s.d) * s.d * 4);
 }
 
-// Of the layer for a few tokens: the routing, then h of the experts that may be active.
-size_t decode_ws(const moe_shape_t& s) {
+// Of the layer for a few tokens: the routing, h of the experts that may be active, and
+// the second kernel's partial sums.
+struct DecodePlan {
+  int parts;
+  int ranges, e16;  // of K and experts where the router is a kernel of its own, else 0
+  size_t h, part, logits, bytes;
+};
+DecodePlan decode_plan(const moe_shape_t& s, size_t weight_bytes) {
   const size_t active = (size_t)std::min<int64_t>(s.E, (int64_t)s.T * s.k);
-  return align_up(sizeof(moe::DecodeTable)) + align_up(active * s.F * s.T * elt_bytes(s));
+  const size_t cols = moe::decode_h_low(s.dtype, s.T) ? 2 * (size_t)s.T : s.T;
+  DecodePlan p;
+  p.parts = moe::decode_parts((int64_t)active * s.F * weight_bytes / 64, s.d, s.T);
+  p.h = align_up(sizeof(moe::DecodeTable));
+  p.part = p.h + align_up(active * s.F * cols * elt_bytes(s));
+  p.logits = p.part + (p.parts > 1 ? align_up((size_t)p.parts * s.d * moe::kDecodeTokens * 4) : 0);
+  const bool apart = (size_t)s.E * s.d * elt_bytes(s) >= (s.dtype == MOE_BF16 && cols == (size_t)s.T ? moe::kRouteApart / 4 : moe::kRouteApart);
+  p.ranges = apart ? (int)ceil_div((int64_t)s.d * elt_bytes(s) / 64, moe::kRouteBlocks) : 0;
+  p.e16 = apart ? (s.E + 15) / 16 * 16 : 0;
+  p.bytes = p.logits + align_up((size_t)p.ranges * p.e16 * moe::kDecodeTokens * 4);
+  return p;
 }
+// (E4M3 weights take no more parts than wider ones, so one size serves both)
+size_t decode_ws(const moe_shape_t& s) { return decode_plan(s, elt_bytes(s)).bytes; }
 
 moe_status_t validate_decode(const moe_shape_t* s) {
   const moe_status_t st = validate(s);
@@ -793,13 +811,22 @@ moe_status_t decode_impl(const moe_shape_t* s, const void* x, const void* norm_w
   a.res = res;
   a.out = out;
   a.table = static_cast<moe::DecodeTable*>(workspace);
-  a.h = static_cast<char*>(workspace) + align_up(sizeof(moe::DecodeTable));
+  const DecodePlan p = decode_plan(*s, s_gate != nullptr ? 1 : elt_bytes(*s));
+  a.h = static_cast<char*>(workspace) + p.h;
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part);
+  a.parts = p.parts;
+  if (w_router != nullptr && p.ranges > 0) {
+    a.logits = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.logits);
+    a.ranges = p.ranges;
+    a.e16 = p.e16;
+  }
   a.T = s->T;
   a.d = s->d;
   a.E = s->E;
   a.k = s->k;
   a.F = s->F;
   a.blocked16 = s->weight_layout == MOE_LAYOUT_BLOCKED16;
+  a.h_low = moe::decode_h_low(s->dtype, s->T);
   a.eps = eps;
   a.scale = scale;
   return hip_status(moe::launch_decode(s->dtype, a, stream));

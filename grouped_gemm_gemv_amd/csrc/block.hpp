@@ -71,7 +71,28 @@ struct DecodeTable {
   int pad[63];
   int expert[256];
   float weight[256][kDecodeTokens];
+  int arrived[4480];  // per column tile of the second kernel: workgroups that are done (zeroed by the first)
 };
+// Columns of d that a workgroup of the second kernel takes.  Up to four tokens 16, the
+// most workgroups; past them 64 where tiles and parts still fill the compute units,
+// because every tile of columns reads all of h, from L2: at the Mixtral shape one token
+// takes 118 us with 16 and 122 with 64, 8 tokens with E4M3 weights 249 and 213.
+constexpr int kDownWaves = 8, kDownMaxParts = 16;
+inline int decode_down_cols(int T, int d) { return T <= 4 || d < 256 / kDownMaxParts * 64 ? 16 : 64; }
+// How many workgroups share a tile's K: enough tiles and parts to fill the compute
+// units, with eight 64-byte chunks, its loads in flight, for each wavefront at least.
+inline int decode_parts(int64_t chunks, int d, int T) {
+  const int64_t fill = 256 / (d / decode_down_cols(T, d)), most = chunks / (8 * kDownWaves);
+  const int64_t p = fill < most ? fill : most;
+  return (int)(p < 1 ? 1 : p > kDownMaxParts ? kDownMaxParts : p);
+}
+
+// The router as a kernel of its own from this many bytes of its weights on (a quarter of it
+// for bf16 batches of more than 8 tokens, whose second terms are not kept in LDS but
+// made again), and the 64-byte blocks of K of one workgroup of it.  Measured, apart against
+// in the first kernel: 64 experts of 2048 and one token 36.0 vs 39.5 us, of 3584 and 16
+// tokens 467 vs 479; 8 experts of 4096 and one token 118.7 vs 118.7, 16 tokens 449 vs 452.
+constexpr int kRouteApart = 128 * 1024, kRouteBlocks = 32;
 
 struct DecodeArgs {
   const void* x;            // [T][d]
@@ -89,14 +110,22 @@ struct DecodeArgs {
   const void* res;          // [T][d] or null
   void* out;                // [T][d]
   DecodeTable* table;
-  void* h;                  // [active][F / KC][T][KC], KC elements in 64 bytes
+  void* h;                  // [active][F / KC][T, with h_low 2 T][KC], KC elements in 64 bytes
   int T, d, E, k, F;
   int blocked16;
+  int h_low;                // h is kept in two terms, the second in columns 8 .. 15
+  int x_low;                // so is x (set by the launcher)
+  float* logits;            // [ranges][e16][16]: decode_route_kernel's sums, or null: routed in the first kernel
+  int ranges, e16;
+  float* part;              // [d / 64][parts][64 columns x 16 tokens], where parts > 1
+  int parts;
   float eps, scale;
 };
+// Whether h is: bf16, and columns to spare.
+inline bool decode_h_low(int dtype, int T) { return dtype == 1 && T <= kDecodeTokens / 2; }
 // LDS that the first kernel needs at run time, and what a compute unit has beside its own arrays.
-constexpr size_t kDecodeLds = 158 * 1024;
+constexpr size_t kDecodeLds = 158 * 1024;  // (so d is at most 70656: 4416 tiles)
 size_t decode_lds_bytes(int elt_bytes, int T, int d, int E);
-hipError_t launch_decode(int dtype, const DecodeArgs& a, hipStream_t stream);
+hipError_t launch_decode(int dtype, const DecodeArgs& a, hipStream_t stream);  // (h_low set)
 
 }  // namespace moe

@@ -7,6 +7,7 @@
 #include "block.hpp"
 #include "device_common.hpp"
 #include "philox.hpp"
+#include "rounding.hpp"
 
 namespace moe {
 namespace {
@@ -134,7 +135,7 @@ __global__ __launch_bounds__(NT > 256 ? NT : 256) void residual_kernel(ResidualA
 #pragma unroll
         for (int j = 0; j < EPC; ++j)
           if ((keep >> j) & 1u) o[i][j] = fmaf(mul, v[j], o[i][j]);
-        static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.out) + row))[c] = narrow<Tr>(o[i]);
+        static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.out) + row))[c] = round_to<Tr>(o[i]);
       }
     }
     if (a.next_w == nullptr) continue;
@@ -154,7 +155,7 @@ __global__ __launch_bounds__(NT > 256 ? NT : 256) void residual_kernel(ResidualA
       widen<Tr>(chunk<Tr>(a.next_w, c), w);
 #pragma unroll
       for (int j = 0; j < EPC; ++j) w[j] *= o[i][j] * r;
-      static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.n) + row))[c] = narrow<Tr>(w);
+      static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.n) + row))[c] = round_to<Tr>(w);
     }
   }
 }
@@ -240,7 +241,7 @@ __global__ __launch_bounds__(NT > 256 ? NT : 256) void residual_backward_kernel(
           D[i][j] = fmaf(r1, fmaf(dn[j], w[j], -x[j] * k1), D[i][j]);
         }
       }
-      static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.dres) + row))[c] = narrow<Tr>(D[i]);
+      static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.dres) + row))[c] = round_to<Tr>(D[i]);
     }
     if (a.y == nullptr) continue;
     const float m = a.scale * a.keep_scale;
@@ -279,7 +280,7 @@ __global__ __launch_bounds__(NT > 256 ? NT : 256) void residual_backward_kernel(
           D[i][j] *= sg;
         }
         if (a.dgate != nullptr)
-          static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.dgate) + row))[c] = narrow<Tr>(dg);
+          static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.dgate) + row))[c] = round_to<Tr>(dg);
       }
 #pragma unroll
       for (int j = 0; j < EPC; ++j) {
@@ -309,7 +310,7 @@ __global__ __launch_bounds__(NT > 256 ? NT : 256) void residual_backward_kernel(
       }
 #pragma unroll
       for (int j = 0; j < EPC; ++j) D[i][j] *= mul;
-      static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.dy) + row))[c] = narrow<Tr>(D[i]);
+      static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.dy) + row))[c] = round_to<Tr>(D[i]);
     }
   }
   // this workgroup's sums: groups in order
@@ -346,77 +347,98 @@ __global__ __launch_bounds__(NT > 256 ? NT : 256) void residual_backward_kernel(
 }
 
 // A weight's gradient from the workgroups' sums [groups][d]: 16 threads take 4
-// columns each, 16 ranges of groups side by side, joined in order.
+// columns each, 64 ranges of groups side by side, eight loads of a thread in
+// flight; ranges joined in order.
+__device__ __forceinline__ void add4(float4& s, const float4& v) {
+  s.x += v.x;
+  s.y += v.y;
+  s.z += v.z;
+  s.w += v.w;
+}
 template <class Tr>
-__global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict__ part, int groups, int d,
-                                                         char* __restrict__ dpost, char* __restrict__ dnext) {
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restrict__ part, int groups, int d,
+                                                          char* __restrict__ dpost, char* __restrict__ dnext) {
   using Elt = typename Tr::T;
   char* dst = blockIdx.y == 0 ? dpost : dnext;
   if (dst == nullptr) return;
-  __shared__ float4 sums[16][16];
+  __shared__ float4 sums[64][16], joined[8][16];
   const int q = threadIdx.x & 15, range = threadIdx.x >> 4;
   const int c = ((int)blockIdx.x * 16 + q) * 4;
-  const int per = (groups + 15) / 16, g0 = range * per, g1 = min(groups, g0 + per);
   const float* src = part + (size_t)blockIdx.y * groups * d + c;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int g = g0; g < g1; ++g) {
-    const float4 v = *reinterpret_cast<const float4*>(src + (size_t)g * d);
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
+  for (int g0 = range; g0 < groups; g0 += 64 * 8) {
+    float4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = g0 + i * 64 < groups ? *reinterpret_cast<const float4*>(src + (size_t)(g0 + i * 64) * d)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) add4(s, v[i]);
   }
   sums[range][q] = s;
   __syncthreads();
-  if (range != 0) return;
-  for (int i = 1; i < 16; ++i) {
-    const float4 v = sums[i][q];
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
+  if (range < 8) {
+    s = sums[range * 8][q];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) add4(s, sums[range * 8 + i][q]);
+    joined[range][q] = s;
   }
+  __syncthreads();
+  if (range != 0) return;
+  s = joined[0][q];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) add4(s, joined[i][q]);
   store4<Tr>(dst + (size_t)c * sizeof(Elt), s.x, s.y, s.z, s.w);
 }
 
-// out = keep x / (1 - p): eight elements for each call of the generator.  out may be x.
+// out = keep x / (1 - p): eight elements for each call of the generator, kDropBlocks
+// such blocks of a thread, loaded first.  out may be x.
+constexpr int kDropBlocks = 2;
 template <class Tr>
 __global__ __launch_bounds__(256) void dropout_kernel(const char* x, int64_t n, unsigned threshold, float keep_scale,
                                                       const uint64_t* rng, char* out) {
   using Elt = typename Tr::T;
   constexpr int P = 8 / Tr::EPC;  // 16-byte chunks of a block
   const uint64_t seed = rng[0], step = rng[1];
-  const int64_t blocks = (n + 7) / 8, full = n / 8;
-  for (int64_t b = (int64_t)blockIdx.x * 256 + threadIdx.x; b < blocks; b += (int64_t)gridDim.x * 256) {
-    if (b < full) {
-      uint4 c[P];
+  const int64_t full = n / 8, stride = (int64_t)gridDim.x * (256 * kDropBlocks);
+  for (int64_t b0 = (int64_t)blockIdx.x * (256 * kDropBlocks) + threadIdx.x; b0 < full; b0 += stride) {
+    uint4 c[kDropBlocks][P];
 #pragma unroll
-      for (int p = 0; p < P; ++p) c[p] = reinterpret_cast<const uint4*>(x)[b * P + p];
+    for (int i = 0; i < kDropBlocks; ++i)
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        c[i][p] = reinterpret_cast<const uint4*>(x)[min(b0 + i * 256, full - 1) * P + p];
+#pragma unroll
+    for (int i = 0; i < kDropBlocks; ++i) {
+      const int64_t b = b0 + i * 256;
       const Philox r = philox((uint64_t)b, step, seed);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         float v[Tr::EPC];
-        widen<Tr>(c[p], v);
+        widen<Tr>(c[i][p], v);
 #pragma unroll
         for (int j = 0; j < Tr::EPC; ++j) v[j] = r.half(p * Tr::EPC + j) >= threshold ? v[j] * keep_scale : 0.f;
-        reinterpret_cast<uint4*>(out)[b * P + p] = narrow<Tr>(v);
+        if (b < full) reinterpret_cast<uint4*>(out)[b * P + p] = round_to<Tr>(v);
       }
-    } else {  // the last, shorter block
-      const Philox r = philox((uint64_t)b, step, seed);
-      for (int j = 0; j < (int)(n - full * 8); ++j) {
-        const bool keep = r.half(j) >= threshold;
-        const int64_t i = full * 8 + j;
-        if constexpr (sizeof(Elt) == 2) {
-          const float v = bf16_to_f32(reinterpret_cast<const uint16_t*>(x)[i]);
-          reinterpret_cast<uint16_t*>(out)[i] = (uint16_t)(keep ? f32_to_bf16(v * keep_scale) : 0u);
-        } else {
-          reinterpret_cast<float*>(out)[i] = keep ? reinterpret_cast<const float*>(x)[i] * keep_scale : 0.f;
-        }
+    }
+  }
+  // the last, shorter block
+  if (blockIdx.x == 0 && threadIdx.x == 0 && (n & 7) != 0) {
+    const Philox r = philox((uint64_t)full, step, seed);
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+      if (j >= (int)(n & 7)) break;
+      const bool keep = r.half(j) >= threshold;
+      const int64_t i = full * 8 + j;
+      if constexpr (sizeof(Elt) == 2) {
+        const float v = bf16_to_f32(reinterpret_cast<const uint16_t*>(x)[i]);
+        reinterpret_cast<uint16_t*>(out)[i] = (uint16_t)(keep ? f32_to_bf16(v * keep_scale) : 0u);
+      } else {
+        reinterpret_cast<float*>(out)[i] = keep ? reinterpret_cast<const float*>(x)[i] * keep_scale : 0.f;
       }
     }
   }
 }
-
 
 constexpr int kBackwardGroups = 512;
 
@@ -452,7 +474,7 @@ hipError_t residual_backward_t(const ResidualBackwardArgs& a, hipStream_t stream
   MOE_ROW_SHAPES(MOE_TRY)
 #undef MOE_TRY
   if (e != hipSuccess || (a.dpost_w == nullptr && a.dnext_w == nullptr)) return e;
-  hipLaunchKernelGGL(column_sum_kernel<Tr>, dim3(a.d / 64, 2), dim3(256), 0, stream, a.part, groups, a.d,
+  hipLaunchKernelGGL(column_sum_kernel<Tr>, dim3(a.d / 64, 2), dim3(1024), 0, stream, a.part, groups, a.d,
                      static_cast<char*>(a.dpost_w), static_cast<char*>(a.dnext_w));
   return hipGetLastError();
 }
@@ -474,8 +496,8 @@ hipError_t launch_residual_backward(int dtype, const ResidualBackwardArgs& a, hi
 
 hipError_t launch_dropout(int dtype, const void* x, int64_t n, unsigned threshold, float keep_scale,
                           const uint64_t* rng, void* out, hipStream_t stream) {
-  const int64_t blocks = (n + 7) / 8;
-  const dim3 grid((unsigned)std::min<int64_t>((blocks + 255) / 256, 1 << 14));
+  const int64_t per = 256 * kDropBlocks, blocks = (n + 7) / 8;
+  const dim3 grid((unsigned)std::min<int64_t>((blocks + per - 1) / per, 1 << 20));
   if (dtype == 1)
     hipLaunchKernelGGL(dropout_kernel<TBF16>, grid, dim3(256), 0, stream, static_cast<const char*>(x), n, threshold,
                        keep_scale, rng, static_cast<char*>(out));

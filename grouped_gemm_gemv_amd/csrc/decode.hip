@@ -12,7 +12,8 @@
 //
 //   decode_up_kernel    every workgroup norms the tokens into LDS, routes them
 //                       (all of them, each workgroup for itself: E d weights
-//                       from L2 against a launch of its own), and works units
+//                       from L2; many of them get a launch of their own,
+//                       decode_route_kernel), and works units
 //                       of 8 columns of F of an active expert: an MFMA tile of
 //                       8 gate rows above 8 up rows, K split over the
 //                       wavefronts, h = silu(g) u
@@ -24,22 +25,35 @@
 // Norm: with p = x norm_w (exact in two bf16 terms where both are bf16), the router
 // takes both terms and the experts the first, p rounded to bf16; 1 / rms is a
 // factor of each fp32 sum.  So logits have fp32's accuracy.  h is rounded to the
-// shape's type; nothing else is before the output.
+// shape's type; nothing else is before the output.  Up to 8 tokens leave half of the
+// instruction's columns idle: there, bf16 batches have the second terms of p and h (x_low,
+// h_low), so that neither rounding is seen in the output (error against 64 bits at the
+// Mixtral shape T = 1: 0.0016 instead of 0.0025, the output's own rounding).
 #include <algorithm>
+#include <type_traits>
 
 #include "block.hpp"
 #include "device_common.hpp"
+#include "rounding.hpp"
 
 namespace moe {
 namespace {
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
-// Weights: read once, by one workgroup.
-__device__ __forceinline__ uint4 load_stream(const char* p) {
-  return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
-}
 __device__ __forceinline__ uint4 load16(const char* p) { return *reinterpret_cast<const uint4*>(p); }
+// Weights: read once, by one workgroup, past the caches where they are blocked (a load is
+// 512 bytes or 1 KB in one piece): 8 tokens of the Mixtral shape take 391 us so and 423
+// with the default policy.  From row-major weights a load takes half a line of each of
+// 16 rows, and the next load finds the other half where the line was kept: 64 experts and
+// 16 tokens 184 us, 197 past the caches.
+template <bool B16>
+__device__ __forceinline__ uint4 load_weights(const char* p) {
+  if constexpr (B16)
+    return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
+  else
+    return load16(p);
+}
 
 // Eight OCP E4M3 codes to the bf16 values they are exactly.
 __device__ __forceinline__ uint4 widen8(unsigned lo, unsigned hi) {
@@ -56,21 +70,23 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
 }
 
-constexpr int kWaves = 8;        // wavefronts of either kernel
+constexpr int kWaves = 8;        // wavefronts of the first kernel
 constexpr int kDepth = 8;        // weight loads of a wavefront in flight
+constexpr int kScaleUnits = 64;  // units whose scales wait in LDS
 constexpr int kUnitCols = 8;     // columns of F of a unit
 constexpr int kMaxGrid = 256;    // workgroups of the first kernel: one for each compute unit
-constexpr size_t kRedBytes = 2 * kWaves * 1024;
+constexpr int kMaxPieces = 160;  // rows of x in pieces of 64 x 16 bytes: T d element size / 1024 + T
+constexpr size_t kRedBytes = 2 * kWaves * 1024, kScaleBytes = kScaleUnits * 16 * 4;
 
 // Storage of the weights: bytes from one row, and from one 64-byte piece of a row, to
 // the next.
+template <bool B16>
 struct Rows {
   size_t row_bytes;
-  int blocked;
   __device__ __forceinline__ size_t at(int row) const {
-    return blocked ? (size_t)(row >> 4) * 16 * row_bytes + (size_t)(row & 15) * 64 : (size_t)row * row_bytes;
+    return B16 ? (size_t)(row >> 4) * 16 * row_bytes + (size_t)(row & 15) * 64 : (size_t)row * row_bytes;
   }
-  __device__ __forceinline__ int step() const { return blocked ? 1024 : 64; }
+  static constexpr int step = B16 ? 1024 : 64;
 };
 
 template <class Tr, bool Q>
@@ -83,19 +99,96 @@ __device__ __forceinline__ f32x4_t mma_chunk(const uint4& w, const uint4 (&b)[Q 
   }
 }
 
-// Q: E4M3 weights.  NE: 16-expert tiles of the router at a time.
-template <class Tr, bool Q, int NE>
+// Sum and maximum over a wavefront without LDS: sixteen lanes by exchanges inside the
+// registers, then the four sixteens in order.
+template <class F>
+__device__ __forceinline__ float wave_fold(float v, F&& op) {
+  const auto dpp = [&](auto ctrl) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  v = op(v, dpp(std::integral_constant<int, 0xB1>{}));   // quad_perm 1 0 3 2
+  v = op(v, dpp(std::integral_constant<int, 0x4E>{}));   // quad_perm 2 3 0 1
+  v = op(v, dpp(std::integral_constant<int, 0x141>{}));  // row_half_mirror
+  v = op(v, dpp(std::integral_constant<int, 0x140>{}));  // row_mirror
+  const auto lane = [&](int l) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), l)); };
+  return op(op(lane(0), lane(16)), op(lane(32), lane(48)));
+}
+
+// What rounding left of fp32 values: the second terms.
+template <class Tr>
+__device__ __forceinline__ uint4 low_terms(float* v, const uint4& rounded) {
+  float r[Tr::EPC];
+  widen<Tr>(rounded, r);
+#pragma unroll
+  for (int j = 0; j < Tr::EPC; ++j) v[j] -= r[j];
+  return round_to<Tr>(v);
+}
+
+// Logits apart, where the router's weights are too many for every workgroup to read
+// (launch_decode): 16 experts and kRouteBlocks 64-byte blocks of K for a workgroup,
+// four loads of a wavefront side by side; sums [range][experts][16 tokens], before 1 / rms
+// and the bias.
+template <class Tr>
+__global__ __launch_bounds__(64 * kWaves) void decode_route_kernel(DecodeArgs a) {
+  using Elt = typename Tr::T;
+  constexpr int EB = sizeof(Elt), U = kRouteBlocks / kWaves;
+  __shared__ float part[kWaves][256];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tok = lane & 15, piece = lane >> 4;
+  const size_t xrow = (size_t)a.d * EB;
+  const int blocks = a.d * EB / 64, b0 = (int)blockIdx.x * kRouteBlocks + wave * U, e0 = (int)blockIdx.y * 16;
+  const bool normed = a.norm_w != nullptr;
+  uint4 xv[U], gv[U], wv[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const size_t o = (size_t)min(b0 + u, blocks - 1) * 64 + piece * 16;
+    wv[u] = load16(static_cast<const char*>(a.w_router) + (size_t)min(e0 + tok, a.E - 1) * xrow + o);
+    xv[u] = load16(static_cast<const char*>(a.x) + (size_t)min(tok, a.T - 1) * xrow + o);
+    if (normed) gv[u] = load16(static_cast<const char*>(a.norm_w) + o);
+  }
+  f32x4_t acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (b0 + u >= blocks) continue;
+    if (normed) {
+      float x[Tr::EPC], g[Tr::EPC];
+      widen<Tr>(xv[u], x);
+      widen<Tr>(gv[u], g);
+#pragma unroll
+      for (int j = 0; j < Tr::EPC; ++j) g[j] *= x[j];
+      const uint4 hi = round_to<Tr>(g);
+      acc = mma16<Tr>(wv[u], hi, acc);
+      if constexpr (EB == 2) acc = mma16<Tr>(wv[u], low_terms<Tr>(g, hi), acc);
+    } else {
+      acc = mma16<Tr>(wv[u], xv[u], acc);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) part[wave][(piece * 4 + r) * 16 + tok] = acc[r];
+  __syncthreads();
+  if (threadIdx.x >= 256) return;
+  float s = part[0][threadIdx.x];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) s += part[w][threadIdx.x];
+  a.logits[((size_t)blockIdx.x * a.e16 + e0) * kDecodeTokens + threadIdx.x] = s;
+}
+
+// Q: E4M3 weights.  B16: the blocked order.  NE: 16-expert tiles of the router at a time; NQ: experts of a lane in
+// the choice.
+template <class Tr, bool Q, bool B16, int NE, int NQ>
 __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
   using Elt = typename Tr::T;
   constexpr int EB = sizeof(Elt), WB = Q ? 1 : EB, KB = 64 / EB, NB = Q ? 2 : 1;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  __shared__ float part_sq[kWaves][kDecodeTokens];
+  __shared__ float part_sq[kMaxPieces];
   __shared__ int list[256], wave_count[4];
+  __shared__ uint8_t chosen[256];
   const int T = a.T, E = a.E, d = a.d, F = a.F;
-  char* xs = lds;                                                       // [d / KB][T][64 bytes]
-  f32x4_t* red = reinterpret_cast<f32x4_t*>(lds + (size_t)T * d * EB);  // [2][kWaves][64]
+  const size_t plane = (size_t)T * d * EB;
+  char* xs = lds;                                                       // [1, with x_low 2][d / KB][T][64 bytes]
+  f32x4_t* red = reinterpret_cast<f32x4_t*>(lds + (a.x_low ? 2 : 1) * plane);  // [2][kWaves][64]
   float* logit = reinterpret_cast<float*>(reinterpret_cast<char*>(red) + kRedBytes);  // [T][E]
   float* wt = logit + T * E;                                            // [E][T]
+  float* scales = wt + T * E;                                           // [kScaleUnits][16]
 
   const int lane = threadIdx.x & 63, tok = lane & 15, piece = lane >> 4, tc = min(tok, T - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -104,73 +197,107 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
   const int blocks = d / KB;
 
   for (int i = threadIdx.x; i < T * E; i += 64 * kWaves) wt[i] = 0.f;
+  if (threadIdx.x < 256) chosen[threadIdx.x] = 0;
 
-  // x norm_w into LDS, the tokens' squares, and the router's products
-  float sq = 0.f, inv = 1.f;
-  for (int e0 = 0; e0 == 0 || (route && e0 < E); e0 += 16 * NE) {
-    constexpr int U = NE == 1 ? 8 : 4;
+  constexpr int U = NE == 1 ? 8 : 2;
+  const bool inside = route && a.logits == nullptr;
+  const int b0 = blocks * wave / kWaves, b1 = blocks * (wave + 1) / kWaves;
+  uint4 wv[U][NE];
+  const auto load_router = [&](int e0, int u, int b) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      wv[u][i] = load16(static_cast<const char*>(a.w_router) + (size_t)min(e0 + i * 16 + tok, E - 1) * xrow +
+                        (size_t)min(b, blocks - 1) * 64 + piece * 16);
+  };
+
+  // x norm_w into LDS, and the sums of squares: a wavefront takes 1 KB of a token's row at a
+  // time, four of them side by side
+  const int chunk16 = d / Tr::EPC, per_row = (chunk16 + 63) / 64, pieces = T * per_row;
+  for (int i0 = wave; i0 < pieces; i0 += kWaves * 4) {
+    uint4 xv[4], gv[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = min(i0 + u * kWaves, pieces - 1), t = i / per_row, c = min((i - t * per_row) * 64 + lane, chunk16 - 1);
+      xv[u] = load16(static_cast<const char*>(a.x) + t * xrow + (size_t)c * 16);
+      if (normed) gv[u] = load16(static_cast<const char*>(a.norm_w) + (size_t)c * 16);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * kWaves, t = i / per_row, c = (i - t * per_row) * 64 + lane;
+      if (i >= pieces) break;
+      const bool in = c < chunk16;
+      uint4 hi = xv[u], lo = make_uint4(0, 0, 0, 0);
+      if (normed) {
+        float x[Tr::EPC], g[Tr::EPC], sq = 0.f;
+        widen<Tr>(xv[u], x);
+        widen<Tr>(gv[u], g);
+#pragma unroll
+        for (int j = 0; j < Tr::EPC; ++j) {
+          sq = fmaf(x[j], x[j], sq);
+          g[j] *= x[j];
+        }
+        sq = wave_fold(in ? sq : 0.f, [](float p, float q) { return p + q; });
+        if (lane == 0) part_sq[i] = sq;
+        hi = round_to<Tr>(g);
+        if constexpr (EB == 2) lo = low_terms<Tr>(g, hi);
+      }
+      if (in) {
+        char* to = xs + ((size_t)(c >> 2) * T + t) * 64 + (c & 3) * 16;
+        *reinterpret_cast<uint4*>(to) = hi;
+        if (a.x_low) *reinterpret_cast<uint4*>(to + plane) = lo;
+      }
+    }
+  }
+  // (behind x's loads, which answer in order)
+  if (inside) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_router(0, u, b0 + u);
+  }
+  __syncthreads();
+  float inv = 1.f;
+  if (normed) {
+    float s = 0.f;
+    for (int i = 0; i < per_row; ++i) s += part_sq[tc * per_row + i];
+    inv = rsqrtf(s / (float)d + a.eps);  // of token `tok`, in every lane
+  }
+
+  // The router: each wavefront a run of K, all experts and tokens
+  for (int e0 = 0; inside && e0 < E; e0 += 16 * NE) {
     f32x4_t acc[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int base = wave; base < blocks; base += kWaves * U) {
-      uint4 xv[U], gv[U], wv[U][NE];
+    if (e0 != 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load_router(e0, u, b0 + u);
+    }
+    for (int base = b0; base < b1; base += U) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const size_t o = (size_t)min(base + u * kWaves, blocks - 1) * 64 + piece * 16;
-        xv[u] = load16(static_cast<const char*>(a.x) + tc * xrow + o);
-        if (normed) gv[u] = load16(static_cast<const char*>(a.norm_w) + o);
-        if (route) {
+        const int b = base + u;
+        if (b >= b1) continue;
+        const char* from = xs + ((size_t)b * T + tc) * 64 + piece * 16;
+        const uint4 hi = *reinterpret_cast<const uint4*>(from);
+        uint4 lo = make_uint4(0, 0, 0, 0);
+        if (EB == 2 && normed) {
+          if (a.x_low) {
+            lo = *reinterpret_cast<const uint4*>(from + plane);
+          } else {  // no room for them: again from the inputs
+            float x[Tr::EPC], g[Tr::EPC];
+            widen<Tr>(load16(static_cast<const char*>(a.x) + tc * xrow + (size_t)b * 64 + piece * 16), x);
+            widen<Tr>(load16(static_cast<const char*>(a.norm_w) + (size_t)b * 64 + piece * 16), g);
 #pragma unroll
-          for (int i = 0; i < NE; ++i)
-            wv[u][i] = load16(static_cast<const char*>(a.w_router) + (size_t)min(e0 + i * 16 + tok, E - 1) * xrow + o);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int b = base + u * kWaves;
-        if (b >= blocks) continue;
-        uint4 hi = xv[u], lo = make_uint4(0, 0, 0, 0);
-        if (normed) {
-          float x[Tr::EPC], g[Tr::EPC];
-          widen<Tr>(xv[u], x);
-          widen<Tr>(gv[u], g);
-          if (e0 == 0) {
-#pragma unroll
-            for (int j = 0; j < Tr::EPC; ++j) sq = fmaf(x[j], x[j], sq);
-          }
-#pragma unroll
-          for (int j = 0; j < Tr::EPC; ++j) g[j] *= x[j];
-          hi = narrow<Tr>(g);
-          if constexpr (EB == 2) {
-            widen<Tr>(hi, x);
-#pragma unroll
-            for (int j = 0; j < Tr::EPC; ++j) g[j] -= x[j];
-            lo = narrow<Tr>(g);
+            for (int j = 0; j < Tr::EPC; ++j) g[j] *= x[j];
+            lo = low_terms<Tr>(g, hi);
           }
         }
-        if (e0 == 0 && tok < T) *reinterpret_cast<uint4*>(xs + ((size_t)b * T + tok) * 64 + piece * 16) = hi;
-        if (route) {
 #pragma unroll
-          for (int i = 0; i < NE; ++i) {
-            acc[i] = mma16<Tr>(wv[u][i], hi, acc[i]);
-            if (EB == 2 && normed) acc[i] = mma16<Tr>(wv[u][i], lo, acc[i]);
-          }
+        for (int i = 0; i < NE; ++i) {
+          acc[i] = mma16<Tr>(wv[u][i], hi, acc[i]);
+          if (EB == 2 && normed) acc[i] = mma16<Tr>(wv[u][i], lo, acc[i]);
         }
+        if (b + U < b1) load_router(e0, u, b + U);
       }
     }
-    if (e0 == 0 && normed) {
-      sq += __shfl_xor(sq, 16);
-      sq += __shfl_xor(sq, 32);
-      if (lane < kDecodeTokens) part_sq[wave][lane] = sq;
-    }
-    __syncthreads();
-    if (e0 == 0 && normed) {
-      float s = part_sq[0][tok];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) s += part_sq[w][tok];
-      inv = rsqrtf(s / (float)d + a.eps);  // of token `tok`, in every lane
-    }
-    if (!route) break;
     // sums of the wavefronts, two tiles at a time: wavefront w has tile w / 4, and 64
     // of its 256 logits
 #pragma unroll
@@ -191,63 +318,82 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
     }
   }
 
+  if (route && !inside) {  // decode_route_kernel's sums over ranges of K, in order
+    for (int i = threadIdx.x; i < E * kDecodeTokens; i += 64 * kWaves) {  // (expert i / 16, token i % 16 = tok)
+      float s = 0.f;
+#pragma unroll 4
+      for (int r = 0; r < a.ranges; ++r) s += a.logits[(size_t)r * a.e16 * kDecodeTokens + i];
+      if (tok < T) logit[tok * E + i / kDecodeTokens] = s * inv + (a.bias != nullptr ? a.bias[i / kDecodeTokens] : 0.f);
+    }
+    __syncthreads();
+  }
+
   const bool first = blockIdx.x == 0;
   if (route) {
-    // Top-k by rank: an expert's slot is the number of experts ahead of it (a larger
-    // logit, or an equal one at a lower index).  A NaN ranks lowest.
+    // Top-k: k times the largest logit, at the lowest index that has it; a NaN ranks
+    // lowest.  What is taken becomes a NaN, which no maximum sees.
     for (int t = wave; t < T; t += kWaves) {
-      const float* z = logit + t * E;
-      float v[4], key[4];
-      int rank[4];
+      float v[NQ], key[NQ];
+      int slot[NQ];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < NQ; ++q) {
         const int e = lane + 64 * q;
-        v[q] = e < E ? z[e] : 0.f;
-        key[q] = fmaxf(v[q], -INFINITY);
-        rank[q] = e < E ? 0 : 256;
+        v[q] = e < E ? logit[t * E + e] : 0.f;
+        key[q] = e < E ? fmaxf(v[q], -INFINITY) : NAN;
+        slot[q] = -1;
       }
-      for (int f = 0; f < E; ++f) {
-        const float zf = fmaxf(z[f], -INFINITY);
+      float top = 0.f;
+      for (int j = 0; j < a.k; ++j) {
+        float m = key[0];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (64 * q < E) rank[q] += (zf > key[q] || (zf == key[q] && f < lane + 64 * q)) ? 1 : 0;
+        for (int q = 1; q < NQ; ++q) m = fmaxf(m, key[q]);
+        m = wave_fold(m, [](float x, float y) { return fmaxf(x, y); });
+        if (j == 0) top = m;
+        bool found = false;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          const uint64_t at = __ballot(key[q] == m);
+          if (!found && at != 0) {
+            found = true;
+            if (lane == __ffsll((unsigned long long)at) - 1) {
+              slot[q] = j;
+              key[q] = NAN;
+            }
+          }
+        }
       }
-      float top = -INFINITY;
+      float ex[NQ], sum = 0.f;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (rank[q] < a.k) top = fmaxf(top, key[q]);
-#pragma unroll
-      for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-      float ex[4], sum = 0.f;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        ex[q] = rank[q] < a.k && v[q] != -INFINITY ? expf(v[q] - top) : 0.f;
+      for (int q = 0; q < NQ; ++q) {
+        ex[q] = slot[q] >= 0 && v[q] != -INFINITY ? expf(v[q] - top) : 0.f;
         sum += ex[q];
       }
-      sum = wave_sum(sum);
+      sum = wave_fold(sum, [](float x, float y) { return x + y; });
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (rank[q] >= a.k) continue;
+      for (int q = 0; q < NQ; ++q) {
+        if (slot[q] < 0) continue;
         const int e = lane + 64 * q;
         const float w = sum == 0.f ? 0.f : ex[q] / sum;  // (every expert masked by a bias of -inf)
         wt[e * T + t] = w;
-        if (first && a.ids != nullptr) a.ids[t * a.k + rank[q]] = e;
-        if (first && a.w != nullptr) a.w[t * a.k + rank[q]] = w;
+        if (w != 0.f) chosen[e] = 1;
+        if (first && a.ids != nullptr) a.ids[t * a.k + slot[q]] = e;
+        if (first && a.w != nullptr) a.w[t * a.k + slot[q]] = w;
       }
     }
   } else if ((int)threadIdx.x < T) {
     // the caller's routing: slots in order, so that an expert chosen twice has one weight
     for (int j = 0; j < a.k; ++j) {
       const int e = a.ids[threadIdx.x * a.k + j];
-      if (e >= 0 && e < E) wt[e * T + threadIdx.x] += a.w[threadIdx.x * a.k + j];
+      if (e < 0 || e >= E) continue;
+      const float w = wt[e * T + threadIdx.x] + a.w[threadIdx.x * a.k + j];
+      wt[e * T + threadIdx.x] = w;
+      if (w != 0.f) chosen[e] = 1;
     }
   }
   __syncthreads();
 
   // the experts with a weight for any token, ascending
-  bool active = false;
-  if ((int)threadIdx.x < E)
-    for (int t = 0; t < T; ++t) active = active || wt[threadIdx.x * T + t] != 0.f;
+  const bool active = threadIdx.x < 256 && chosen[threadIdx.x & 255] != 0;
   const uint64_t ballot = __ballot(active);
   if (wave < 4 && lane == 0) wave_count[wave] = __popcll(ballot);
   __syncthreads();
@@ -263,37 +409,63 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
   n_active = __builtin_amdgcn_readfirstlane(n_active);
   if (first) {
     if (threadIdx.x == 0) a.table->n_active = n_active;
+    for (int i = threadIdx.x; i < d / 16; i += 64 * kWaves) a.table->arrived[i] = 0;
     for (int i = threadIdx.x; i < n_active; i += 64 * kWaves) a.table->expert[i] = list[i];
     for (int i = threadIdx.x; i < n_active * T; i += 64 * kWaves) a.table->weight[i / T][i % T] = wt[list[i / T] * T + i % T];
   }
 
-  // ---- gate and up: units of 8 columns, dealt to the workgroups in turn
-  const int per = F / kUnitCols, total = n_active * per;
-  const int chunks = d * WB / 64;
-  const int c0 = chunks * wave / kWaves, mine = chunks * (wave + 1) / kWaves - c0;
-  const int grid = (int)gridDim.x;
-  const int units = (int)blockIdx.x < total ? (total - (int)blockIdx.x + grid - 1) / grid : 0;
-  if (units == 0) return;
-  const Rows rows{(size_t)d * WB, a.blocked16};
-  const int step = rows.step();
+  // ---- gate and up: units of 8 columns, dealt to groups of wavefronts in turn.  A group
+  // splits K; it is the whole workgroup unless that left a wavefront fewer than 2 kDepth
+  // chunks of a unit: with one round of loads between two barriers, 8 tokens with E4M3
+  // weights take 237 us and not 213 at the Mixtral shape.  A round then ends one unit at
+  // the most, and the code behind a unit's end stands once (inlined at each load the
+  // kernel was 60 KB, whose fetches took longer than the first loads of data)
+  const int per = F / kUnitCols, total = n_active * per, chunks = d * WB / 64;
+  const int split = chunks >= 16 * kDepth ? 8 : chunks >= 8 * kDepth ? 4 : chunks >= 4 * kDepth ? 2 : 1;
+  const int groups = kWaves / split, group = wave / split, part = wave % split;
+  const int c0 = chunks * part / split, mine = chunks * (part + 1) / split - c0;
+  const int round = max(mine, kDepth);  // (a narrow unit is padded to a round)
+  const int stride = (int)gridDim.x * groups, u0 = (int)blockIdx.x * groups;
+  const int turns = u0 < total ? (total - u0 + stride - 1) / stride : 0;  // of the workgroup's first group: the most
+  const int units = u0 + group < total ? (total - u0 - group + stride - 1) / stride : 0;
+  if (turns == 0) return;
+  const Rows<B16> rows{(size_t)d * WB};
+  constexpr int step = Rows<B16>::step;
   const char* base = static_cast<const char*>(tok < 8 ? a.w_gate : a.w_up) + piece * 16 + (size_t)c0 * step;
   const auto unit_at = [&](int i) {
-    const int u = (int)blockIdx.x + i * grid, e = list[u / per];
+    const int u = u0 + group + i * stride, e = list[u / per];
     return base + (size_t)e * F * rows.row_bytes + rows.at((u % per) * kUnitCols + (tok & 7));
   };
-  // a unit's sums of all wavefronts to h, by one wavefront, each unit another's turn
-  const auto finish = [&](int i, f32x4_t acc) {
-    red[((i & 1) * kWaves + wave) * 64 + lane] = acc;
+  // E4M3: the scales of the next turns to LDS, 8 of gate's and 8 of up's for each unit, so
+  // that finishing one waits for no load
+  const auto fetch_scales = [&](int i0) {
+    for (int j = threadIdx.x; j < kScaleUnits * 16; j += 64 * kWaves) {
+      const int v = j >> 4, u = u0 + v % groups + (i0 + v / groups) * stride;
+      if (u < total) scales[j] = ((j & 8) ? a.s_up : a.s_gate)[(size_t)list[u / per] * F + (u % per) * kUnitCols + (j & 7)];
+    }
+  };
+  if constexpr (Q) {
+    fetch_scales(0);
+    __syncthreads();
+  }
+  // turn i's sums, which the wavefronts have left in LDS, to h: by one wavefront of each
+  // group, each turn another
+  const auto finish = [&](int i) {
+    if (Q && i != 0 && i % (kScaleUnits / groups) == 0) {  // every unit before has had its scales when all are here
+      __syncthreads();
+      fetch_scales(i);
+    }
     lds_barrier();
-    if (wave != i % kWaves) return;
-    f32x4_t s = red[(i & 1) * kWaves * 64 + lane];
+    if (part != i % split || i >= units) return;
+    const f32x4_t* from = red + ((i & 1) * kWaves + group * split) * 64 + lane;
+    f32x4_t s = from[0];
+    for (int w = 1; w < split; ++w) s += from[w * 64];
+    const int u = u0 + group + i * stride, n = u / per, f0 = (u % per) * kUnitCols;
+    // with low terms, columns 8 .. 15 hold those of tokens 0 .. 7
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) s += red[((i & 1) * kWaves + w) * 64 + lane];
-    const int u = (int)blockIdx.x + i * grid, n = u / per, f0 = (u % per) * kUnitCols;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) s[r] *= inv;
+    for (int r = 0; r < 4; ++r) s[r] = (a.x_low ? s[r] + __shfl_down(s[r], 8) : s[r]) * inv;
     if constexpr (Q) {
-      const float4 sc = *reinterpret_cast<const float4*>((piece < 2 ? a.s_gate : a.s_up) + (size_t)list[n] * F + f0 + (piece & 1) * 4);
+      const float4 sc = *reinterpret_cast<const float4*>(scales + ((i * groups + group) % kScaleUnits) * 16 + piece * 4);
       s[0] *= sc.x, s[1] *= sc.y, s[2] *= sc.z, s[3] *= sc.w;
     }
     // rows 0..7 (pieces 0, 1) are the gate's columns, rows 8..15 the same columns of up
@@ -305,99 +477,132 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
     }
     if (piece < 2 && tok < T) {
       const int f = f0 + piece * 4;
-      store4<Tr>(static_cast<char*>(a.h) + (((size_t)n * (F / KB) + f / KB) * T + tok) * 64 + (f % KB) * EB, hv[0], hv[1],
-                 hv[2], hv[3]);
+      char* to = static_cast<char*>(a.h) + (((size_t)n * (F / KB) + f / KB) * (a.h_low ? 2 * T : T) + tok) * 64 + (f % KB) * EB;
+      store4<Tr>(to, hv[0], hv[1], hv[2], hv[3]);
+      if (EB == 2 && a.h_low) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float hi = bf16_to_f32(f32_to_bf16(hv[r]));
+          hv[r] = fabsf(hi) < INFINITY ? hv[r] - hi : 0.f;
+        }
+        store4<Tr>(to + (size_t)T * 64, hv[0], hv[1], hv[2], hv[3]);
+      }
     }
   };
-  if (mine == 0) {  // (fewer chunks than wavefronts)
-    for (int i = 0; i < units; ++i) finish(i, f32x4_t{0.f, 0.f, 0.f, 0.f});
-    return;
+  int done = 0;  // turns finished
+  if (units != 0) {
+    // kDepth loads in flight, across units; behind the last unit the cursor repeats its
+    // last chunk
+    int li = 0, lc = 0;
+    const char *lp = unit_at(0), *next = unit_at(min(1, units - 1));
+    bool fetched = false;
+    const auto load = [&]() {
+      const uint4 v = load_weights<B16>(lp);
+      if (++lc < mine) lp += step;
+      if (lc == round && li + 1 < units) {
+        ++li;
+        lc = 0;
+        lp = next;
+        fetched = true;
+      }
+      return v;
+    };
+    const int col = a.x_low ? min(tok & 7, T - 1) : tc;
+    const char* xlane = xs + (a.x_low && tok >= 8 ? plane : 0) + (size_t)c0 * NB * T * 64 +
+                        (Q ? ((size_t)(piece >> 1) * T + col) * 64 + (piece & 1) * 32 : (size_t)col * 64 + piece * 16);
+    int uc = 0;
+    bool ended = false;
+    f32x4_t acc{0.f, 0.f, 0.f, 0.f};
+    const auto work = [&](const uint4& w) {
+      if (uc < mine) {
+        uint4 b[NB];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) b[j] = *reinterpret_cast<const uint4*>(xlane + (size_t)uc * NB * T * 64 + j * 16);
+        acc = mma_chunk<Tr, Q>(w, b, acc);
+      }
+      if (++uc == round) {
+        red[((done & 1) * kWaves + wave) * 64 + lane] = acc;
+        uc = 0;
+        acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        ended = true;
+      }
+    };
+    uint4 ring[kDepth];
+#pragma unroll
+    for (int j = 0; j < kDepth; ++j) ring[j] = load();
+    for (int left = units * round; left > 0; left -= kDepth) {
+      if (fetched) {
+        next = unit_at(min(li + 1, units - 1));
+        fetched = false;
+      }
+#pragma unroll
+      for (int j = 0; j < kDepth; ++j) {
+        if (j < left) work(ring[j]);
+        ring[j] = load();
+      }
+      if (ended) {
+        finish(done++);
+        ended = false;
+      }
+    }
   }
-  // kDepth loads in flight, across units; behind the last unit the cursor repeats its
-  // last chunk
-  int li = 0, lc = 0;
-  const char* lp = unit_at(0);
-  const auto load = [&]() {
-    const uint4 v = load_stream(lp);
-    if (++lc < mine) {
-      lp += step;
-    } else if (li + 1 < units) {
-      lp = unit_at(++li);
-      lc = 0;
-    } else {
-      --lc;
-    }
-    return v;
-  };
-  const char* xlane = xs + (Q ? ((size_t)(piece >> 1) * T + tc) * 64 + (piece & 1) * 32 : (size_t)tc * 64 + piece * 16) +
-                      (size_t)c0 * NB * T * 64;
-  int ui = 0, uc = 0;
-  f32x4_t acc{0.f, 0.f, 0.f, 0.f};
-  const auto work = [&](const uint4& w) {
-    uint4 b[NB];
-#pragma unroll
-    for (int j = 0; j < NB; ++j) b[j] = *reinterpret_cast<const uint4*>(xlane + (size_t)uc * NB * T * 64 + j * 16);
-    acc = mma_chunk<Tr, Q>(w, b, acc);
-    if (++uc == mine) {
-      finish(ui, acc);
-      ++ui;
-      uc = 0;
-      acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
-  };
-  uint4 ring[kDepth];
-#pragma unroll
-  for (int j = 0; j < kDepth; ++j) ring[j] = load();
-  int left = units * mine;
-  for (; left >= kDepth; left -= kDepth) {
-#pragma unroll
-    for (int j = 0; j < kDepth; ++j) {
-      work(ring[j]);
-      ring[j] = load();
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kDepth; ++j)
-    if (j < left) work(ring[j]);
+  for (; done < turns; ++done) finish(done);  // (others' barriers)
 }
 
-template <class Tr, bool Q>
-__global__ __launch_bounds__(64 * kWaves) void decode_down_kernel(DecodeArgs a) {
+// One part of the K range of 16 NR columns of d: out's columns where the tile has one part,
+// else partial sums, which the workgroup that is done last adds up in the parts'
+// order.  The columns share each load of h, which every tile reads whole.
+template <class Tr, bool Q, bool B16, int NR>
+__global__ __launch_bounds__(64 * kDownWaves) void decode_down_kernel(DecodeArgs a) {
   using Elt = typename Tr::T;
-  constexpr int EB = sizeof(Elt), WB = Q ? 1 : EB, NB = Q ? 2 : 1;
-  __shared__ f32x4_t red[kWaves][64];
+  constexpr int EB = sizeof(Elt), WB = Q ? 1 : EB, NB = Q ? 2 : 1, D = NR == 1 ? 8 : 4, kCols = NR * 16;
+  __shared__ f32x4_t red[kDownWaves][NR][64];
   __shared__ float wts[256][kDecodeTokens];
-  __shared__ float scale[Q ? 256 : 1][16];
+  __shared__ float scale[Q ? 256 : 1][kCols];
   __shared__ int list[256];
+  __shared__ int last;
   const int T = a.T, d = a.d, F = a.F;
   const int lane = threadIdx.x & 63, tok = lane & 15, piece = lane >> 4, tc = min(tok, T - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int o0 = (int)blockIdx.x * 16;
-  const int n_active = __builtin_amdgcn_readfirstlane(a.table->n_active);
-  for (int i = threadIdx.x; i < n_active; i += 64 * kWaves) list[i] = a.table->expert[i];
-  for (int i = threadIdx.x; i < n_active * kDecodeTokens; i += 64 * kWaves) {
+  const int tile = (int)blockIdx.x, part = (int)blockIdx.y, o0 = tile * kCols;
+  // the table, as much of it as there may be, without waiting for its length
+  const int most = min(a.E, T * a.k);
+  for (int i = threadIdx.x; i < most * kDecodeTokens; i += 64 * kDownWaves) {
     const int n = i / kDecodeTokens, t = i % kDecodeTokens;
-    wts[n][t] = t < T ? a.table->weight[n][t] : 0.f;
-    if constexpr (Q) scale[n][t] = a.s_down[(size_t)a.table->expert[n] * d + o0 + t];
+    wts[n][t] = a.table->weight[n][t];
+    if (t == 0) list[n] = a.table->expert[n];
   }
-  __syncthreads();
-
+  const int n_active = __builtin_amdgcn_readfirstlane(a.table->n_active);
   const int per = F * WB / 64, total = n_active * per;  // chunks of an expert, of all
-  const int i0 = (int)((long long)total * wave / kWaves), i1 = (int)((long long)total * (wave + 1) / kWaves);
-  f32x4_t sum{0.f, 0.f, 0.f, 0.f};
+  const int p0 = (int)((long long)total * part / a.parts), p1 = (int)((long long)total * (part + 1) / a.parts);
+  const int i0 = p0 + (int)((long long)(p1 - p0) * wave / kDownWaves);
+  const int i1 = p0 + (int)((long long)(p1 - p0) * (wave + 1) / kDownWaves);
+  __syncthreads();
+  if constexpr (Q) {
+    const int n0 = p0 / per, n1 = (p1 + per - 1) / per;
+    for (int i = n0 * kCols + threadIdx.x; i < n1 * kCols; i += 64 * kDownWaves)
+      scale[i / kCols][i % kCols] = a.s_down[(size_t)list[i / kCols] * d + o0 + i % kCols];
+    __syncthreads();
+  }
+
+  f32x4_t sum[NR];
+#pragma unroll
+  for (int q = 0; q < NR; ++q) sum[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   if (i0 < i1) {
-    const Rows rows{(size_t)F * WB, a.blocked16};
-    const int step = rows.step();
+    const Rows<B16> rows{(size_t)F * WB};
+    constexpr int step = Rows<B16>::step;
     const char* base = static_cast<const char*>(a.w_down) + rows.at(o0 + tok) + piece * 16;
-    const size_t expert_bytes = (size_t)d * rows.row_bytes;
-    const int bstep = T * 64 * NB;
+    const size_t tile_bytes = 16 * rows.row_bytes, expert_bytes = (size_t)d * rows.row_bytes;
+    const int cols = a.h_low ? 2 * T : T, bstep = cols * 64 * NB;
+    const int col = a.h_low ? min(tok & 7, T - 1) + (tok >> 3) * T : tc, wcol = a.h_low ? tok & 7 : tok;
     int ln = i0 / per, lc = i0 % per, li = i0;
     const char* lp = base + list[ln] * expert_bytes + (size_t)lc * step;
     const char* bp = static_cast<const char*>(a.h) + (size_t)i0 * bstep +
-                     (Q ? ((size_t)(piece >> 1) * T + tc) * 64 + (piece & 1) * 32 : (size_t)tc * 64 + piece * 16);
-    uint4 ring[kDepth], act[kDepth][NB];
+                     (Q ? ((size_t)(piece >> 1) * cols + col) * 64 + (piece & 1) * 32 : (size_t)col * 64 + piece * 16);
+    uint4 ring[D][NR], act[D][NB];
     const auto load = [&](int j) {
-      ring[j] = load_stream(lp);
+#pragma unroll
+      for (int q = 0; q < NR; ++q) ring[j][q] = load_weights<B16>(lp + q * tile_bytes);
 #pragma unroll
       for (int q = 0; q < NB; ++q) act[j][q] = load16(bp + q * 16);
       if (++li >= i1) return;  // behind the last chunk: it again
@@ -409,21 +614,29 @@ __global__ __launch_bounds__(64 * kWaves) void decode_down_kernel(DecodeArgs a) 
         lp = base + list[++ln] * expert_bytes;
       }
     };
-    int n = i0 / per, c = i0 % per;
-    f32x4_t acc{0.f, 0.f, 0.f, 0.f};
+    int n = i0 / per, c = i0 % per, since = 0;
+    f32x4_t acc[NR];
+#pragma unroll
+    for (int q = 0; q < NR; ++q) acc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     // a token that did not choose the expert takes nothing of its sum, whatever that holds
     const auto fold = [&]() {
-      const float w = wts[n][tok];
+      const float w = wts[n][wcol];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float v = acc[r];
-        if constexpr (Q) v *= scale[n][piece * 4 + r];
-        sum[r] = w != 0.f ? fmaf(w, v, sum[r]) : sum[r];
+      for (int q = 0; q < NR; ++q) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float v = acc[q][r];
+          if constexpr (Q) v *= scale[n][q * 16 + piece * 4 + r];
+          sum[q][r] = w != 0.f ? fmaf(w, v, sum[q][r]) : sum[q][r];
+        }
+        acc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
-      acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      since = 0;
     };
     const auto work = [&](int j) {
-      acc = mma_chunk<Tr, Q>(ring[j], act[j], acc);
+#pragma unroll
+      for (int q = 0; q < NR; ++q) acc[q] = mma_chunk<Tr, Q>(ring[j][q], act[j], acc[q]);
+      ++since;
       if (++c == per) {
         fold();
         ++n;
@@ -431,62 +644,117 @@ __global__ __launch_bounds__(64 * kWaves) void decode_down_kernel(DecodeArgs a) 
       }
     };
 #pragma unroll
-    for (int j = 0; j < kDepth; ++j) load(j);
+    for (int j = 0; j < D; ++j) load(j);
     int left = i1 - i0;
-    for (; left >= kDepth; left -= kDepth) {
+    for (; left >= D; left -= D) {
 #pragma unroll
-      for (int j = 0; j < kDepth; ++j) {
+      for (int j = 0; j < D; ++j) {
         work(j);
         load(j);
       }
     }
 #pragma unroll
-    for (int j = 0; j < kDepth; ++j)
+    for (int j = 0; j < D; ++j)
       if (j < left) work(j);
-    if (c != 0) fold();
+    if (since != 0) fold();
   }
-  red[wave][lane] = sum;
+#pragma unroll
+  for (int q = 0; q < NR; ++q) red[wave][q][lane] = sum[q];
   __syncthreads();
-  if (wave != 0 || tok >= T) return;
+  // thread (q, lane) has columns 16 q + 4 piece .. + 3 of token tok; with low terms
+  // their products are eight lanes on
+  const int q = wave & (NR - 1);
+  const bool mine = wave < NR && tok < T;
+  f32x4_t v{0.f, 0.f, 0.f, 0.f};
+  if (mine) {
+    v = red[0][q][lane];
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) sum += red[w][lane];
-  const size_t at = ((size_t)tok * d + o0 + piece * 4) * EB;
+    for (int w = 1; w < kDownWaves; ++w) v += red[w][q][lane];
+    if (a.h_low) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    sum[r] *= a.scale;
-    if (a.res != nullptr) {
-      const char* p = static_cast<const char*>(a.res) + at + r * EB;
-      sum[r] += EB == 2 ? bf16_to_f32(*reinterpret_cast<const uint16_t*>(p)) : *reinterpret_cast<const float*>(p);
+      for (int w = 0; w < kDownWaves; ++w) v += red[w][q][lane + 8];
     }
   }
-  store4<Tr>(static_cast<char*>(a.out) + at, sum[0], sum[1], sum[2], sum[3]);
+  if (a.parts > 1) {
+    // Stored and loaded past the caches that other dies do not share (agent scope): every
+    // wavefront's stores are done before the barrier, the count comes behind it, and
+    // nobody waits for anybody.  A fence of that scope would write back and drop all of L2.
+    float* all = a.part + ((size_t)tile * a.parts * (NR * 64) + q * 64 + lane) * 4;
+    if (mine) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        __hip_atomic_store(all + (size_t)part * (NR * 256) + r, v[r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (threadIdx.x == 0)
+      last = __hip_atomic_fetch_add(&a.table->arrived[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.parts - 1;
+    __syncthreads();
+    if (!last) return;
+    if (mine) {
+      v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int p = 0; p < a.parts; ++p)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          v[r] += __hip_atomic_load(all + (size_t)p * (NR * 256) + r, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  if (!mine) return;
+  const size_t at = ((size_t)tok * d + o0 + q * 16 + piece * 4) * EB;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    v[r] *= a.scale;
+    if (a.res != nullptr) {
+      const char* p = static_cast<const char*>(a.res) + at + r * EB;
+      v[r] += EB == 2 ? bf16_to_f32(*reinterpret_cast<const uint16_t*>(p)) : *reinterpret_cast<const float*>(p);
+    }
+  }
+  store4<Tr>(static_cast<char*>(a.out) + at, v[0], v[1], v[2], v[3]);
 }
 
-template <class Tr, bool Q>
-hipError_t decode_t(const DecodeArgs& a, hipStream_t stream) {
-  const size_t lds = decode_lds_bytes(sizeof(typename Tr::T), a.T, a.d, a.E);
+template <class Tr, bool Q, bool B16>
+hipError_t decode_t(DecodeArgs a, hipStream_t stream) {
+  constexpr int EB = sizeof(typename Tr::T);
+  size_t lds = decode_lds_bytes(EB, a.T, a.d, a.E);
+  const size_t both = lds + (size_t)a.T * a.d * EB;
+  a.x_low = a.h_low && a.norm_w != nullptr && both <= kDecodeLds;
+  if (a.x_low) lds = both;
+  if (a.logits != nullptr) {
+    hipLaunchKernelGGL(decode_route_kernel<Tr>, dim3(a.ranges, a.e16 / 16), dim3(64 * kWaves), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   const int64_t units = (int64_t)std::min(a.E, a.T * a.k) * (a.F / kUnitCols);
   const dim3 grid((unsigned)std::min<int64_t>(units, kMaxGrid));
+  const auto up = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), lds, stream, a); };
   if (a.E <= 16)
-    hipLaunchKernelGGL((decode_up_kernel<Tr, Q, 1>), grid, dim3(64 * kWaves), lds, stream, a);
+    up(decode_up_kernel<Tr, Q, B16, 1, 1>);
+  else if (a.E <= 64)
+    up(decode_up_kernel<Tr, Q, B16, 4, 1>);
   else
-    hipLaunchKernelGGL((decode_up_kernel<Tr, Q, 4>), grid, dim3(64 * kWaves), lds, stream, a);
+    up(decode_up_kernel<Tr, Q, B16, 4, 4>);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((decode_down_kernel<Tr, Q>), dim3(a.d / 16), dim3(64 * kWaves), 0, stream, a);
+  const dim3 tiles(a.d / decode_down_cols(a.T, a.d), a.parts);
+  const auto down = [&](auto kernel) { hipLaunchKernelGGL(kernel, tiles, dim3(64 * kDownWaves), 0, stream, a); };
+  if (decode_down_cols(a.T, a.d) == 16)
+    down(decode_down_kernel<Tr, Q, B16, 1>);
+  else
+    down(decode_down_kernel<Tr, Q, B16, 4>);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// x [T][d], the wavefronts' sums, logits and weights [T][E] each.
+// x [T][d], the wavefronts' sums, logits and weights [T][E] each, and scales.
 size_t decode_lds_bytes(int elt_bytes, int T, int d, int E) {
-  return (size_t)T * d * elt_bytes + kRedBytes + (size_t)8 * T * E;
+  return (size_t)T * d * elt_bytes + kRedBytes + kScaleBytes + (size_t)8 * T * E;
 }
 
 hipError_t launch_decode(int dtype, const DecodeArgs& a, hipStream_t stream) {
-  if (a.s_gate != nullptr) return decode_t<TBF16, true>(a, stream);
-  return dtype == 1 ? decode_t<TBF16, false>(a, stream) : decode_t<TF32, false>(a, stream);
+  if (a.s_gate != nullptr) return a.blocked16 ? decode_t<TBF16, true, true>(a, stream) : decode_t<TBF16, true, false>(a, stream);
+  if (dtype == 1) return a.blocked16 ? decode_t<TBF16, false, true>(a, stream) : decode_t<TBF16, false, false>(a, stream);
+  return a.blocked16 ? decode_t<TF32, false, true>(a, stream) : decode_t<TF32, false, false>(a, stream);
 }
 
 }  // namespace moe

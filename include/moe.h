@@ -537,7 +537,7 @@ moe_status_t moe_dropout(const void* x, int64_t n, int dtype, float p, const uin
  * are rounded to dtype for the experts' products, everything else is fp32 with one
  * rounding of out.  Capacity and tile_rows do not matter: no entry is dropped.
  *  - T <= 16, and x must fit in a workgroup's LDS: T d element size + 8 T E <=
- *    145408 bytes (16 tokens of 4096 bf16 with up to 112 experts, 8 of 7168 with
+ *    141312 bytes (16 tokens of 4096 bf16 with up to 80 experts, 8 of 7168 with
  *    256); else MOE_ERR_UNSUPPORTED, and moe_forward takes the batch.
  *  - With w_router, topk_ids and topk_w [T,k] receive the routing, or are NULL.
  *    Equal logits: the lower index.  A NaN logit ranks below every other; an expert

@@ -103,7 +103,7 @@ def test_residual_workspace_size():
 
 @built
 @pytest.mark.parametrize("kw,code", [
-    (dict(T=16, d=4096, E=8), 0), (dict(T=16, d=4096, E=112), 0), (dict(T=16, d=4096, E=113), 4),
+    (dict(T=16, d=4096, E=8), 0), (dict(T=16, d=4096, E=80), 0), (dict(T=16, d=4096, E=81), 4),
     (dict(T=8, d=7168, E=256), 0), (dict(T=9, d=7168, E=256), 4), (dict(T=17, d=64), 4), (dict(T=8, d=4096, dt=0), 0),
     (dict(T=16, d=4096, dt=0), 4), (dict(T=0), 1), (dict(d=96), 4), (dict(T=1, d=65536, E=8), 0),
     (dict(T=16, d=4096, C=3), 0),

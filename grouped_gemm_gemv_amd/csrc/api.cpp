@@ -764,7 +764,9 @@ DecodePlan decode_plan(const moe_shape_t& s, size_t weight_bytes) {
   p.h = align_up(sizeof(moe::DecodeTable));
   p.part = p.h + align_up(active * s.F * cols * elt_bytes(s));
   p.logits = p.part + (p.parts > 1 ? align_up((size_t)p.parts * s.d * moe::kDecodeTokens * 4) : 0);
-  const bool apart = (size_t)s.E * s.d * elt_bytes(s) >= (s.dtype == MOE_BF16 && cols == (size_t)s.T ? moe::kRouteApart / 4 : moe::kRouteApart);
+  const size_t router = (size_t)s.E * s.d * elt_bytes(s), experts = active * 3 * s.d * s.F * weight_bytes;
+  const bool apart = router >= moe::kRouteApart || experts >= moe::kDealApart ||
+                     (s.dtype == MOE_BF16 && s.T > moe::kDecodeTokens / 2 && router >= moe::kRouteApart / 4);
   p.ranges = apart ? (int)ceil_div((int64_t)s.d * elt_bytes(s) / 64, moe::kRouteBlocks) : 0;
   p.e16 = apart ? (s.E + 15) / 16 * 16 : 0;
   p.bytes = p.logits + align_up((size_t)p.ranges * p.e16 * moe::kDecodeTokens * 4);

@@ -69,6 +69,8 @@ constexpr int kDecodeTokens = 16;
 struct DecodeTable {
   int n_active;
   int pad[63];
+  int claimed;  // turns of the first kernel's deal that are taken
+  int pad2[63];
   int expert[256];
   float weight[256][kDecodeTokens];
   int arrived[4480];  // per column tile of the second kernel: workgroups that are done (zeroed by the first)
@@ -92,7 +94,10 @@ inline int decode_parts(int64_t chunks, int d, int T) {
 // made again), and the 64-byte blocks of K of one workgroup of it.  Measured, apart against
 // in the first kernel: 64 experts of 2048 and one token 36.0 vs 39.5 us, of 3584 and 16
 // tokens 467 vs 479; 8 experts of 4096 and one token 118.7 vs 118.7, 16 tokens 449 vs 452.
+// And from this many bytes of the experts that may be active on, for the deal of units that
+// it makes possible (see the first kernel's main loop).
 constexpr int kRouteApart = 128 * 1024, kRouteBlocks = 32;
+constexpr size_t kDealApart = size_t(256) << 20;
 
 struct DecodeArgs {
   const void* x;            // [T][d]
@@ -124,7 +129,7 @@ struct DecodeArgs {
 // Whether h is: bf16, and columns to spare.
 inline bool decode_h_low(int dtype, int T) { return dtype == 1 && T <= kDecodeTokens / 2; }
 // LDS that the first kernel needs at run time, and what a compute unit has beside its own arrays.
-constexpr size_t kDecodeLds = 158 * 1024;  // (so d is at most 70656: 4416 tiles)
+constexpr size_t kDecodeLds = 154 * 1024;  // (so d is at most 70656: 4416 tiles)
 size_t decode_lds_bytes(int elt_bytes, int T, int d, int E);
 hipError_t launch_decode(int dtype, const DecodeArgs& a, hipStream_t stream);  // (h_low set)
 

@@ -72,11 +72,10 @@ __device__ __forceinline__ void lds_barrier() {
 
 constexpr int kWaves = 8;        // wavefronts of the first kernel
 constexpr int kDepth = 8;        // weight loads of a wavefront in flight
-constexpr int kScaleUnits = 64;  // units whose scales wait in LDS
 constexpr int kUnitCols = 8;     // columns of F of a unit
 constexpr int kMaxGrid = 256;    // workgroups of the first kernel: one for each compute unit
 constexpr int kMaxPieces = 160;  // rows of x in pieces of 64 x 16 bytes: T d element size / 1024 + T
-constexpr size_t kRedBytes = 2 * kWaves * 1024, kScaleBytes = kScaleUnits * 16 * 4;
+constexpr size_t kRedBytes = 2 * kWaves * 1024;
 
 // Storage of the weights: bytes from one row, and from one 64-byte piece of a row, to
 // the next.
@@ -137,6 +136,7 @@ __global__ __launch_bounds__(64 * kWaves) void decode_route_kernel(DecodeArgs a)
   const size_t xrow = (size_t)a.d * EB;
   const int blocks = a.d * EB / 64, b0 = (int)blockIdx.x * kRouteBlocks + wave * U, e0 = (int)blockIdx.y * 16;
   const bool normed = a.norm_w != nullptr;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.table->claimed = 0;
   uint4 xv[U], gv[U], wv[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -182,13 +182,14 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
   __shared__ float part_sq[kMaxPieces];
   __shared__ int list[256], wave_count[4];
   __shared__ uint8_t chosen[256];
+  __shared__ int claims[8];
+  __shared__ __attribute__((aligned(16))) float scales[Q ? 4 : 1][kWaves * 16];
   const int T = a.T, E = a.E, d = a.d, F = a.F;
   const size_t plane = (size_t)T * d * EB;
   char* xs = lds;                                                       // [1, with x_low 2][d / KB][T][64 bytes]
   f32x4_t* red = reinterpret_cast<f32x4_t*>(lds + (a.x_low ? 2 : 1) * plane);  // [2][kWaves][64]
   float* logit = reinterpret_cast<float*>(reinterpret_cast<char*>(red) + kRedBytes);  // [T][E]
   float* wt = logit + T * E;                                            // [E][T]
-  float* scales = wt + T * E;                                           // [kScaleUnits][16]
 
   const int lane = threadIdx.x & 63, tok = lane & 15, piece = lane >> 4, tc = min(tok, T - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -425,47 +426,63 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
   const int groups = kWaves / split, group = wave / split, part = wave % split;
   const int c0 = chunks * part / split, mine = chunks * (part + 1) / split - c0;
   const int round = max(mine, kDepth);  // (a narrow unit is padded to a round)
+  // The deal: turn i of a workgroup is a unit for each of its groups, from slot base_of(i).
+  // The first turns are dealt evenly, the last sixth to whoever is there first, from a
+  // counter that decode_route_kernel has cleared: odd dies take 5 to 10 % longer for the
+  // same share.  A claim is made four turns ahead and posted in LDS three ahead.
   const int stride = (int)gridDim.x * groups, u0 = (int)blockIdx.x * groups;
-  const int turns = u0 < total ? (total - u0 + stride - 1) / stride : 0;  // of the workgroup's first group: the most
-  const int units = u0 + group < total ? (total - u0 - group + stride - 1) / stride : 0;
-  if (turns == 0) return;
+  const int even = total / stride, fixed = a.logits != nullptr && even >= 8 ? max(4, even * 5 / 6) : 0x7fffffff;
+  const auto base_of = [&](int i) { return i < fixed ? u0 + i * stride : fixed * stride + claims[i & 7] * groups; };
+  const auto there = [&](int slot) { return slot < total; };
+  if (!there(u0)) return;
+  // Two units share each 1 KB of a blocked matrix's 16 rows: they go to workgroups 8
+  // apart, which are on one die
+  const auto unit = [&](int slot) {
+    return groups == 1 && (slot | 15) < total ? (slot & ~15) | ((slot & 7) << 1) | ((slot >> 3) & 1) : slot;
+  };
   const Rows<B16> rows{(size_t)d * WB};
   constexpr int step = Rows<B16>::step;
   const char* base = static_cast<const char*>(tok < 8 ? a.w_gate : a.w_up) + piece * 16 + (size_t)c0 * step;
-  const auto unit_at = [&](int i) {
-    const int u = u0 + group + i * stride, e = list[u / per];
+  const auto unit_at = [&](int slot) {
+    const int u = unit(slot), e = list[u / per];
     return base + (size_t)e * F * rows.row_bytes + rows.at((u % per) * kUnitCols + (tok & 7));
   };
-  // E4M3: the scales of the next turns to LDS, 8 of gate's and 8 of up's for each unit, so
-  // that finishing one waits for no load
-  const auto fetch_scales = [&](int i0) {
-    for (int j = threadIdx.x; j < kScaleUnits * 16; j += 64 * kWaves) {
-      const int v = j >> 4, u = u0 + v % groups + (i0 + v / groups) * stride;
-      if (u < total) scales[j] = ((j & 8) ? a.s_up : a.s_gate)[(size_t)list[u / per] * F + (u % per) * kUnitCols + (j & 7)];
-    }
+  // E4M3: the scales of a turn's units, 8 of gate's and 8 of up's each, one for a thread; in
+  // LDS a turn before they are used, so that finishing a unit waits for no load
+  const auto scale_of = [&](int i) {
+    const int slot = base_of(i) + ((int)threadIdx.x >> 4), u = unit(slot);
+    if ((int)threadIdx.x >= groups * 16 || !there(slot)) return 0.f;
+    return ((threadIdx.x & 8) ? a.s_up : a.s_gate)[(size_t)list[u / per] * F + (u % per) * kUnitCols + (threadIdx.x & 7)];
   };
+  float scale_next = 0.f;
+  int claim_next = 0;
   if constexpr (Q) {
-    fetch_scales(0);
+    if (threadIdx.x < kWaves * 16) {
+      scales[0][threadIdx.x] = scale_of(0);
+      scale_next = scale_of(1);
+    }
     __syncthreads();
   }
   // turn i's sums, which the wavefronts have left in LDS, to h: by one wavefront of each
   // group, each turn another
   const auto finish = [&](int i) {
-    if (Q && i != 0 && i % (kScaleUnits / groups) == 0) {  // every unit before has had its scales when all are here
-      __syncthreads();
-      fetch_scales(i);
-    }
+    if (Q && threadIdx.x < kWaves * 16) scales[(i + 1) & 3][threadIdx.x] = scale_next;
+    if (i + 3 >= fixed && threadIdx.x == 0) claims[(i + 3) & 7] = claim_next;
     lds_barrier();
-    if (part != i % split || i >= units) return;
+    if (i + 4 >= fixed && threadIdx.x == 0)
+      claim_next = __hip_atomic_fetch_add(&a.table->claimed, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (Q && threadIdx.x < kWaves * 16) scale_next = scale_of(i + 2);
+    const int slot = base_of(i) + group;
+    if (part != i % split || !there(slot)) return;
     const f32x4_t* from = red + ((i & 1) * kWaves + group * split) * 64 + lane;
     f32x4_t s = from[0];
     for (int w = 1; w < split; ++w) s += from[w * 64];
-    const int u = u0 + group + i * stride, n = u / per, f0 = (u % per) * kUnitCols;
+    const int u = unit(slot), n = u / per, f0 = (u % per) * kUnitCols;
     // with low terms, columns 8 .. 15 hold those of tokens 0 .. 7
 #pragma unroll
     for (int r = 0; r < 4; ++r) s[r] = (a.x_low ? s[r] + __shfl_down(s[r], 8) : s[r]) * inv;
     if constexpr (Q) {
-      const float4 sc = *reinterpret_cast<const float4*>(scales + ((i * groups + group) % kScaleUnits) * 16 + piece * 4);
+      const float4 sc = *reinterpret_cast<const float4*>(&scales[i & 3][group * 16 + piece * 4]);
       s[0] *= sc.x, s[1] *= sc.y, s[2] *= sc.z, s[3] *= sc.w;
     }
     // rows 0..7 (pieces 0, 1) are the gate's columns, rows 8..15 the same columns of up
@@ -489,21 +506,21 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
       }
     }
   };
-  int done = 0;  // turns finished
-  if (units != 0) {
-    // kDepth loads in flight, across units; behind the last unit the cursor repeats its
-    // last chunk
-    int li = 0, lc = 0;
-    const char *lp = unit_at(0), *next = unit_at(min(1, units - 1));
-    bool fetched = false;
+  int turn = 0;  // turns finished
+  if (there(u0 + group)) {
+    // kDepth loads in flight, across units: the cursor is at chunk lc of turn li, and
+    // behind the last unit repeats its last chunk
+    int li = 0, lc = 0, slot = base_of(1) + group;
+    const char *lp = unit_at(u0 + group), *next = unit_at(there(slot) ? slot : u0 + group);
+    bool more = there(slot), moved = false;
     const auto load = [&]() {
       const uint4 v = load_weights<B16>(lp);
       if (++lc < mine) lp += step;
-      if (lc == round && li + 1 < units) {
+      if (lc == round && more) {
         ++li;
         lc = 0;
         lp = next;
-        fetched = true;
+        moved = true;
       }
       return v;
     };
@@ -511,9 +528,10 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
     const char* xlane = xs + (a.x_low && tok >= 8 ? plane : 0) + (size_t)c0 * NB * T * 64 +
                         (Q ? ((size_t)(piece >> 1) * T + col) * 64 + (piece & 1) * 32 : (size_t)col * 64 + piece * 16);
     int uc = 0;
-    bool ended = false;
+    bool alive = true, ended = false;
     f32x4_t acc{0.f, 0.f, 0.f, 0.f};
     const auto work = [&](const uint4& w) {
+      if (!alive) return;
       if (uc < mine) {
         uint4 b[NB];
 #pragma unroll
@@ -521,32 +539,35 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
         acc = mma_chunk<Tr, Q>(w, b, acc);
       }
       if (++uc == round) {
-        red[((done & 1) * kWaves + wave) * 64 + lane] = acc;
+        red[((turn & 1) * kWaves + wave) * 64 + lane] = acc;
         uc = 0;
         acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
         ended = true;
+        alive = li > turn;  // the cursor is kDepth loads ahead, in the next unit if there is one
       }
     };
     uint4 ring[kDepth];
 #pragma unroll
     for (int j = 0; j < kDepth; ++j) ring[j] = load();
-    for (int left = units * round; left > 0; left -= kDepth) {
-      if (fetched) {
-        next = unit_at(min(li + 1, units - 1));
-        fetched = false;
+    while (alive) {
+      if (moved) {
+        slot = base_of(li + 1) + group;
+        more = there(slot);
+        if (more) next = unit_at(slot);
+        moved = false;
       }
 #pragma unroll
       for (int j = 0; j < kDepth; ++j) {
-        if (j < left) work(ring[j]);
+        work(ring[j]);
         ring[j] = load();
       }
       if (ended) {
-        finish(done++);
+        finish(turn++);
         ended = false;
       }
     }
   }
-  for (; done < turns; ++done) finish(done);  // (others' barriers)
+  for (; there(base_of(turn)); ++turn) finish(turn);  // (others' barriers)
 }
 
 // One part of the K range of 16 NR columns of d: out's columns where the tile has one part,
@@ -746,9 +767,9 @@ hipError_t decode_t(DecodeArgs a, hipStream_t stream) {
 
 }  // namespace
 
-// x [T][d], the wavefronts' sums, logits and weights [T][E] each, and scales.
+// x [T][d], the wavefronts' sums, logits and weights [T][E] each.
 size_t decode_lds_bytes(int elt_bytes, int T, int d, int E) {
-  return (size_t)T * d * elt_bytes + kRedBytes + kScaleBytes + (size_t)8 * T * E;
+  return (size_t)T * d * elt_bytes + kRedBytes + (size_t)8 * T * E;
 }
 
 hipError_t launch_decode(int dtype, const DecodeArgs& a, hipStream_t stream) {

@@ -479,8 +479,17 @@ class Residual:
     scale: float = 1.0
     dropout: float = 0.0
 
-    def c(self, gate: int) -> MoeResidual:
-        return MoeResidual(self.eps, self.scale, self.dropout, gate)
+    def c(self, gate: int):
+        """The C struct for a kind of gate, by reference; made once for each of the three."""
+        refs = self.__dict__.get("_crefs")
+        if refs is None:
+            refs = tuple(ctypes.byref(MoeResidual(self.eps, self.scale, self.dropout, g)) for g in range(3))
+            object.__setattr__(self, "_crefs", refs)
+        return refs[gate]
+
+    def __getstate__(self):
+        """The fields alone, as Shape's."""
+        return {f.name: getattr(self, f.name) for f in dataclasses.fields(self)}
 
 
 def _gate(gate, s: Shape, name: str, device):
@@ -527,7 +536,7 @@ def moe_residual(shape: Shape, r: Residual, res, y, post_w, gate, rng, next_w, o
     s, dev = shape, y.device
     Td = (s.T, s.d)
     kind, g = _gate(gate, s, "gate", dev)
-    _call("moe_residual", dev, stream, _c(s), ctypes.byref(r.c(kind)), _in(res, "res", Td, s.dtype, dev),
+    _call("moe_residual", dev, stream, _c(s), r.c(kind), _in(res, "res", Td, s.dtype, dev),
           _in(y, "y", Td, s.dtype, dev), _in(post_w, "post_w", (s.d,), s.dtype, dev), g, _rng(rng, dev),
           _in(next_w, "next_w", (s.d,), s.dtype, dev), _in(out, "out", Td, s.dtype, dev), _in(n, "n", Td, s.dtype, dev))
 
@@ -541,7 +550,7 @@ def moe_residual_backward(shape: Shape, r: Residual, out, y, post_w, gate, rng, 
     kind, g = _gate(gate, s, "gate", dev)
     if dgate is not None and (gate is None or dgate.shape != gate.shape):
         raise ValueError("dgate must have the gate's shape")
-    _call("moe_residual_backward", dev, stream, _c(s), ctypes.byref(r.c(kind)), _in(out, "out", Td, s.dtype, dev),
+    _call("moe_residual_backward", dev, stream, _c(s), r.c(kind), _in(out, "out", Td, s.dtype, dev),
           _in(y, "y", Td, s.dtype, dev), _in(post_w, "post_w", (s.d,), s.dtype, dev), g, _rng(rng, dev),
           _in(next_w, "next_w", (s.d,), s.dtype, dev), _in(dout, "dout", Td, s.dtype, dev),
           _in(dn, "dn", Td, s.dtype, dev), _in(dres, "dres", Td, s.dtype, dev), _in(dy, "dy", Td, s.dtype, dev),

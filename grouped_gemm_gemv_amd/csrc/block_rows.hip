@@ -7,7 +7,7 @@
 #include "block.hpp"
 #include "device_common.hpp"
 #include "philox.hpp"
-#include "rounding.hpp"
+#include "vec.hpp"
 
 namespace moe {
 namespace {
@@ -28,7 +28,7 @@ __device__ __forceinline__ float sigmoid(float g, float* slope = nullptr) {
 template <int NT, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* part) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  for (int i = 0; i < N; ++i) v[i] = wave_fold(v[i], [](float x, float y) { return x + y; });
   if constexpr (NT > 64) {
     constexpr int W = NT / 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -36,7 +36,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* part) {
 #pragma unroll
       for (int i = 0; i < N; ++i) part[i * W + wave] = v[i];
     }
-    __syncthreads();
+    lds_barrier();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       v[i] = part[i * W];
@@ -46,54 +46,71 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* part) {
   }
 }
 
-// Which of the EPC elements of 16-byte chunk c of row t are kept, a bit each: the
-// generator's block is the eight elements from (t d + c EPC) / 8 8 on.
+// Which of the EPC elements of 16-byte chunk c of row t are kept: the generator's block
+// is the eight elements that hold them.
 template <class Tr>
-__device__ __forceinline__ unsigned kept(size_t t, int d, int c, uint64_t seed, uint64_t step, unsigned threshold) {
-  const uint64_t at = (uint64_t)t * d + (uint64_t)c * Tr::EPC;
-  const Philox r = philox(at >> 3, step, seed);
-  unsigned bits = 0;
-#pragma unroll
-  for (int i = 0; i < Tr::EPC; ++i) {
-    const unsigned h = Tr::EPC == 8 ? r.half(i) : (at & 4) ? r.half(4 + (i & 3)) : r.half(i);
-    bits |= (h >= threshold ? 1u : 0u) << i;
+struct Kept {
+  Philox r;
+  unsigned threshold;
+  __device__ __forceinline__ Kept(size_t t, int d, int c, uint64_t seed, uint64_t step, unsigned threshold)
+      : threshold(threshold) {
+    const uint64_t at = (uint64_t)t * d + (uint64_t)c * Tr::EPC;
+    r = philox(at >> 3, step, seed);
+    if (Tr::EPC == 4 && (at & 4)) r.w[0] = r.w[2], r.w[1] = r.w[3];
   }
-  return bits;
+  __device__ __forceinline__ bool operator()(int j) const { return r.half(j) >= threshold; }
+};
+
+// Chunk c of a row, zeros past its last one.
+__device__ __forceinline__ uint4 chunk(const void* row, int c, int chunks) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (c < chunks) v = load16(static_cast<const char*>(row) + (unsigned)c * 16u);
+  return v;
+}
+__device__ __forceinline__ void put(void* row, int c, int chunks, const uint4& v) {
+  if (c < chunks) *reinterpret_cast<u32x4*>(static_cast<char*>(row) + (unsigned)c * 16u) = __builtin_bit_cast(u32x4, v);
 }
 
+// Threads of a workgroup for rows of NT threads: short rows share one.
+constexpr int block_of(int NT) { return NT == 64 ? 256 : NT; }
+
+// A bf16 or fp32 value in a chunk of its own.
 template <class Tr>
-__device__ __forceinline__ uint4 chunk(const void* row, int c) {
-  return static_cast<const uint4*>(row)[c];
+__device__ __forceinline__ float element(const void* p, size_t i) {
+  if constexpr (Tr::EPC == 8)
+    return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
+  else
+    return static_cast<const float*>(p)[i];
 }
 
-// NT threads of a row, V 16-byte chunks each; 256 / NT rows (one past 256) for a
-// workgroup.
+// NT threads of a row, V 16-byte chunks each.
 template <class Tr, int NT, int V>
-__global__ __launch_bounds__(NT > 256 ? NT : 256) void residual_kernel(ResidualArgs a) {
-  using Elt = typename Tr::T;
-  constexpr int EPC = Tr::EPC, G = NT < 256 ? 256 / NT : 1;
+__global__ __launch_bounds__(block_of(NT)) void residual_kernel(ResidualArgs a) {
+  constexpr int EPC = Tr::EPC, G = block_of(NT) / NT;
   __shared__ float part[2][2][NT / 64];
   const int tid = threadIdx.x % NT, chunks = a.d / EPC;
   const uint64_t seed = a.rng != nullptr ? a.rng[0] : 0, step = a.rng != nullptr ? a.rng[1] : 0;
+  const size_t width = (size_t)a.d * sizeof(typename Tr::T);
   // (groups of one wavefront meet no barrier; larger ones are the whole workgroup.  A row's
   // sums go where the row before had none: a row may have one barrier only)
   int place = 0;
-  for (size_t t = (size_t)blockIdx.x * G + threadIdx.x / NT; t < (size_t)a.T; t += (size_t)gridDim.x * G, place ^= 1) {
-    const size_t row = t * a.d * sizeof(Elt);
-    const auto at = [&](const void* p) { return static_cast<const char*>(p) + row; };
+  for (size_t t = (size_t)blockIdx.x * G + __builtin_amdgcn_readfirstlane(threadIdx.x / NT); t < (size_t)a.T;
+       t += (size_t)gridDim.x * G, place ^= 1) {
+    const auto at = [&](const void* p) { return static_cast<const char*>(p) + t * width; };
+    const auto to = [&](void* p) { return static_cast<char*>(p) + t * width; };
     uint4 rc[V], yc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * NT;
-      const bool in = c < chunks;
-      yc[i] = a.y != nullptr && in ? chunk<Tr>(at(a.y), c) : make_uint4(0, 0, 0, 0);
-      rc[i] = in ? chunk<Tr>(at(a.res), c) : make_uint4(0, 0, 0, 0);
+      yc[i] = a.y != nullptr ? chunk(at(a.y), c, chunks) : make_uint4(0, 0, 0, 0);
+      rc[i] = chunk(at(a.res), c, chunks);
     }
     float o[V][EPC];
 #pragma unroll
     for (int i = 0; i < V; ++i) widen<Tr>(rc[i], o[i]);
     if (a.y != nullptr) {
-      float r = 1.f;
+      float mul = a.scale * a.keep_scale;
+      if (a.gate != nullptr && !a.gate_full) mul *= sigmoid(element<Tr>(a.gate, t));
       if (a.post_w != nullptr) {
         float s[1] = {0.f};
 #pragma unroll
@@ -104,38 +121,33 @@ __global__ __launch_bounds__(NT > 256 ? NT : 256) void residual_kernel(ResidualA
           for (int j = 0; j < EPC; ++j) s[0] = fmaf(y[j], y[j], s[0]);
         }
         row_sum<NT>(s, part[place][0]);
-        r = inv_rms(s[0], a.d, a.eps);
-      }
-      float mul = a.scale * a.keep_scale;
-      if (a.gate != nullptr && !a.gate_full) {
-        float g[EPC];
-        widen<Tr>(make_uint4(sizeof(Elt) == 2 ? static_cast<const uint16_t*>(a.gate)[t] : static_cast<const uint32_t*>(a.gate)[t], 0, 0, 0), g);
-        mul *= sigmoid(g[0]);
+        mul *= inv_rms(s[0], a.d, a.eps);
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int c = tid + i * NT;
-        if (c >= chunks) continue;
         float v[EPC];
         widen<Tr>(yc[i], v);
         if (a.post_w != nullptr) {
           float w[EPC];
-          widen<Tr>(chunk<Tr>(a.post_w, c), w);
+          widen<Tr>(chunk(a.post_w, c, chunks), w);
 #pragma unroll
-          for (int j = 0; j < EPC; ++j) v[j] *= r * w[j];
+          for (int j = 0; j < EPC; ++j) v[j] *= w[j];
         }
         if (a.gate_full) {
           float g[EPC];
-          widen<Tr>(chunk<Tr>(at(a.gate), c), g);
+          widen<Tr>(chunk(at(a.gate), c, chunks), g);
 #pragma unroll
           for (int j = 0; j < EPC; ++j) v[j] *= sigmoid(g[j]);
         }
-        // a dropped element adds nothing, whatever it holds
-        const unsigned keep = a.threshold != 0 ? kept<Tr>(t, a.d, c, seed, step, a.threshold) : ~0u;
+        if (a.threshold != 0) {  // a dropped element adds nothing, whatever it holds
+          const Kept<Tr> keep(t, a.d, c, seed, step, a.threshold);
 #pragma unroll
-        for (int j = 0; j < EPC; ++j)
-          if ((keep >> j) & 1u) o[i][j] = fmaf(mul, v[j], o[i][j]);
-        static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.out) + row))[c] = round_to<Tr>(o[i]);
+          for (int j = 0; j < EPC; ++j) v[j] = keep(j) ? v[j] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < EPC; ++j) o[i][j] = fmaf(mul, v[j], o[i][j]);
+        put(to(a.out), c, chunks, round_to<Tr>(o[i]));
       }
     }
     if (a.next_w == nullptr) continue;
@@ -150,12 +162,11 @@ __global__ __launch_bounds__(NT > 256 ? NT : 256) void residual_kernel(ResidualA
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * NT;
-      if (c >= chunks) continue;
       float w[EPC];
-      widen<Tr>(chunk<Tr>(a.next_w, c), w);
+      widen<Tr>(chunk(a.next_w, c, chunks), w);
 #pragma unroll
       for (int j = 0; j < EPC; ++j) w[j] *= o[i][j] * r;
-      static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.n) + row))[c] = round_to<Tr>(w);
+      put(to(a.n), c, chunks, round_to<Tr>(w));
     }
   }
 }
@@ -170,148 +181,172 @@ __global__ __launch_bounds__(NT > 256 ? NT : 256) void residual_kernel(ResidualA
 // The sums over tokens: each thread keeps its columns' over the rows that its
 // workgroup works, rows in ascending order.
 template <class Tr, int NT, int V>
-__global__ __launch_bounds__(NT > 256 ? NT : 256) void residual_backward_kernel(ResidualBackwardArgs a) {
+__global__ __launch_bounds__(block_of(NT)) void residual_backward_kernel(ResidualBackwardArgs a) {
   using Elt = typename Tr::T;
-  constexpr int EPC = Tr::EPC, G = NT < 256 ? 256 / NT : 1;
+  constexpr int EPC = Tr::EPC, B = block_of(NT), G = B / NT;
   extern __shared__ float sums[];  // [G > 1 ? G : 0][d]
   __shared__ float part1[2][3 * (NT / 64)], part2[NT / 64];
-  const int tid = threadIdx.x % NT, group = threadIdx.x / NT, chunks = a.d / EPC;
+  const int tid = threadIdx.x % NT, group = __builtin_amdgcn_readfirstlane(threadIdx.x / NT), chunks = a.d / EPC;
   float gp[V][EPC], gn[V][EPC];  // columns' sums of dpost_w and dnext_w
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < EPC; ++j) gp[i][j] = gn[i][j] = 0.f;
   const uint64_t seed = a.rng != nullptr ? a.rng[0] : 0, step = a.rng != nullptr ? a.rng[1] : 0;
+  const size_t width = (size_t)a.d * sizeof(Elt);
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  // Rows' loads run a row ahead where their registers allow: they are issued behind the first
+  // barrier of the row before, none of whose barriers waits for them (4096 x 4096 with
+  // everything: 53 us, 59 without)
+  constexpr bool kAhead = V * EPC <= 8;
+  uint4 xc[V], yc[V], dnc[V], doc[V], pwc[V], nwc[V];
+  const auto load_row = [&](size_t t, uint4 (&x)[V], uint4 (&dn)[V], uint4 (&y)[V], uint4 (&dout)[V]) {
+    const auto at = [&](const void* p) { return static_cast<const char*>(p) + t * width; };
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * NT;
+      x[i] = a.next_w != nullptr ? chunk(at(a.x), c, chunks) : zero;
+      dn[i] = a.next_w != nullptr ? chunk(at(a.dn), c, chunks) : zero;
+      y[i] = a.y != nullptr ? chunk(at(a.y), c, chunks) : zero;
+      dout[i] = a.dout != nullptr ? chunk(at(a.dout), c, chunks) : zero;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    pwc[i] = a.post_w != nullptr ? chunk(a.post_w, tid + i * NT, chunks) : zero;
+    nwc[i] = a.next_w != nullptr ? chunk(a.next_w, tid + i * NT, chunks) : zero;
+  }
+  const size_t first = (size_t)blockIdx.x * G + group, ahead = (size_t)gridDim.x * G;
+  if (kAhead && first < (size_t)a.T) load_row(first, xc, dnc, yc, doc);
   // (groups of one wavefront meet no barrier in the loop; larger ones are the whole workgroup;
   // a row's first sums go to the place that the row before did not use, since a norm alone
   // has no second barrier behind their reading)
   int place = 0;
-  for (size_t t = (size_t)blockIdx.x * G + group; t < (size_t)a.T; t += (size_t)gridDim.x * G, place ^= 1) {
-    const size_t row = t * a.d * sizeof(Elt);
-    const auto at = [&](const void* p) { return static_cast<const char*>(p) + row; };
-    uint4 xc[V], yc[V], dnc[V], doc[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = tid + i * NT;
-      const bool in = c < chunks;
-      xc[i] = a.next_w != nullptr && in ? chunk<Tr>(at(a.x), c) : zero;
-      dnc[i] = a.next_w != nullptr && in ? chunk<Tr>(at(a.dn), c) : zero;
-      yc[i] = a.y != nullptr && in ? chunk<Tr>(at(a.y), c) : zero;
-      doc[i] = a.dout != nullptr && in ? chunk<Tr>(at(a.dout), c) : zero;
-    }
+  for (size_t t = first; t < (size_t)a.T; t += ahead, place ^= 1) {
+    const auto at = [&](const void* p) { return static_cast<const char*>(p) + t * width; };
+    const auto to = [&](void* p) { return static_cast<char*>(p) + t * width; };
+    if (!kAhead) load_row(t, xc, dnc, yc, doc);
     // squares of x, z x, squares of y
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * NT;
-      float y[EPC];
-      widen<Tr>(yc[i], y);
+      if (a.post_w != nullptr) {
+        float y[EPC];
+        widen<Tr>(yc[i], y);
 #pragma unroll
-      for (int j = 0; j < EPC; ++j) s[2] = fmaf(y[j], y[j], s[2]);
-      if (a.next_w != nullptr && c < chunks) {
+        for (int j = 0; j < EPC; ++j) s[2] = fmaf(y[j], y[j], s[2]);
+      }
+      if (a.next_w != nullptr) {
         float x[EPC], dn[EPC], w[EPC];
         widen<Tr>(xc[i], x);
         widen<Tr>(dnc[i], dn);
-        widen<Tr>(chunk<Tr>(a.next_w, c), w);
+        widen<Tr>(nwc[i], w);
 #pragma unroll
         for (int j = 0; j < EPC; ++j) {
           s[0] = fmaf(x[j], x[j], s[0]);
-          s[1] = fmaf(dn[j] * w[j], x[j], s[1]);
+          s[1] = fmaf(dn[j] * x[j], w[j], s[1]);
         }
       }
     }
-    row_sum<NT>(s, part1[place]);
-    const float r1 = inv_rms(s[0], a.d, a.eps), k1 = r1 * r1 * (s[1] / (float)a.d);
+    if (a.next_w != nullptr || a.post_w != nullptr) row_sum<NT>(s, part1[place]);
+    uint4 xn[V], yn[V], dnn[V], don[V];
+    if (kAhead && t + ahead < (size_t)a.T) load_row(t + ahead, xn, dnn, yn, don);
+    const auto advance = [&]() {
+      if (!kAhead) return;
+#pragma unroll
+      for (int i = 0; i < V; ++i) xc[i] = xn[i], yc[i] = yn[i], dnc[i] = dnn[i], doc[i] = don[i];
+    };
+    const float r1 = inv_rms(s[0], a.d, a.eps), k1 = -r1 * r1 * r1 * (s[1] / (float)a.d);
     const float r2 = a.post_w != nullptr ? inv_rms(s[2], a.d, a.eps) : 1.f;
     float D[V][EPC];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * NT;
       widen<Tr>(doc[i], D[i]);
-      if (c >= chunks) continue;
       if (a.next_w != nullptr) {
         float x[EPC], dn[EPC], w[EPC];
         widen<Tr>(xc[i], x);
         widen<Tr>(dnc[i], dn);
-        widen<Tr>(chunk<Tr>(a.next_w, c), w);
+        widen<Tr>(nwc[i], w);
 #pragma unroll
         for (int j = 0; j < EPC; ++j) {
-          gn[i][j] = fmaf(dn[j] * r1, x[j], gn[i][j]);
-          D[i][j] = fmaf(r1, fmaf(dn[j], w[j], -x[j] * k1), D[i][j]);
+          dn[j] *= r1;
+          gn[i][j] = fmaf(dn[j], x[j], gn[i][j]);
+          D[i][j] += fmaf(dn[j], w[j], x[j] * k1);
         }
       }
-      static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.dres) + row))[c] = round_to<Tr>(D[i]);
+      put(to(a.dres), c, chunks, round_to<Tr>(D[i]));
     }
-    if (a.y == nullptr) continue;
-    const float m = a.scale * a.keep_scale;
+    if (a.y == nullptr) {
+      advance();
+      continue;
+    }
     float gate = 1.f, slope = 0.f;
-    if (a.gate != nullptr && !a.gate_full) {
-      float g[EPC];
-      widen<Tr>(make_uint4(sizeof(Elt) == 2 ? static_cast<const uint16_t*>(a.gate)[t] : static_cast<const uint32_t*>(a.gate)[t], 0, 0, 0), g);
-      gate = sigmoid(g[0], &slope);
-    }
-    // D becomes c (or sigmoid q without a norm); its product with y, and with a gate
-    // for each token the same before the sigmoid, are one sum: sigmoid is a factor of it
+    if (a.gate != nullptr && !a.gate_full) gate = sigmoid(element<Tr>(a.gate, t), &slope);
+    // D becomes q (times the sigmoid of a full gate); its product with y and post_w, q v r2
+    // and c y up to factors of the row, is one sum
+    const float m = a.scale * a.keep_scale, mg = m * gate * r2;
     float cy[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * NT;
-      if (c >= chunks) continue;
       float y[EPC], w[EPC];
       widen<Tr>(yc[i], y);
 #pragma unroll
       for (int j = 0; j < EPC; ++j) w[j] = 1.f;
-      if (a.post_w != nullptr) widen<Tr>(chunk<Tr>(a.post_w, c), w);
-      const unsigned keep = a.threshold != 0 ? kept<Tr>(t, a.d, c, seed, step, a.threshold) : ~0u;
+      if (a.post_w != nullptr) widen<Tr>(pwc[i], w);
+      if (a.threshold != 0) {  // what is dropped takes no part, whatever it holds
+        const Kept<Tr> keep(t, a.d, c, seed, step, a.threshold);
 #pragma unroll
-      for (int j = 0; j < EPC; ++j) {  // what is dropped takes no part, whatever it holds
-        D[i][j] = (keep >> j) & 1u ? m * D[i][j] : 0.f;
-        y[j] = (keep >> j) & 1u ? y[j] : 0.f;
+        for (int j = 0; j < EPC; ++j) {
+          D[i][j] = keep(j) ? D[i][j] : 0.f;
+          y[j] = keep(j) ? y[j] : 0.f;
+        }
       }
       if (a.gate_full) {
         float g[EPC], dg[EPC];
-        widen<Tr>(chunk<Tr>(at(a.gate), c), g);
+        widen<Tr>(chunk(at(a.gate), c, chunks), g);
 #pragma unroll
         for (int j = 0; j < EPC; ++j) {
           float sl;
           const float sg = sigmoid(g[j], &sl);
-          dg[j] = sl * D[i][j] * (y[j] * r2 * w[j]);
+          dg[j] = sl * (m * D[i][j]) * (y[j] * r2 * w[j]);
           D[i][j] *= sg;
         }
-        if (a.dgate != nullptr)
-          static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.dgate) + row))[c] = round_to<Tr>(dg);
+        if (a.dgate != nullptr) put(to(a.dgate), c, chunks, round_to<Tr>(dg));
       }
 #pragma unroll
       for (int j = 0; j < EPC; ++j) {
-        gp[i][j] = fmaf(gate * D[i][j] * r2, y[j], gp[i][j]);
+        const float p = D[i][j] * y[j];
+        gp[i][j] = fmaf(mg, p, gp[i][j]);
+        cy[0] = fmaf(p, w[j], cy[0]);
         D[i][j] *= w[j];
-        cy[0] = fmaf(D[i][j], y[j], cy[0]);
       }
     }
-    row_sum<NT>(cy, part2);
+    if (a.post_w != nullptr || (a.gate != nullptr && !a.gate_full)) row_sum<NT>(cy, part2);
     if (a.gate != nullptr && !a.gate_full && a.dgate != nullptr && tid == 0) {
-      const float g = slope * r2 * cy[0];
+      const float g = slope * r2 * m * cy[0];
       if constexpr (sizeof(Elt) == 2)
         static_cast<uint16_t*>(a.dgate)[t] = (uint16_t)f32_to_bf16(g);
       else
         static_cast<float*>(a.dgate)[t] = g;
     }
-    const float k2 = r2 * r2 * (cy[0] / (float)a.d), mul = gate * r2;
+    const float k2 = -mg * r2 * r2 * (cy[0] / (float)a.d);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * NT;
-      if (c >= chunks) continue;
+#pragma unroll
+      for (int j = 0; j < EPC; ++j) D[i][j] *= mg;
       if (a.post_w != nullptr) {
         float y[EPC];
         widen<Tr>(yc[i], y);
 #pragma unroll
-        for (int j = 0; j < EPC; ++j) D[i][j] -= y[j] * k2;
+        for (int j = 0; j < EPC; ++j) D[i][j] = fmaf(y[j], k2, D[i][j]);
       }
-#pragma unroll
-      for (int j = 0; j < EPC; ++j) D[i][j] *= mul;
-      static_cast<uint4*>(static_cast<void*>(static_cast<char*>(a.dy) + row))[c] = round_to<Tr>(D[i]);
+      put(to(a.dy), c, chunks, round_to<Tr>(D[i]));
     }
+    advance();
   }
   // this workgroup's sums: groups in order
   const auto flush = [&](float (&g)[V][EPC], float* dst) {
@@ -324,7 +359,7 @@ __global__ __launch_bounds__(NT > 256 ? NT : 256) void residual_backward_kernel(
         for (int j = 0; j < EPC; ++j) sums[(size_t)group * a.d + c * EPC + j] = g[i][j];
       }
       __syncthreads();
-      for (int c = threadIdx.x; c < a.d; c += 256) {
+      for (int c = threadIdx.x; c < a.d; c += B) {
         float v = sums[c];
 #pragma unroll
         for (int w = 1; w < G; ++w) v += sums[(size_t)w * a.d + c];
@@ -440,19 +475,17 @@ __global__ __launch_bounds__(256) void dropout_kernel(const char* x, int64_t n, 
   }
 }
 
-constexpr int kBackwardGroups = 512;
-
 // Threads of a row and elements of each: the first whose product holds the row.
-#define MOE_ROW_SHAPES(M) M(64, 8) M(64, 16) M(256, 8) M(256, 16) M(512, 16) M(512, 32)
+#define MOE_ROW_SHAPES(M) M(64, 8) M(128, 8) M(256, 8) M(512, 8) M(1024, 8) M(1024, 16)
 
 template <class Tr>
 hipError_t residual_t(const ResidualArgs& a, hipStream_t stream) {
-#define MOE_TRY(NT, N)                                                                                      \
-  if (a.d <= NT * N) {                                                                                      \
-    constexpr int G = NT < 256 ? 256 / NT : 1;                                                              \
-    hipLaunchKernelGGL((residual_kernel<Tr, NT, N / Tr::EPC>), dim3(std::min((a.T - 1) / G + 1, 1 << 20)),  \
-                       dim3(NT > 256 ? NT : 256), 0, stream, a);                                            \
-    return hipGetLastError();                                                                               \
+#define MOE_TRY(NT, N)                                                                                          \
+  if (a.d <= NT * N) {                                                                                          \
+    constexpr int B = block_of(NT);                                                                             \
+    hipLaunchKernelGGL((residual_kernel<Tr, NT, N / Tr::EPC>), dim3(std::min((a.T - 1) / (B / NT) + 1, 1 << 20)), \
+                       dim3(B), 0, stream, a);                                                                  \
+    return hipGetLastError();                                                                                   \
   }
   MOE_ROW_SHAPES(MOE_TRY)
 #undef MOE_TRY
@@ -464,12 +497,13 @@ hipError_t residual_backward_t(const ResidualBackwardArgs& a, hipStream_t stream
   const int groups = residual_backward_groups(a.T, a.d);
   hipError_t e = hipErrorInvalidValue;
   bool launched = false;
-#define MOE_TRY(NT, N)                                                                                      \
-  if (!launched && a.d <= NT * N) {                                                                         \
-    launched = true;                                                                                        \
-    hipLaunchKernelGGL((residual_backward_kernel<Tr, NT, N / Tr::EPC>), dim3(groups),                       \
-                       dim3(NT > 256 ? NT : 256), NT < 256 ? (size_t)(256 / NT) * a.d * 4 : 0, stream, a);  \
-    e = hipGetLastError();                                                                                  \
+#define MOE_TRY(NT, N)                                                                                          \
+  if (!launched && a.d <= NT * N) {                                                                             \
+    constexpr int B = block_of(NT);                                                                             \
+    launched = true;                                                                                            \
+    hipLaunchKernelGGL((residual_backward_kernel<Tr, NT, N / Tr::EPC>), dim3(groups), dim3(B),                  \
+                       B > NT ? (size_t)(B / NT) * a.d * 4 : 0, stream, a);                                     \
+    e = hipGetLastError();                                                                                      \
   }
   MOE_ROW_SHAPES(MOE_TRY)
 #undef MOE_TRY
@@ -482,8 +516,14 @@ hipError_t residual_backward_t(const ResidualBackwardArgs& a, hipStream_t stream
 }  // namespace
 
 int residual_backward_groups(int T, int d) {
-  const int per = d <= 1024 ? 4 : 1;  // rows side by side in a workgroup
-  return std::min((T - 1) / per + 1, kBackwardGroups);
+  const int per = d <= 512 ? 4 : 1;  // rows side by side in a workgroup
+  int threads = 64;                  // of a workgroup, as MOE_ROW_SHAPES has them
+  while (threads < 1024 && d > threads * 8) threads *= 2;
+  threads = block_of(threads);
+  // sixteen wavefronts for each compute unit, all that their registers allow: half or twice
+  // as many take 58 and 64 us for 16384 rows of 1024 bf16 against 54, and 62 and 65 against
+  // 53 for 4096 of 4096
+  return std::min((T - 1) / per + 1, 256 * 1024 / threads);
 }
 
 hipError_t launch_residual(int dtype, const ResidualArgs& a, hipStream_t stream) {

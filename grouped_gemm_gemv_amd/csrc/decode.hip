@@ -30,18 +30,14 @@
 // h_low), so that neither rounding is seen in the output (error against 64 bits at the
 // Mixtral shape T = 1: 0.0016 instead of 0.0025, the output's own rounding).
 #include <algorithm>
-#include <type_traits>
 
 #include "block.hpp"
 #include "device_common.hpp"
-#include "rounding.hpp"
+#include "vec.hpp"
 
 namespace moe {
 namespace {
 
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ uint4 load16(const char* p) { return *reinterpret_cast<const uint4*>(p); }
 // Weights: read once, by one workgroup, past the caches where they are blocked (a load is
 // 512 bytes or 1 KB in one piece): 8 tokens of the Mixtral shape take 391 us so and 423
 // with the default policy.  From row-major weights a load takes half a line of each of
@@ -61,13 +57,6 @@ __device__ __forceinline__ uint4 widen8(unsigned lo, unsigned hi) {
                __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
                __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)),
                __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))};
-}
-
-// Barrier over LDS alone: loads from memory stay in flight across it.
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
 }
 
 constexpr int kWaves = 8;        // wavefronts of the first kernel
@@ -96,21 +85,6 @@ __device__ __forceinline__ f32x4_t mma_chunk(const uint4& w, const uint4 (&b)[Q 
   } else {
     return mma16<Tr>(w, b[0], acc);
   }
-}
-
-// Sum and maximum over a wavefront without LDS: sixteen lanes by exchanges inside the
-// registers, then the four sixteens in order.
-template <class F>
-__device__ __forceinline__ float wave_fold(float v, F&& op) {
-  const auto dpp = [&](auto ctrl) {
-    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), decltype(ctrl)::value, 0xf, 0xf, true));
-  };
-  v = op(v, dpp(std::integral_constant<int, 0xB1>{}));   // quad_perm 1 0 3 2
-  v = op(v, dpp(std::integral_constant<int, 0x4E>{}));   // quad_perm 2 3 0 1
-  v = op(v, dpp(std::integral_constant<int, 0x141>{}));  // row_half_mirror
-  v = op(v, dpp(std::integral_constant<int, 0x140>{}));  // row_mirror
-  const auto lane = [&](int l) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), l)); };
-  return op(op(lane(0), lane(16)), op(lane(32), lane(48)));
 }
 
 // What rounding left of fp32 values: the second terms.

@@ -324,15 +324,19 @@ def _call(name: str, device, stream, *args):
     """One entry point on the tensors' device, on `stream` or that device's current stream."""
     if device.type != "cuda":
         raise ValueError("libmoe takes device tensors")
-    if stream is not None and stream.device != device:
+    if stream is None:
+        # (the handle alone: a Stream object around it takes longer than the rest of this function)
+        s = torch._C._cuda_getCurrentRawStream(device.index)
+    elif stream.device != device:
         raise ValueError(f"stream is on {stream.device}, expected {device}")
-    s = stream if stream is not None else torch.cuda.current_stream(device)
+    else:
+        s = stream.cuda_stream
     fn = getattr(lib(), name)
     if device.index == torch.cuda.current_device():
-        status = fn(*args, s.cuda_stream)
+        status = fn(*args, s)
     else:
         with torch.cuda.device(device):
-            status = fn(*args, s.cuda_stream)
+            status = fn(*args, s)
     check(name, status)
 
 

@@ -227,6 +227,26 @@ def test_dropout_bitwise(n, p, dtype):
     M.moe_dropout(empty, p, rng, empty)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dropout_of_odd_values(dtype):
+    """Subnormal numbers, zeros of both signs, infinities and the largest values keep their bits' meaning."""
+    import grouped_gemm_gemv_amd as M
+    vals = [0.0, -0.0, 1e-38, -1e-39, 1e-40, 9.2e-41, 3.3e38, -3.38e38, float("inf"), float("-inf"), float("nan"), 1.0]
+    x = _t(np.resize(np.array(vals), 6000), dtype)
+    rng = torch.tensor([3, 4], device="cuda")
+    out = _nan(x)
+    M.moe_dropout(x, 0.25, rng, out)
+    t = K.threshold(0.25)
+    scale = np.float32(65536.0) / np.float32(65536 - t)
+    with np.errstate(over="ignore", invalid="ignore"):
+        want = np.where(K.keep(0.25, 3, 4, x.numel()), x.float().cpu().numpy() * scale, np.float32(0))
+    want = torch.from_numpy(want).to(x.dtype)
+    got = out.cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    live = ~torch.isnan(want)
+    assert np.array_equal(bits(got[live]), bits(want[live]))
+
+
 def test_dropout_masks_differ_by_step_and_seed_and_agree_with_the_fused_one():
     import grouped_gemm_gemv_amd as M
     T, d, p = 16, 1024, 0.5

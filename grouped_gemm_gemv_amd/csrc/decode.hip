@@ -174,7 +174,7 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
   for (int i = threadIdx.x; i < T * E; i += 64 * kWaves) wt[i] = 0.f;
   if (threadIdx.x < 256) chosen[threadIdx.x] = 0;
 
-  constexpr int U = NE == 1 ? 8 : 2;
+  constexpr int U = NE == 1 ? 4 : 2;
   const bool inside = route && a.logits == nullptr;
   const int b0 = blocks * wave / kWaves, b1 = blocks * (wave + 1) / kWaves;
   uint4 wv[U][NE];

@@ -758,7 +758,7 @@ struct DecodePlan {
 };
 DecodePlan decode_plan(const moe_shape_t& s, size_t weight_bytes) {
   const size_t active = (size_t)std::min<int64_t>(s.E, (int64_t)s.T * s.k);
-  const size_t cols = moe::decode_h_low(s.dtype, s.T) ? 2 * (size_t)s.T : s.T;
+  const size_t cols = moe::decode_h_low(s.dtype) ? 2 * (size_t)s.T : s.T;
   DecodePlan p;
   p.parts = moe::decode_parts((int64_t)active * s.F * weight_bytes / 64, s.d, s.T);
   p.h = align_up(sizeof(moe::DecodeTable));
@@ -766,7 +766,8 @@ DecodePlan decode_plan(const moe_shape_t& s, size_t weight_bytes) {
   p.logits = p.part + (p.parts > 1 ? align_up((size_t)p.parts * s.d * moe::kDecodeTokens * 4) : 0);
   const size_t router = (size_t)s.E * s.d * elt_bytes(s), experts = active * 3 * s.d * s.F * weight_bytes;
   const bool apart = router >= moe::kRouteApart || experts >= moe::kDealApart ||
-                     (s.dtype == MOE_BF16 && s.T > moe::kDecodeTokens / 2 && router >= moe::kRouteApart / 4);
+                     (s.dtype == MOE_BF16 && !moe::decode_x_low((int)elt_bytes(s), s.T, s.d, s.E) &&
+                      router >= moe::kRouteApart / 4);
   p.ranges = apart ? (int)ceil_div((int64_t)s.d * elt_bytes(s) / 64, moe::kRouteBlocks) : 0;
   p.e16 = apart ? (s.E + 15) / 16 * 16 : 0;
   p.bytes = p.logits + align_up((size_t)p.ranges * p.e16 * moe::kDecodeTokens * 4);
@@ -828,7 +829,7 @@ moe_status_t decode_impl(const moe_shape_t* s, const void* x, const void* norm_w
   a.k = s->k;
   a.F = s->F;
   a.blocked16 = s->weight_layout == MOE_LAYOUT_BLOCKED16;
-  a.h_low = moe::decode_h_low(s->dtype, s->T);
+  a.h_low = moe::decode_h_low(s->dtype);
   a.eps = eps;
   a.scale = scale;
   return hip_status(moe::launch_decode(s->dtype, a, stream));

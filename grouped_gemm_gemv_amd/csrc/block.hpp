@@ -90,8 +90,8 @@ inline int decode_parts(int64_t chunks, int d, int T) {
 }
 
 // The router as a kernel of its own from this many bytes of its weights on (a quarter of it
-// for bf16 batches of more than 8 tokens, whose second terms are not kept in LDS but
-// made again), and the 64-byte blocks of K of one workgroup of it.  Measured, apart against
+// for bf16 batches whose second terms have no room in LDS and are made beside the
+// products), and the 64-byte blocks of K of one workgroup of it.  Measured, apart against
 // in the first kernel: 64 experts of 2048 and one token 36.0 vs 39.5 us, of 3584 and 16
 // tokens 467 vs 479; 8 experts of 4096 and one token 118.7 vs 118.7, 16 tokens 449 vs 452.
 // And from this many bytes of the experts that may be active on, for the deal of units that
@@ -118,19 +118,20 @@ struct DecodeArgs {
   void* h;                  // [active][F / KC][T, with h_low 2 T][KC], KC elements in 64 bytes
   int T, d, E, k, F;
   int blocked16;
-  int h_low;                // h is kept in two terms, the second in columns 8 .. 15
-  int x_low;                // so is x (set by the launcher)
+  int h_low;                // h is kept in two terms
+  int x_low;                // x norm_w is in LDS in two terms (set by the launcher)
   float* logits;            // [ranges][e16][16]: decode_route_kernel's sums, or null: routed in the first kernel
   int ranges, e16;
   float* part;              // [d / 64][parts][64 columns x 16 tokens], where parts > 1
   int parts;
   float eps, scale;
 };
-// Whether h is: bf16, and columns to spare.
-inline bool decode_h_low(int dtype, int T) { return dtype == 1 && T <= kDecodeTokens / 2; }
+inline bool decode_h_low(int dtype) { return dtype == 1; }
 // LDS that the first kernel needs at run time, and what a compute unit has beside its own arrays.
 constexpr size_t kDecodeLds = 154 * 1024;  // (so d is at most 70656: 4416 tiles)
 size_t decode_lds_bytes(int elt_bytes, int T, int d, int E);
+// Whether LDS has room for the second terms of x norm_w too.
+bool decode_x_low(int elt_bytes, int T, int d, int E);
 hipError_t launch_decode(int dtype, const DecodeArgs& a, hipStream_t stream);  // (h_low set)
 
 }  // namespace moe

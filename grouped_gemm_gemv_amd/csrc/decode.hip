@@ -1,5 +1,5 @@
 // The layer for a few tokens (T <= 16): norm, router, experts, combine and
-// residual in two kernels.
+// residual in two kernels, or three where the router's weights are many.
 //
 // With at most 16 tokens every product of the layer has at most 16 columns, the
 // width of one 16x16 matrix instruction, so the weights are the instruction's rows
@@ -8,7 +8,9 @@
 // no dispatch arrays, the matrix cores have the room (16 rows x 64 bytes of weights
 // per instruction: at the rate of HBM one in 90 cycles of a compute unit), and the
 // work is a single stream over the active experts' weights, which is what bounds
-// it.
+// it.  Mixtral shape, one token, blocked bf16: 77 us and 38 us of the two kernels for
+// 470 and 235 MB, 6.1 and 6.2 TB/s; 8 tokens with E4M3 weights: 130 and 71 us for 0.85 and
+// 0.42 GB, 6.5 and 6.0 TB/s (a streaming read alone reaches 7.0).
 //
 //   decode_up_kernel    every workgroup norms the tokens into LDS, routes them
 //                       (all of them, each workgroup for itself: E d weights
@@ -17,19 +19,23 @@
 //                       of 8 columns of F of an active expert: an MFMA tile of
 //                       8 gate rows above 8 up rows, K split over the
 //                       wavefronts, h = silu(g) u
-//   decode_down_kernel  a workgroup for each 16 columns of d: one sum over
-//                       the active experts' F columns, split over the
+//   decode_down_kernel  a workgroup for 16 or 64 columns of d and a part of the
+//                       sum over the active experts' F columns, split over the
 //                       wavefronts; where an expert ends, its sum is weighted
-//                       into the total, token by token
+//                       into the total, token by token; the parts are added
+//                       up, in order, by the workgroup that is done last
 //
-// Norm: with p = x norm_w (exact in two bf16 terms where both are bf16), the router
-// takes both terms and the experts the first, p rounded to bf16; 1 / rms is a
-// factor of each fp32 sum.  So logits have fp32's accuracy.  h is rounded to the
-// shape's type; nothing else is before the output.  Up to 8 tokens leave half of the
-// instruction's columns idle: there, bf16 batches have the second terms of p and h (x_low,
-// h_low), so that neither rounding is seen in the output (error against 64 bits at the
-// Mixtral shape T = 1: 0.0016 instead of 0.0025, the output's own rounding).
+// Norm: 1 / rms is a factor of each fp32 sum.  p = x norm_w is exact in two bf16 terms where
+// both are bf16, and h is kept in two, so that only the output is rounded: the error
+// against 64 bits at the Mixtral shape is 0.0017, and 0.0029 with first terms alone.  The
+// second terms of up to 8 tokens are in the instruction's idle columns and cost nothing;
+// those of more are instructions of their own (16 tokens: 447 us, 435 without them).
+// Where LDS has no room for p twice (16 tokens of more than about 2200), it has x, and each
+// wavefront makes both terms beside its loads of weights: some 50 vector instructions for each
+// 16 bytes of a lane, so a unit is 16 columns of F there and they serve two tiles (447 us; 486
+// for one; with E4M3 weights 268 and 360, and 244 without second terms).
 #include <algorithm>
+#include <type_traits>
 
 #include "block.hpp"
 #include "device_common.hpp"
@@ -146,18 +152,34 @@ __global__ __launch_bounds__(64 * kWaves) void decode_route_kernel(DecodeArgs a)
   a.logits[((size_t)blockIdx.x * a.e16 + e0) * kDecodeTokens + threadIdx.x] = s;
 }
 
+// Both terms of x norm_w.
+template <class Tr>
+__device__ __forceinline__ void two_terms(const uint4& x, const uint4& norm_w, uint4& hi, uint4& lo) {
+  float v[Tr::EPC], g[Tr::EPC];
+  widen<Tr>(x, v);
+  widen<Tr>(norm_w, g);
+#pragma unroll
+  for (int j = 0; j < Tr::EPC; ++j) v[j] *= g[j];
+  hi = round_to<Tr>(v);
+  lo = low_terms<Tr>(v, hi);
+}
+
 // Q: E4M3 weights.  B16: the blocked order.  NE: 16-expert tiles of the router at a time; NQ: experts of a lane in
-// the choice.
-template <class Tr, bool Q, bool B16, int NE, int NQ>
+// the choice.  RAW: x is in LDS as it is, both terms of p are made for each chunk of weights, and a unit is two
+// tiles, 16 gate rows and 16 up rows.
+template <class Tr, bool Q, bool B16, int NE, int NQ, bool RAW>
 __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
   using Elt = typename Tr::T;
   constexpr int EB = sizeof(Elt), WB = Q ? 1 : EB, KB = 64 / EB, NB = Q ? 2 : 1;
+  // (with E4M3 a load is two chunks of work: 16 of them in flight take 268 us at 16 tokens of
+  // the Mixtral shape and 8 take 277; bf16 449 and 450)
+  constexpr int TU = RAW ? 2 : 1, kCols = kUnitCols * TU, D = RAW && !Q ? kDepth / 2 : kDepth;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   __shared__ float part_sq[kMaxPieces];
   __shared__ int list[256], wave_count[4];
   __shared__ uint8_t chosen[256];
   __shared__ int claims[8];
-  __shared__ __attribute__((aligned(16))) float scales[Q ? 4 : 1][kWaves * 16];
+  __shared__ __attribute__((aligned(16))) float scales[Q ? 4 : 1][kWaves * 16 * TU];
   const int T = a.T, E = a.E, d = a.d, F = a.F;
   const size_t plane = (size_t)T * d * EB;
   char* xs = lds;                                                       // [1, with x_low 2][d / KB][T][64 bytes]
@@ -170,6 +192,8 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
   const bool normed = a.norm_w != nullptr, route = a.w_router != nullptr;
   const size_t xrow = (size_t)d * EB;
   const int blocks = d / KB;
+  // the second terms of p: in the columns that T leaves, or instructions of their own
+  const bool spare = a.x_low && T <= 8, second = a.x_low && T > 8;
 
   for (int i = threadIdx.x; i < T * E; i += 64 * kWaves) wt[i] = 0.f;
   if (threadIdx.x < 256) chosen[threadIdx.x] = 0;
@@ -213,8 +237,10 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
         }
         sq = wave_fold(in ? sq : 0.f, [](float p, float q) { return p + q; });
         if (lane == 0) part_sq[i] = sq;
-        hi = round_to<Tr>(g);
-        if constexpr (EB == 2) lo = low_terms<Tr>(g, hi);
+        if constexpr (!RAW) {
+          hi = round_to<Tr>(g);
+          if constexpr (EB == 2) lo = low_terms<Tr>(g, hi);
+        }
       }
       if (in) {
         char* to = xs + ((size_t)(c >> 2) * T + t) * 64 + (c & 3) * 16;
@@ -251,20 +277,11 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
         const int b = base + u;
         if (b >= b1) continue;
         const char* from = xs + ((size_t)b * T + tc) * 64 + piece * 16;
-        const uint4 hi = *reinterpret_cast<const uint4*>(from);
-        uint4 lo = make_uint4(0, 0, 0, 0);
-        if (EB == 2 && normed) {
-          if (a.x_low) {
-            lo = *reinterpret_cast<const uint4*>(from + plane);
-          } else {  // no room for them: again from the inputs
-            float x[Tr::EPC], g[Tr::EPC];
-            widen<Tr>(load16(static_cast<const char*>(a.x) + tc * xrow + (size_t)b * 64 + piece * 16), x);
-            widen<Tr>(load16(static_cast<const char*>(a.norm_w) + (size_t)b * 64 + piece * 16), g);
-#pragma unroll
-            for (int j = 0; j < Tr::EPC; ++j) g[j] *= x[j];
-            lo = low_terms<Tr>(g, hi);
-          }
-        }
+        uint4 hi = *reinterpret_cast<const uint4*>(from), lo = make_uint4(0, 0, 0, 0);
+        if constexpr (RAW)
+          two_terms<Tr>(hi, load16(static_cast<const char*>(a.norm_w) + (size_t)b * 64 + piece * 16), hi, lo);
+        else if (EB == 2 && normed)
+          lo = *reinterpret_cast<const uint4*>(from + plane);
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
           acc[i] = mma16<Tr>(wv[u][i], hi, acc[i]);
@@ -389,17 +406,17 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
     for (int i = threadIdx.x; i < n_active * T; i += 64 * kWaves) a.table->weight[i / T][i % T] = wt[list[i / T] * T + i % T];
   }
 
-  // ---- gate and up: units of 8 columns, dealt to groups of wavefronts in turn.  A group
+  // ---- gate and up: units of 8 columns (RAW: 16), dealt to groups of wavefronts in turn.  A group
   // splits K; it is the whole workgroup unless that left a wavefront fewer than 2 kDepth
   // chunks of a unit: with one round of loads between two barriers, 8 tokens with E4M3
   // weights take 237 us and not 213 at the Mixtral shape.  A round then ends one unit at
   // the most, and the code behind a unit's end stands once (inlined at each load the
   // kernel was 60 KB, whose fetches took longer than the first loads of data)
-  const int per = F / kUnitCols, total = n_active * per, chunks = d * WB / 64;
+  const int per = F / kCols, total = n_active * per, chunks = d * WB / 64;
   const int split = chunks >= 16 * kDepth ? 8 : chunks >= 8 * kDepth ? 4 : chunks >= 4 * kDepth ? 2 : 1;
   const int groups = kWaves / split, group = wave / split, part = wave % split;
   const int c0 = chunks * part / split, mine = chunks * (part + 1) / split - c0;
-  const int round = max(mine, kDepth);  // (a narrow unit is padded to a round)
+  const int round = max(mine, D);  // (a narrow unit is padded to a round)
   // The deal: turn i of a workgroup is a unit for each of its groups, from slot base_of(i).
   // The first turns are dealt evenly, the last sixth to whoever is there first, from a
   // counter that decode_route_kernel has cleared: odd dies take 5 to 10 % longer for the
@@ -412,26 +429,27 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
   // Two units share each 1 KB of a blocked matrix's 16 rows: they go to workgroups 8
   // apart, which are on one die
   const auto unit = [&](int slot) {
-    return groups == 1 && (slot | 15) < total ? (slot & ~15) | ((slot & 7) << 1) | ((slot >> 3) & 1) : slot;
+    return TU == 1 && groups == 1 && (slot | 15) < total ? (slot & ~15) | ((slot & 7) << 1) | ((slot >> 3) & 1) : slot;
   };
   const Rows<B16> rows{(size_t)d * WB};
   constexpr int step = Rows<B16>::step;
-  const char* base = static_cast<const char*>(tok < 8 ? a.w_gate : a.w_up) + piece * 16 + (size_t)c0 * step;
+  const char* base = static_cast<const char*>(TU == 2 || tok < 8 ? a.w_gate : a.w_up) + piece * 16 + (size_t)c0 * step;
+  const int64_t to_up = reinterpret_cast<intptr_t>(a.w_up) - reinterpret_cast<intptr_t>(a.w_gate);
   const auto unit_at = [&](int slot) {
     const int u = unit(slot), e = list[u / per];
-    return base + (size_t)e * F * rows.row_bytes + rows.at((u % per) * kUnitCols + (tok & 7));
+    return base + (size_t)e * F * rows.row_bytes + rows.at((u % per) * kCols + (TU == 2 ? tok : tok & 7));
   };
   // E4M3: the scales of a turn's units, 8 of gate's and 8 of up's each, one for a thread; in
   // LDS a turn before they are used, so that finishing a unit waits for no load
   const auto scale_of = [&](int i) {
-    const int slot = base_of(i) + ((int)threadIdx.x >> 4), u = unit(slot);
-    if ((int)threadIdx.x >= groups * 16 || !there(slot)) return 0.f;
-    return ((threadIdx.x & 8) ? a.s_up : a.s_gate)[(size_t)list[u / per] * F + (u % per) * kUnitCols + (threadIdx.x & 7)];
+    const int slot = base_of(i) + (int)threadIdx.x / (2 * kCols), u = unit(slot);
+    if ((int)threadIdx.x >= groups * 2 * kCols || !there(slot)) return 0.f;
+    return ((threadIdx.x & kCols) ? a.s_up : a.s_gate)[(size_t)list[u / per] * F + (u % per) * kCols + (threadIdx.x & (kCols - 1))];
   };
   float scale_next = 0.f;
   int claim_next = 0;
   if constexpr (Q) {
-    if (threadIdx.x < kWaves * 16) {
+    if (threadIdx.x < kWaves * 2 * kCols) {
       scales[0][threadIdx.x] = scale_of(0);
       scale_next = scale_of(1);
     }
@@ -440,33 +458,43 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
   // turn i's sums, which the wavefronts have left in LDS, to h: by one wavefront of each
   // group, each turn another
   const auto finish = [&](int i) {
-    if (Q && threadIdx.x < kWaves * 16) scales[(i + 1) & 3][threadIdx.x] = scale_next;
+    if (Q && threadIdx.x < kWaves * 2 * kCols) scales[(i + 1) & 3][threadIdx.x] = scale_next;
     if (i + 3 >= fixed && threadIdx.x == 0) claims[(i + 3) & 7] = claim_next;
     lds_barrier();
     if (i + 4 >= fixed && threadIdx.x == 0)
       claim_next = __hip_atomic_fetch_add(&a.table->claimed, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (Q && threadIdx.x < kWaves * 16) scale_next = scale_of(i + 2);
+    if (Q && threadIdx.x < kWaves * 2 * kCols) scale_next = scale_of(i + 2);
     const int slot = base_of(i) + group;
-    if (part != i % split || !there(slot)) return;
-    const f32x4_t* from = red + ((i & 1) * kWaves + group * split) * 64 + lane;
-    f32x4_t s = from[0];
-    for (int w = 1; w < split; ++w) s += from[w * 64];
-    const int u = unit(slot), n = u / per, f0 = (u % per) * kUnitCols;
-    // with low terms, columns 8 .. 15 hold those of tokens 0 .. 7
+    const bool mine = part == i % split && there(slot);
+    f32x4_t s[TU];
+    if (mine) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) s[r] = (a.x_low ? s[r] + __shfl_down(s[r], 8) : s[r]) * inv;
-    if constexpr (Q) {
-      const float4 sc = *reinterpret_cast<const float4*>(&scales[i & 3][group * 16 + piece * 4]);
-      s[0] *= sc.x, s[1] *= sc.y, s[2] *= sc.z, s[3] *= sc.w;
+      for (int q = 0; q < TU; ++q) {
+        const f32x4_t* from = red + ((TU == 2 ? q : i & 1) * kWaves + group * split) * 64 + lane;
+        s[q] = from[0];
+        for (int w = 1; w < split; ++w) s[q] += from[w * 64];
+      }
     }
-    // rows 0..7 (pieces 0, 1) are the gate's columns, rows 8..15 the same columns of up
+    if constexpr (TU == 2) lds_barrier();  // (one place for the sums: the next turn's come behind this)
+    if (!mine) return;
+    const int u = unit(slot), n = u / per, f0 = (u % per) * kCols;
+#pragma unroll
+    for (int q = 0; q < TU; ++q) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[q][r] = (spare ? s[q][r] + __shfl_down(s[q][r], 8) : s[q][r]) * inv;
+      if constexpr (Q) {
+        const float4 sc = *reinterpret_cast<const float4*>(&scales[i & 3][(group * TU + q) * 16 + piece * 4]);
+        s[q][0] *= sc.x, s[q][1] *= sc.y, s[q][2] *= sc.z, s[q][3] *= sc.w;
+      }
+    }
+    // one tile: rows 0..7 (pieces 0, 1) are the gate's columns, rows 8..15 the same of up
     float hv[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float up = __shfl_down(s[r], 32);
-      hv[r] = s[r] / (1.f + __expf(-s[r])) * up;
+      const float up = TU == 2 ? s[TU - 1][r] : __shfl_down(s[0][r], 32);
+      hv[r] = s[0][r] / (1.f + __expf(-s[0][r])) * up;
     }
-    if (piece < 2 && tok < T) {
+    if ((TU == 2 || piece < 2) && tok < T) {
       const int f = f0 + piece * 4;
       char* to = static_cast<char*>(a.h) + (((size_t)n * (F / KB) + f / KB) * (a.h_low ? 2 * T : T) + tok) * 64 + (f % KB) * EB;
       store4<Tr>(to, hv[0], hv[1], hv[2], hv[3]);
@@ -486,43 +514,72 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
     // behind the last unit repeats its last chunk
     int li = 0, lc = 0, slot = base_of(1) + group;
     const char *lp = unit_at(u0 + group), *next = unit_at(there(slot) ? slot : u0 + group);
+    const char* const g0 = static_cast<const char*>(a.norm_w) + (size_t)c0 * NB * 64 + (Q ? piece * 32 : piece * 16);
+    const char* gp = g0;
     bool more = there(slot), moved = false;
-    const auto load = [&]() {
-      const uint4 v = load_weights<B16>(lp);
-      if (++lc < mine) lp += step;
+    uint4 ring[D][TU], gains[RAW ? D : 1][NB];
+    const auto load = [&](int j) {
+      ring[j][0] = load_weights<B16>(lp);
+      if constexpr (TU == 2) ring[j][TU - 1] = load_weights<B16>(lp + to_up);
+      if constexpr (RAW) {
+#pragma unroll
+        for (int q = 0; q < NB; ++q) gains[j][q] = load16(gp + q * 16);
+      }
+      if (++lc < mine) {
+        lp += step;
+        gp += NB * 64;
+      }
       if (lc == round && more) {
         ++li;
         lc = 0;
         lp = next;
+        gp = g0;
         moved = true;
       }
-      return v;
     };
-    const int col = a.x_low ? min(tok & 7, T - 1) : tc;
-    const char* xlane = xs + (a.x_low && tok >= 8 ? plane : 0) + (size_t)c0 * NB * T * 64 +
+    const int col = spare ? min(tok & 7, T - 1) : tc;
+    const char* xlane = xs + (spare && tok >= 8 ? plane : 0) + (size_t)c0 * NB * T * 64 +
                         (Q ? ((size_t)(piece >> 1) * T + col) * 64 + (piece & 1) * 32 : (size_t)col * 64 + piece * 16);
     int uc = 0;
     bool alive = true, ended = false;
-    f32x4_t acc{0.f, 0.f, 0.f, 0.f};
-    const auto work = [&](const uint4& w) {
+    f32x4_t acc[TU];
+#pragma unroll
+    for (int q = 0; q < TU; ++q) acc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const auto work = [&](int j) {
       if (!alive) return;
       if (uc < mine) {
         uint4 b[NB];
 #pragma unroll
-        for (int j = 0; j < NB; ++j) b[j] = *reinterpret_cast<const uint4*>(xlane + (size_t)uc * NB * T * 64 + j * 16);
-        acc = mma_chunk<Tr, Q>(w, b, acc);
+        for (int q = 0; q < NB; ++q) b[q] = *reinterpret_cast<const uint4*>(xlane + (size_t)uc * NB * T * 64 + q * 16);
+        if constexpr (RAW) {
+          uint4 lo[NB];
+#pragma unroll
+          for (int q = 0; q < NB; ++q) two_terms<Tr>(b[q], gains[j][q], b[q], lo[q]);
+#pragma unroll
+          for (int q = 0; q < TU; ++q) acc[q] = mma_chunk<Tr, Q>(ring[j][q], lo, acc[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < TU; ++q) acc[q] = mma_chunk<Tr, Q>(ring[j][q], b, acc[q]);
+        if (EB == 2 && !RAW && second) {
+#pragma unroll
+          for (int q = 0; q < NB; ++q)
+            b[q] = *reinterpret_cast<const uint4*>(xlane + plane + (size_t)uc * NB * T * 64 + q * 16);
+          acc[0] = mma_chunk<Tr, Q>(ring[j][0], b, acc[0]);
+        }
       }
       if (++uc == round) {
-        red[((turn & 1) * kWaves + wave) * 64 + lane] = acc;
+#pragma unroll
+        for (int q = 0; q < TU; ++q) {
+          red[((TU == 2 ? q : turn & 1) * kWaves + wave) * 64 + lane] = acc[q];
+          acc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
         uc = 0;
-        acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
         ended = true;
         alive = li > turn;  // the cursor is kDepth loads ahead, in the next unit if there is one
       }
     };
-    uint4 ring[kDepth];
 #pragma unroll
-    for (int j = 0; j < kDepth; ++j) ring[j] = load();
+    for (int j = 0; j < D; ++j) load(j);
     while (alive) {
       if (moved) {
         slot = base_of(li + 1) + group;
@@ -531,9 +588,9 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
         moved = false;
       }
 #pragma unroll
-      for (int j = 0; j < kDepth; ++j) {
-        work(ring[j]);
-        ring[j] = load();
+      for (int j = 0; j < D; ++j) {
+        work(j);
+        load(j);
       }
       if (ended) {
         finish(turn++);
@@ -546,8 +603,9 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
 
 // One part of the K range of 16 NR columns of d: out's columns where the tile has one part,
 // else partial sums, which the workgroup that is done last adds up in the parts'
-// order.  The columns share each load of h, which every tile reads whole.
-template <class Tr, bool Q, bool B16, int NR>
+// order.  The columns share each load of h, which every tile reads whole.  TWO: h's second
+// terms are loads and instructions of their own.
+template <class Tr, bool Q, bool B16, int NR, bool TWO>
 __global__ __launch_bounds__(64 * kDownWaves) void decode_down_kernel(DecodeArgs a) {
   using Elt = typename Tr::T;
   constexpr int EB = sizeof(Elt), WB = Q ? 1 : EB, NB = Q ? 2 : 1, D = NR == 1 ? 8 : 4, kCols = NR * 16;
@@ -557,7 +615,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void decode_down_kernel(DecodeArgs
   __shared__ int list[256];
   __shared__ int last;
   const int T = a.T, d = a.d, F = a.F;
-  const int lane = threadIdx.x & 63, tok = lane & 15, piece = lane >> 4, tc = min(tok, T - 1);
+  const int lane = threadIdx.x & 63, tok = lane & 15, piece = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tile = (int)blockIdx.x, part = (int)blockIdx.y, o0 = tile * kCols;
   // the table, as much of it as there may be, without waiting for its length
@@ -589,17 +647,29 @@ __global__ __launch_bounds__(64 * kDownWaves) void decode_down_kernel(DecodeArgs
     const char* base = static_cast<const char*>(a.w_down) + rows.at(o0 + tok) + piece * 16;
     const size_t tile_bytes = 16 * rows.row_bytes, expert_bytes = (size_t)d * rows.row_bytes;
     const int cols = a.h_low ? 2 * T : T, bstep = cols * 64 * NB;
-    const int col = a.h_low ? min(tok & 7, T - 1) + (tok >> 3) * T : tc, wcol = a.h_low ? tok & 7 : tok;
+    const bool spare = !TWO && a.h_low;
+    const int wcol = spare ? tok & 7 : tok;
+    // h's column for this lane: its token's, or, where that did not choose the expert,
+    // the first's that did, so that no line is read for it
+    const auto column = [&](int n) {
+      const bool has = wcol < T && wts[n][wcol] != 0.f;
+      const int any = max(__ffsll((unsigned long long)__ballot(has)) - 1, 0) & (spare ? 7 : 15);
+      const int col = (has ? wcol : any) + (spare && tok >= 8 ? T : 0);
+      return static_cast<const char*>(a.h) +
+             (Q ? ((size_t)(piece >> 1) * cols + col) * 64 + (piece & 1) * 32 : (size_t)col * 64 + piece * 16);
+    };
     int ln = i0 / per, lc = i0 % per, li = i0;
     const char* lp = base + list[ln] * expert_bytes + (size_t)lc * step;
-    const char* bp = static_cast<const char*>(a.h) + (size_t)i0 * bstep +
-                     (Q ? ((size_t)(piece >> 1) * cols + col) * 64 + (piece & 1) * 32 : (size_t)col * 64 + piece * 16);
-    uint4 ring[D][NR], act[D][NB];
+    const char* bp = column(ln) + (size_t)i0 * bstep;
+    uint4 ring[D][NR], act[D][NB], low[D][NB];
     const auto load = [&](int j) {
 #pragma unroll
       for (int q = 0; q < NR; ++q) ring[j][q] = load_weights<B16>(lp + q * tile_bytes);
 #pragma unroll
-      for (int q = 0; q < NB; ++q) act[j][q] = load16(bp + q * 16);
+      for (int q = 0; q < NB; ++q) {
+        act[j][q] = load16(bp + q * 16);
+        if constexpr (TWO) low[j][q] = load16(bp + (size_t)T * 64 + q * 16);
+      }
       if (++li >= i1) return;  // behind the last chunk: it again
       bp += bstep;
       if (++lc < per) {
@@ -607,6 +677,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void decode_down_kernel(DecodeArgs
       } else {
         lc = 0;
         lp = base + list[++ln] * expert_bytes;
+        bp = column(ln) + (size_t)li * bstep;
       }
     };
     int n = i0 / per, c = i0 % per, since = 0;
@@ -630,7 +701,10 @@ __global__ __launch_bounds__(64 * kDownWaves) void decode_down_kernel(DecodeArgs
     };
     const auto work = [&](int j) {
 #pragma unroll
-      for (int q = 0; q < NR; ++q) acc[q] = mma_chunk<Tr, Q>(ring[j][q], act[j], acc[q]);
+      for (int q = 0; q < NR; ++q) {
+        acc[q] = mma_chunk<Tr, Q>(ring[j][q], act[j], acc[q]);
+        if constexpr (TWO) acc[q] = mma_chunk<Tr, Q>(ring[j][q], low[j], acc[q]);
+      }
       ++since;
       if (++c == per) {
         fold();
@@ -665,7 +739,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void decode_down_kernel(DecodeArgs
     v = red[0][q][lane];
 #pragma unroll
     for (int w = 1; w < kDownWaves; ++w) v += red[w][q][lane];
-    if (a.h_low) {
+    if (!TWO && a.h_low) {
 #pragma unroll
       for (int w = 0; w < kDownWaves; ++w) v += red[w][q][lane + 8];
     }
@@ -711,31 +785,47 @@ template <class Tr, bool Q, bool B16>
 hipError_t decode_t(DecodeArgs a, hipStream_t stream) {
   constexpr int EB = sizeof(typename Tr::T);
   size_t lds = decode_lds_bytes(EB, a.T, a.d, a.E);
-  const size_t both = lds + (size_t)a.T * a.d * EB;
-  a.x_low = a.h_low && a.norm_w != nullptr && both <= kDecodeLds;
-  if (a.x_low) lds = both;
+  a.x_low = a.norm_w != nullptr && decode_x_low(EB, a.T, a.d, a.E);
+  if (a.x_low) lds += (size_t)a.T * a.d * EB;
   if (a.logits != nullptr) {
     hipLaunchKernelGGL(decode_route_kernel<Tr>, dim3(a.ranges, a.e16 / 16), dim3(64 * kWaves), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const int64_t units = (int64_t)std::min(a.E, a.T * a.k) * (a.F / kUnitCols);
+  const bool raw = EB == 2 && a.norm_w != nullptr && !a.x_low;
+  const int64_t units = (int64_t)std::min(a.E, a.T * a.k) * (a.F / (raw ? 2 * kUnitCols : kUnitCols));
   const dim3 grid((unsigned)std::min<int64_t>(units, kMaxGrid));
   const auto up = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), lds, stream, a); };
-  if (a.E <= 16)
-    up(decode_up_kernel<Tr, Q, B16, 1, 1>);
-  else if (a.E <= 64)
-    up(decode_up_kernel<Tr, Q, B16, 4, 1>);
+  const auto up_of = [&](auto raw_t) {
+    constexpr bool RAW = decltype(raw_t)::value;
+    if (a.E <= 16)
+      up(decode_up_kernel<Tr, Q, B16, 1, 1, RAW>);
+    else if (a.E <= 64)
+      up(decode_up_kernel<Tr, Q, B16, 4, 1, RAW>);
+    else
+      up(decode_up_kernel<Tr, Q, B16, 4, 4, RAW>);
+  };
+  if (raw)
+    up_of(std::bool_constant<EB == 2>{});
   else
-    up(decode_up_kernel<Tr, Q, B16, 4, 4>);
+    up_of(std::false_type{});
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 tiles(a.d / decode_down_cols(a.T, a.d), a.parts);
   const auto down = [&](auto kernel) { hipLaunchKernelGGL(kernel, tiles, dim3(64 * kDownWaves), 0, stream, a); };
+  if constexpr (EB == 2) {
+    if (a.T > 8) {
+      if (decode_down_cols(a.T, a.d) == 16)
+        down(decode_down_kernel<Tr, Q, B16, 1, true>);
+      else
+        down(decode_down_kernel<Tr, Q, B16, 4, true>);
+      return hipGetLastError();
+    }
+  }
   if (decode_down_cols(a.T, a.d) == 16)
-    down(decode_down_kernel<Tr, Q, B16, 1>);
+    down(decode_down_kernel<Tr, Q, B16, 1, false>);
   else
-    down(decode_down_kernel<Tr, Q, B16, 4>);
+    down(decode_down_kernel<Tr, Q, B16, 4, false>);
   return hipGetLastError();
 }
 
@@ -744,6 +834,10 @@ hipError_t decode_t(DecodeArgs a, hipStream_t stream) {
 // x [T][d], the wavefronts' sums, logits and weights [T][E] each.
 size_t decode_lds_bytes(int elt_bytes, int T, int d, int E) {
   return (size_t)T * d * elt_bytes + kRedBytes + (size_t)8 * T * E;
+}
+
+bool decode_x_low(int elt_bytes, int T, int d, int E) {
+  return elt_bytes == 2 && decode_lds_bytes(elt_bytes, T, d, E) + (size_t)T * d * elt_bytes <= kDecodeLds;
 }
 
 hipError_t launch_decode(int dtype, const DecodeArgs& a, hipStream_t stream) {

@@ -529,13 +529,16 @@ moe_status_t moe_dropout(const void* x, int64_t n, int dtype, float p, const uin
                          hipStream_t stream);
 
 /* ---- the layer for a few tokens ---------------------------------------------
- * moe_forward for a serving step: a whole pre-norm block in two kernels.
+ * moe_forward for a serving step: a whole pre-norm block in two kernels, or three
+ * where the router's weights are many.
  *   m = x r(x) norm_w  (or x without norm_w)
  *   routing of m as moe_route's (w_router not NULL), or topk_ids and topk_w
  *   out = res + scale sum_j topk_w[t,j] (silu(m W_gate^T) (m W_up^T)) W_down^T
- * (without res: the sum alone, scaled).  The logits have fp32's accuracy; m and h
- * are rounded to dtype for the experts' products, everything else is fp32 with one
- * rounding of out.  Capacity and tile_rows do not matter: no entry is dropped.
+ * (without res: the sum alone, scaled).  Everything has fp32's accuracy or, in bf16,
+ * two bf16 terms (x norm_w exactly, h to 2^-16), with one rounding of out: a batch as
+ * moe_norm, moe_forward and moe_residual give it, without the roundings between
+ * them.  x^2 d must stay in fp32's range.  Capacity and tile_rows do not matter: no entry
+ * is dropped.
  *  - T <= 16, and x must fit in a workgroup's LDS: T d element size + 8 T E <=
  *    141312 bytes (16 tokens of 4096 bf16 with up to 80 experts, 8 of 7168 with
  *    256); else MOE_ERR_UNSUPPORTED, and moe_forward takes the batch.

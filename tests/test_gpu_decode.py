@@ -158,6 +158,23 @@ def _given(T, k, E, drop=0.2):
     return make
 
 
+@pytest.mark.parametrize("T,d,E,F", [(3, 256, 4, 192), (8, 1024, 4, 256), (9, 256, 4, 192), (16, 1024, 5, 320),
+                                     (16, 2304, 4, 128), (16, 4096, 4, 192), (8, 6144, 4, 128), (1, 512, 4, 64)])
+@pytest.mark.parametrize("layout,fp8", [(0, False), (1, False), (0, True), (1, True)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_bf16_is_rounded_once(T, d, E, F, layout, fp8, norm):
+    """p and h are kept in two terms each, wherever the second ones are, so all that is left is the output's rounding:
+    even over a step, which is 2^-7 |v| at the most, that is a root mean square of 2^-7 |v| / sqrt(12) at the most
+    (0.0023; over the values of a step about 0.0017).  One term of both comes to 0.0029."""
+    print(f"\n[gpu] decode rounded once T={T} d={d} E={E} F={F} layout={layout} fp8={fp8} norm={norm}", flush=True)
+    c = Case(T, d, E, 2, F, fp8=fp8, norm=norm, res=False, layout=layout, given=_given(T, 2, E, drop=0.0), seed=T + d)
+    got = c.check()
+    want, _ = K.decode(host64(c.x), None if c.norm is None else host64(c.norm), EPS, c.ids.cpu().numpy(), host64(c.tw),
+                       *c.w64, None, 1.0, "bf16")
+    err = np.linalg.norm(host64(got) - want) / np.linalg.norm(want)
+    assert err <= 2.0**-7 / 12**0.5, err
+
+
 @pytest.mark.parametrize("dtype,fp8", [("bf16", False), ("f32", False), ("bf16", True)])
 @pytest.mark.parametrize("T,E,k", [(1, 4, 2), (7, 3, 3), (16, 100, 6)])
 def test_given_routing_with_repeats_and_gaps(T, E, k, dtype, fp8):

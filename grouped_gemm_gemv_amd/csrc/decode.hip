@@ -35,7 +35,6 @@
 // 16 bytes of a lane, so a unit is 16 columns of F there and they serve two tiles (447 us; 486
 // for one; with E4M3 weights 268 and 360, and 244 without second terms).
 #include <algorithm>
-#include <type_traits>
 
 #include "block.hpp"
 #include "device_common.hpp"
@@ -796,19 +795,22 @@ hipError_t decode_t(DecodeArgs a, hipStream_t stream) {
   const int64_t units = (int64_t)std::min(a.E, a.T * a.k) * (a.F / (raw ? 2 * kUnitCols : kUnitCols));
   const dim3 grid((unsigned)std::min<int64_t>(units, kMaxGrid));
   const auto up = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), lds, stream, a); };
-  const auto up_of = [&](auto raw_t) {
-    constexpr bool RAW = decltype(raw_t)::value;
-    if (a.E <= 16)
-      up(decode_up_kernel<Tr, Q, B16, 1, 1, RAW>);
-    else if (a.E <= 64)
-      up(decode_up_kernel<Tr, Q, B16, 4, 1, RAW>);
-    else
-      up(decode_up_kernel<Tr, Q, B16, 4, 4, RAW>);
+  const auto up_raw = [&]() {  // (rows so wide route up to 7 experts in this kernel and more of them apart)
+    if constexpr (EB == 2) {
+      if (a.E <= 64)
+        up(decode_up_kernel<Tr, Q, B16, 1, 1, true>);
+      else
+        up(decode_up_kernel<Tr, Q, B16, 1, 4, true>);
+    }
   };
   if (raw)
-    up_of(std::bool_constant<EB == 2>{});
+    up_raw();
+  else if (a.E <= 16)
+    up(decode_up_kernel<Tr, Q, B16, 1, 1, false>);
+  else if (a.E <= 64)
+    up(decode_up_kernel<Tr, Q, B16, 4, 1, false>);
   else
-    up_of(std::false_type{});
+    up(decode_up_kernel<Tr, Q, B16, 4, 4, false>);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 tiles(a.d / decode_down_cols(a.T, a.d), a.parts);

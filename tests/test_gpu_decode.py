@@ -150,6 +150,18 @@ def test_wide_rows(dtype, T, d, E, k, F):
     Case(T, d, E, k, F, dtype=dtype, layout=1, seed=11).check()
 
 
+@pytest.mark.parametrize("T,d,E,k,F,fp8,layout", [
+    (16, 2304, 4, 2, 128, False, 0), (12, 3584, 4, 2, 192, True, 1),  # x once in LDS, routed beside the products
+    (16, 4096, 80, 8, 64, True, 1), (16, 4096, 80, 8, 64, False, 0),  # all of LDS: 141312 bytes of x, logits and weights
+    (9, 4096, 256, 16, 64, False, 1),                                 # four experts of a lane
+    (1, 70592, 1, 1, 64, False, 0), (1, 70592, 2, 1, 64, True, 1),    # the widest row, four thousand tiles of columns
+    (16, 2048, 20, 3, 64, False, 0),                                  # both terms in LDS, instructions of their own
+])
+def test_wide_rows_with_a_router(T, d, E, k, F, fp8, layout):
+    print(f"\n[gpu] decode T={T} d={d} E={E} k={k} F={F} fp8={fp8} layout={layout}", flush=True)
+    Case(T, d, E, k, F, fp8=fp8, layout=layout, bias=True, seed=T + E).check()
+
+
 def _given(T, k, E, drop=0.2):
     def make(rng):
         ids = rng.integers(0, E, (T, k))  # the same expert may come twice

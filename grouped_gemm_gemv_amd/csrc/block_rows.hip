@@ -280,7 +280,8 @@ __global__ __launch_bounds__(block_of(NT)) void residual_backward_kernel(Residua
       }
     }
     if (a.next_w != nullptr || a.post_w != nullptr) row_sum<NT>(s, part1[place]);
-    const float r1 = inv_rms(s[0], inv_d, a.eps), k1 = -r1 * r1 * r1 * (s[1] * inv_d);
+    // (the mean first: r1^3 alone leaves fp32 for rows below 1e-12 or above 1e12)
+    const float r1 = inv_rms(s[0], inv_d, a.eps), k1 = -(s[1] * inv_d * r1) * r1 * r1;
     const float r2 = a.post_w != nullptr ? inv_rms(s[2], inv_d, a.eps) : 1.f;
     float D[V][EPC];
 #pragma unroll
@@ -358,18 +359,18 @@ __global__ __launch_bounds__(block_of(NT)) void residual_backward_kernel(Residua
       else
         static_cast<float*>(a.dgate)[t] = g;
     }
-    const float k2 = -mg * r2 * r2 * (cy[0] * inv_d);
+    const float k2 = -(cy[0] * inv_d * r2) * r2;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * NT;
-#pragma unroll
-      for (int j = 0; j < EPC; ++j) D[i][j] *= mg;
       if (a.post_w != nullptr) {
         float y[EPC];
         widen<Tr>(yc[i], y);
 #pragma unroll
         for (int j = 0; j < EPC; ++j) D[i][j] = fmaf(y[j], k2, D[i][j]);
       }
+#pragma unroll
+      for (int j = 0; j < EPC; ++j) D[i][j] *= mg;
       put(to(a.dy), c, chunks, round_to<Tr>(D[i]));
     }
     if (kAhead) {

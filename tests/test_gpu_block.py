@@ -279,6 +279,60 @@ def test_dropout_past_2_31_elements():
         assert np.array_equal(x[at:at + 88].float().cpu().numpy(), np.where(halves >= 32768, 2.0, 0.0)), at
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_of_any_size_and_a_small_eps(dtype):
+    """1 / rms of 1e-15 to 1e15, whose cube no fp32 number holds, and rows of zeros beside an eps of 1e-30."""
+    import grouped_gemm_gemv_amd as M
+    eps = 1e-30
+    c = Case(7, 320, dtype, gate="token", scale=0.5, seed=8)
+    c.r = M.Residual(eps, c.scale, 0.0)
+    rng = np.random.default_rng(80)
+    for t, (a, b) in enumerate([(1e15, 1e-15), (1e-15, 1e15), (1e15, 1e15), (1e-15, 1e-15), (0, 0), (1, 0), (0, 1)]):
+        c.res[t], c.y[t] = _t(rng.standard_normal(320) * a, dtype), _t(rng.standard_normal(320) * b, dtype)
+    out, n = c.forward()
+    want = K.residual(c.h(c.res), c.h(c.y), c.h(c.post), c.hgate(), None, c.h(c.next), float(np.float32(eps)), 0.5, dtype)
+    close("out", out, want["out"])
+    close("n", n, want["n"])
+    c.res[4] = 0
+    x = c.res  # (any row may stand for the sum)
+    got = c.backward(x)
+    want = K.residual_backward(c.h(x), c.h(c.y), c.h(c.post), c.hgate(), None, c.h(c.next), c.h(c.dout), c.h(c.dn),
+                               float(np.float32(eps)), 0.5, dtype)
+    for name in ("dres", "dy", "dpost", "dnext"):
+        assert torch.isfinite(got[name].float()).all(), name
+        close(name, got[name], want[name])
+
+
+def test_rows_past_2_31_elements():
+    """The last rows of arrays of 4.4 GB are those of a small batch of their own; their masks those of the flat array."""
+    import grouped_gemm_gemv_amd as M
+    T, d, last = 270000, 8192, 3
+    c, bf = Case(last, d, gate="token", seed=10), torch.bfloat16
+    big = M.Shape(T, d, 1, 1, 64, dtype=bf)
+    want, want_n = c.forward()
+    g = c.backward(want)
+
+    def grown(v):
+        b = torch.ones((T,) + tuple(v.shape[1:]), dtype=bf, device="cuda")
+        b[-last:] = v
+        return b
+
+    res, y, gate = grown(c.res), grown(c.y), grown(c.gate)
+    out, n = torch.empty_like(res), torch.empty_like(res)
+    M.moe_residual(big, c.r, res, y, c.post, gate, None, c.next, out, n)
+    assert np.array_equal(bits(out[-last:]), bits(want)) and np.array_equal(bits(n[-last:]), bits(want_n))
+    dout, dn = grown(c.dout), grown(c.dn)
+    dres, dy, dgate = res, n, torch.empty_like(gate)
+    M.moe_residual_backward(big, c.r, out, y, c.post, gate, None, c.next, dout, dn, dres, dy, dgate, None, None,
+                            M.workspace(M.residual_workspace_size(big)))
+    for name, v in (("dres", dres), ("dy", dy), ("dgate", dgate)):
+        assert np.array_equal(bits(v[-last:]), bits(g[name])), name
+    rng = torch.tensor([77, 3], device="cuda")
+    M.moe_residual(big, M.Residual(dropout=0.5), dres.zero_(), y, None, None, rng, None, out, None)
+    M.moe_dropout(y, 0.5, rng, dn)
+    assert torch.equal(out[-2 * last:], dn[-2 * last:]) and torch.equal(out[131070:131075], dn[131070:131075])
+
+
 # ---- how calls may be made ----
 
 

@@ -320,19 +320,25 @@ def _ws(ws: torch.Tensor, device):
     return _p(ws), ws.numel() * ws.element_size()
 
 
+_gpus = set()  # devices that are GPUs
+
+
 def _call(name: str, device, stream, *args):
     """One entry point on the tensors' device, on `stream` or that device's current stream."""
-    if device.type != "cuda":
-        raise ValueError("libmoe takes device tensors")
+    if device not in _gpus:  # (the name of its type takes longer to make than all else here)
+        if device.type != "cuda":
+            raise ValueError("libmoe takes device tensors")
+        _gpus.add(device)
+    index = device.index
     if stream is None:
         # (the handle alone: a Stream object around it takes longer than the rest of this function)
-        s = torch._C._cuda_getCurrentRawStream(device.index)
+        s = torch._C._cuda_getCurrentRawStream(index)
     elif stream.device != device:
         raise ValueError(f"stream is on {stream.device}, expected {device}")
     else:
         s = stream.cuda_stream
     fn = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
+    if index == torch.cuda.current_device():
         status = fn(*args, s)
     else:
         with torch.cuda.device(device):

@@ -35,6 +35,7 @@
 // 16 bytes of a lane, so a unit is 16 columns of F there and they serve two tiles (447 us; 486
 // for one; with E4M3 weights 268 and 360, and 244 without second terms).
 #include <algorithm>
+#include <type_traits>
 
 #include "block.hpp"
 #include "device_common.hpp"
@@ -43,14 +44,14 @@
 namespace moe {
 namespace {
 
-// Weights: read once, by one workgroup, past the caches where they are blocked (a load is
-// 512 bytes or 1 KB in one piece): 8 tokens of the Mixtral shape take 391 us so and 423
-// with the default policy.  From row-major weights a load takes half a line of each of
-// 16 rows, and the next load finds the other half where the line was kept: 64 experts and
-// 16 tokens 184 us, 197 past the caches.
-template <bool B16>
+// Weights: read once, by one workgroup, past the caches (PAST) where a load takes whole lines: 8
+// tokens of the Mixtral shape take 391 us so and 423 with the default policy, row-major 400
+// and 425.  A load of half a line of each of 16 rows leaves the other half to the next
+// one, which finds it where the line was kept: 64 experts and 16 tokens 184 us, 197 past the
+// caches, and 161 in whole lines.
+template <bool PAST>
 __device__ __forceinline__ uint4 load_weights(const char* p) {
-  if constexpr (B16)
+  if constexpr (PAST)
     return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
   else
     return load16(p);
@@ -73,14 +74,46 @@ constexpr size_t kRedBytes = 2 * kWaves * 1024;
 
 // Storage of the weights: bytes from one row, and from one 64-byte piece of a row, to
 // the next.
-template <bool B16>
+template <bool B16, bool LINES>
 struct Rows {
   size_t row_bytes;
   __device__ __forceinline__ size_t at(int row) const {
     return B16 ? (size_t)(row >> 4) * 16 * row_bytes + (size_t)(row & 15) * 64 : (size_t)row * row_bytes;
   }
-  static constexpr int step = B16 ? 1024 : 64;
+  static constexpr int step = B16 ? 1024 : LINES ? 128 : 64;
 };
+
+// Row-major weights are loaded in whole lines (LINES), 128 bytes of 8 rows at a time:
+// lane l has piece l >> 3 of row l & 7 and, from a second load, of row 8 + (l & 7).  A
+// change between the halves of each sixteen lanes makes two operands of that: lane l has
+// row l & 15, and of its 8 pieces 2 (l >> 4) in the first and the next one in the
+// second.  (E4M3 rows of an odd number of 64 bytes have no last line: they are loaded by 16
+// rows of half a line.)
+__device__ __forceinline__ void change_halves(uint4& v0, uint4& v1) {
+  const auto from = [](unsigned keep, unsigned other, auto banks) {  // lane l takes lane l ^ 8's in these banks of 4
+    return (unsigned)__builtin_amdgcn_update_dpp((int)keep, (int)other, 0x128, 0xf, decltype(banks)::value, false);
+  };
+  constexpr std::integral_constant<int, 0xC> upper{};
+  constexpr std::integral_constant<int, 0x3> lower{};
+  const uint4 a{from(v0.x, v1.x, upper), from(v0.y, v1.y, upper), from(v0.z, v1.z, upper), from(v0.w, v1.w, upper)};
+  v1 = uint4{from(v1.x, v0.x, lower), from(v1.y, v0.y, lower), from(v1.z, v0.z, lower), from(v1.w, v0.w, lower)};
+  v0 = a;
+}
+
+// Where a lane's part of x norm_w and h starts in a step's blocks [columns][64 bytes]: it is as
+// long as its weights', which in lines are two pieces of 16 bytes and in E4M3 half as long as
+// their operands.
+template <bool Q, bool LINES>
+__device__ __forceinline__ size_t act_offset(int piece, int col, int cols) {
+  constexpr int parts = Q && LINES ? 1 : Q || LINES ? 2 : 4;  // of a block
+  return ((size_t)(piece / parts) * cols + col) * 64 + piece % parts * (64 / parts);
+}
+
+// Operand h of a step's: NB chunks of it.
+template <int NB, int N>
+__device__ __forceinline__ const uint4 (&pick(const uint4 (&v)[N], int h))[NB] {
+  return reinterpret_cast<const uint4(&)[NB]>(v[h * NB]);
+}
 
 template <class Tr, bool Q>
 __device__ __forceinline__ f32x4_t mma_chunk(const uint4& w, const uint4 (&b)[Q ? 2 : 1], f32x4_t acc) {
@@ -166,13 +199,14 @@ __device__ __forceinline__ void two_terms(const uint4& x, const uint4& norm_w, u
 // Q: E4M3 weights.  B16: the blocked order.  NE: 16-expert tiles of the router at a time; NQ: experts of a lane in
 // the choice.  RAW: x is in LDS as it is, both terms of p are made for each chunk of weights, and a unit is two
 // tiles, 16 gate rows and 16 up rows.
-template <class Tr, bool Q, bool B16, int NE, int NQ, bool RAW>
+template <class Tr, bool Q, bool B16, bool LINES, int NE, int NQ, bool RAW>
 __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
   using Elt = typename Tr::T;
   constexpr int EB = sizeof(Elt), WB = Q ? 1 : EB, KB = 64 / EB, NB = Q ? 2 : 1;
   // (with E4M3 a load is two chunks of work: 16 of them in flight take 268 us at 16 tokens of
   // the Mixtral shape and 8 take 277; bf16 449 and 450)
-  constexpr int TU = RAW ? 2 : 1, kCols = kUnitCols * TU, D = RAW && !Q ? kDepth / 2 : kDepth;
+  constexpr int CH = LINES ? 2 : 1;  // 64-byte chunks of K of a step
+  constexpr int TU = RAW ? 2 : 1, kCols = kUnitCols * TU, D = (RAW && !Q ? kDepth / 2 : kDepth) / CH;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   __shared__ float part_sq[kMaxPieces];
   __shared__ int list[256], wave_count[4];
@@ -411,8 +445,8 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
   // weights take 237 us and not 213 at the Mixtral shape.  A round then ends one unit at
   // the most, and the code behind a unit's end stands once (inlined at each load the
   // kernel was 60 KB, whose fetches took longer than the first loads of data)
-  const int per = F / kCols, total = n_active * per, chunks = d * WB / 64;
-  const int split = chunks >= 16 * kDepth ? 8 : chunks >= 8 * kDepth ? 4 : chunks >= 4 * kDepth ? 2 : 1;
+  const int per = F / kCols, total = n_active * per, chunks = d * WB / 64 / CH;
+  const int split = chunks * CH >= 16 * kDepth ? 8 : chunks * CH >= 8 * kDepth ? 4 : chunks * CH >= 4 * kDepth ? 2 : 1;
   const int groups = kWaves / split, group = wave / split, part = wave % split;
   const int c0 = chunks * part / split, mine = chunks * (part + 1) / split - c0;
   const int round = max(mine, D);  // (a narrow unit is padded to a round)
@@ -430,13 +464,16 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
   const auto unit = [&](int slot) {
     return TU == 1 && groups == 1 && (slot | 15) < total ? (slot & ~15) | ((slot & 7) << 1) | ((slot >> 3) & 1) : slot;
   };
-  const Rows<B16> rows{(size_t)d * WB};
-  constexpr int step = Rows<B16>::step;
-  const char* base = static_cast<const char*>(TU == 2 || tok < 8 ? a.w_gate : a.w_up) + piece * 16 + (size_t)c0 * step;
+  const Rows<B16, LINES> rows{(size_t)d * WB};
+  constexpr int step = Rows<B16, LINES>::step;
+  const int my_piece = LINES ? lane >> 3 : piece;
+  const char* base = static_cast<const char*>(LINES || TU == 2 || tok < 8 ? a.w_gate : a.w_up) + my_piece * 16 + (size_t)c0 * step;
   const int64_t to_up = reinterpret_cast<intptr_t>(a.w_up) - reinterpret_cast<intptr_t>(a.w_gate);
+  // to the second load of a tile in lines: its rows 8 .. 15
+  const int64_t to_half = TU == 2 ? (int64_t)(8 * rows.row_bytes) : to_up;
   const auto unit_at = [&](int slot) {
     const int u = unit(slot), e = list[u / per];
-    return base + (size_t)e * F * rows.row_bytes + rows.at((u % per) * kCols + (TU == 2 ? tok : tok & 7));
+    return base + (size_t)e * F * rows.row_bytes + rows.at((u % per) * kCols + (TU == 2 && !LINES ? tok : tok & 7));
   };
   // E4M3: the scales of a turn's units, 8 of gate's and 8 of up's each, one for a thread; in
   // LDS a turn before they are used, so that finishing a unit waits for no load
@@ -513,20 +550,23 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
     // behind the last unit repeats its last chunk
     int li = 0, lc = 0, slot = base_of(1) + group;
     const char *lp = unit_at(u0 + group), *next = unit_at(there(slot) ? slot : u0 + group);
-    const char* const g0 = static_cast<const char*>(a.norm_w) + (size_t)c0 * NB * 64 + (Q ? piece * 32 : piece * 16);
+    const char* const g0 = static_cast<const char*>(a.norm_w) + (size_t)c0 * CH * NB * 64 + piece * (Q && LINES ? 64 : Q || LINES ? 32 : 16);
     const char* gp = g0;
     bool more = there(slot), moved = false;
-    uint4 ring[D][TU], gains[RAW ? D : 1][NB];
+    uint4 ring[D][TU][CH], gains[RAW ? D : 1][CH][NB];
     const auto load = [&](int j) {
-      ring[j][0] = load_weights<B16>(lp);
-      if constexpr (TU == 2) ring[j][TU - 1] = load_weights<B16>(lp + to_up);
-      if constexpr (RAW) {
 #pragma unroll
-        for (int q = 0; q < NB; ++q) gains[j][q] = load16(gp + q * 16);
+      for (int h = 0; h < CH; ++h) {
+        ring[j][0][h] = load_weights<B16 || LINES>(lp + h * to_half);
+        if constexpr (TU == 2) ring[j][TU - 1][h] = load_weights<B16 || LINES>(lp + to_up + h * to_half);
+        if constexpr (RAW) {
+#pragma unroll
+          for (int q = 0; q < NB; ++q) gains[j][h][q] = load16(gp + (h * NB + q) * 16);
+        }
       }
       if (++lc < mine) {
         lp += step;
-        gp += NB * 64;
+        gp += CH * NB * 64;
       }
       if (lc == round && more) {
         ++li;
@@ -537,8 +577,8 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
       }
     };
     const int col = spare ? min(tok & 7, T - 1) : tc;
-    const char* xlane = xs + (spare && tok >= 8 ? plane : 0) + (size_t)c0 * NB * T * 64 +
-                        (Q ? ((size_t)(piece >> 1) * T + col) * 64 + (piece & 1) * 32 : (size_t)col * 64 + piece * 16);
+    const char* xlane = xs + (spare && tok >= 8 ? plane : 0) + (size_t)c0 * CH * NB * T * 64 +
+                        act_offset<Q, LINES>(piece, col, T);
     int uc = 0;
     bool alive = true, ended = false;
     f32x4_t acc[TU];
@@ -547,23 +587,30 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
     const auto work = [&](int j) {
       if (!alive) return;
       if (uc < mine) {
-        uint4 b[NB];
+        if constexpr (LINES) {
 #pragma unroll
-        for (int q = 0; q < NB; ++q) b[q] = *reinterpret_cast<const uint4*>(xlane + (size_t)uc * NB * T * 64 + q * 16);
-        if constexpr (RAW) {
-          uint4 lo[NB];
-#pragma unroll
-          for (int q = 0; q < NB; ++q) two_terms<Tr>(b[q], gains[j][q], b[q], lo[q]);
-#pragma unroll
-          for (int q = 0; q < TU; ++q) acc[q] = mma_chunk<Tr, Q>(ring[j][q], lo, acc[q]);
+          for (int q = 0; q < TU; ++q) change_halves(ring[j][q][0], ring[j][q][CH - 1]);
         }
+        const char* const from = xlane + (size_t)uc * CH * NB * T * 64;
 #pragma unroll
-        for (int q = 0; q < TU; ++q) acc[q] = mma_chunk<Tr, Q>(ring[j][q], b, acc[q]);
-        if (EB == 2 && !RAW && second) {
+        for (int h = 0; h < CH; ++h) {
+          uint4 b[NB];
 #pragma unroll
-          for (int q = 0; q < NB; ++q)
-            b[q] = *reinterpret_cast<const uint4*>(xlane + plane + (size_t)uc * NB * T * 64 + q * 16);
-          acc[0] = mma_chunk<Tr, Q>(ring[j][0], b, acc[0]);
+          for (int q = 0; q < NB; ++q) b[q] = *reinterpret_cast<const uint4*>(from + (h * NB + q) * 16);
+          if constexpr (RAW) {
+            uint4 lo[NB];
+#pragma unroll
+            for (int q = 0; q < NB; ++q) two_terms<Tr>(b[q], gains[j][h][q], b[q], lo[q]);
+#pragma unroll
+            for (int q = 0; q < TU; ++q) acc[q] = mma_chunk<Tr, Q>(ring[j][q][h], lo, acc[q]);
+          }
+#pragma unroll
+          for (int q = 0; q < TU; ++q) acc[q] = mma_chunk<Tr, Q>(ring[j][q][h], b, acc[q]);
+          if (EB == 2 && !RAW && second) {
+#pragma unroll
+            for (int q = 0; q < NB; ++q) b[q] = *reinterpret_cast<const uint4*>(from + plane + (h * NB + q) * 16);
+            acc[0] = mma_chunk<Tr, Q>(ring[j][0][h], b, acc[0]);
+          }
         }
       }
       if (++uc == round) {
@@ -604,10 +651,11 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
 // else partial sums, which the workgroup that is done last adds up in the parts'
 // order.  The columns share each load of h, which every tile reads whole.  TWO: h's second
 // terms are loads and instructions of their own.
-template <class Tr, bool Q, bool B16, int NR, bool TWO>
+template <class Tr, bool Q, bool B16, bool LINES, int NR, bool TWO>
 __global__ __launch_bounds__(64 * kDownWaves) void decode_down_kernel(DecodeArgs a) {
   using Elt = typename Tr::T;
-  constexpr int EB = sizeof(Elt), WB = Q ? 1 : EB, NB = Q ? 2 : 1, D = NR == 1 ? 8 : 4, kCols = NR * 16;
+  constexpr int EB = sizeof(Elt), WB = Q ? 1 : EB, NB = Q ? 2 : 1, kCols = NR * 16;
+  constexpr int CH = LINES ? 2 : 1, D = (NR == 1 ? 8 : 4) / CH;  // chunks of K of a step, steps in flight
   __shared__ f32x4_t red[kDownWaves][NR][64];
   __shared__ float wts[256][kDecodeTokens];
   __shared__ float scale[Q ? 256 : 1][kCols];
@@ -625,7 +673,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void decode_down_kernel(DecodeArgs
     if (t == 0) list[n] = a.table->expert[n];
   }
   const int n_active = __builtin_amdgcn_readfirstlane(a.table->n_active);
-  const int per = F * WB / 64, total = n_active * per;  // chunks of an expert, of all
+  const int per = F * WB / 64 / CH, total = n_active * per;  // steps of an expert, of all
   const int p0 = (int)((long long)total * part / a.parts), p1 = (int)((long long)total * (part + 1) / a.parts);
   const int i0 = p0 + (int)((long long)(p1 - p0) * wave / kDownWaves);
   const int i1 = p0 + (int)((long long)(p1 - p0) * (wave + 1) / kDownWaves);
@@ -641,11 +689,11 @@ __global__ __launch_bounds__(64 * kDownWaves) void decode_down_kernel(DecodeArgs
 #pragma unroll
   for (int q = 0; q < NR; ++q) sum[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   if (i0 < i1) {
-    const Rows<B16> rows{(size_t)F * WB};
-    constexpr int step = Rows<B16>::step;
-    const char* base = static_cast<const char*>(a.w_down) + rows.at(o0 + tok) + piece * 16;
+    const Rows<B16, LINES> rows{(size_t)F * WB};
+    constexpr int step = Rows<B16, LINES>::step;
+    const char* base = static_cast<const char*>(a.w_down) + (LINES ? rows.at(o0 + (lane & 7)) + (lane >> 3) * 16 : rows.at(o0 + tok) + piece * 16);
     const size_t tile_bytes = 16 * rows.row_bytes, expert_bytes = (size_t)d * rows.row_bytes;
-    const int cols = a.h_low ? 2 * T : T, bstep = cols * 64 * NB;
+    const int cols = a.h_low ? 2 * T : T, bstep = cols * 64 * NB * CH;
     const bool spare = !TWO && a.h_low;
     const int wcol = spare ? tok & 7 : tok;
     // h's column for this lane: its token's, or, where that did not choose the expert,
@@ -655,17 +703,19 @@ __global__ __launch_bounds__(64 * kDownWaves) void decode_down_kernel(DecodeArgs
       const int any = max(__ffsll((unsigned long long)__ballot(has)) - 1, 0) & (spare ? 7 : 15);
       const int col = (has ? wcol : any) + (spare && tok >= 8 ? T : 0);
       return static_cast<const char*>(a.h) +
-             (Q ? ((size_t)(piece >> 1) * cols + col) * 64 + (piece & 1) * 32 : (size_t)col * 64 + piece * 16);
+             act_offset<Q, LINES>(piece, col, cols);
     };
     int ln = i0 / per, lc = i0 % per, li = i0;
     const char* lp = base + list[ln] * expert_bytes + (size_t)lc * step;
     const char* bp = column(ln) + (size_t)i0 * bstep;
-    uint4 ring[D][NR], act[D][NB], low[D][NB];
+    uint4 ring[D][NR][CH], act[D][CH * NB], low[D][CH * NB];
     const auto load = [&](int j) {
 #pragma unroll
-      for (int q = 0; q < NR; ++q) ring[j][q] = load_weights<B16>(lp + q * tile_bytes);
+      for (int q = 0; q < NR; ++q)
 #pragma unroll
-      for (int q = 0; q < NB; ++q) {
+        for (int h = 0; h < CH; ++h) ring[j][q][h] = load_weights<B16 || LINES>(lp + q * tile_bytes + h * 8 * rows.row_bytes);
+#pragma unroll
+      for (int q = 0; q < CH * NB; ++q) {
         act[j][q] = load16(bp + q * 16);
         if constexpr (TWO) low[j][q] = load16(bp + (size_t)T * 64 + q * 16);
       }
@@ -701,8 +751,12 @@ __global__ __launch_bounds__(64 * kDownWaves) void decode_down_kernel(DecodeArgs
     const auto work = [&](int j) {
 #pragma unroll
       for (int q = 0; q < NR; ++q) {
-        acc[q] = mma_chunk<Tr, Q>(ring[j][q], act[j], acc[q]);
-        if constexpr (TWO) acc[q] = mma_chunk<Tr, Q>(ring[j][q], low[j], acc[q]);
+        if constexpr (LINES) change_halves(ring[j][q][0], ring[j][q][CH - 1]);
+#pragma unroll
+        for (int h = 0; h < CH; ++h) {
+          acc[q] = mma_chunk<Tr, Q>(ring[j][q][h], pick<NB>(act[j], h), acc[q]);
+          if constexpr (TWO) acc[q] = mma_chunk<Tr, Q>(ring[j][q][h], pick<NB>(low[j], h), acc[q]);
+        }
       }
       ++since;
       if (++c == per) {
@@ -795,39 +849,44 @@ hipError_t decode_t(DecodeArgs a, hipStream_t stream) {
   const int64_t units = (int64_t)std::min(a.E, a.T * a.k) * (a.F / (raw ? 2 * kUnitCols : kUnitCols));
   const dim3 grid((unsigned)std::min<int64_t>(units, kMaxGrid));
   const auto up = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), lds, stream, a); };
-  const auto up_raw = [&]() {  // (rows so wide route up to 7 experts in this kernel and more of them apart)
+  const auto up_of = [&](auto lines) {
+    constexpr bool L = decltype(lines)::value;
     if constexpr (EB == 2) {
-      if (a.E <= 64)
-        up(decode_up_kernel<Tr, Q, B16, 1, 1, true>);
-      else
-        up(decode_up_kernel<Tr, Q, B16, 1, 4, true>);
+      if (raw && a.E <= 64)  // (rows so wide route up to 7 experts in this kernel and more of them apart)
+        return up(decode_up_kernel<Tr, Q, B16, L, 1, 1, true>);
+      if (raw) return up(decode_up_kernel<Tr, Q, B16, L, 1, 4, true>);
     }
+    if (a.E <= 16) return up(decode_up_kernel<Tr, Q, B16, L, 1, 1, false>);
+    if (a.E <= 64) return up(decode_up_kernel<Tr, Q, B16, L, 4, 1, false>);
+    up(decode_up_kernel<Tr, Q, B16, L, 4, 4, false>);
   };
-  if (raw)
-    up_raw();
-  else if (a.E <= 16)
-    up(decode_up_kernel<Tr, Q, B16, 1, 1, false>);
-  else if (a.E <= 64)
-    up(decode_up_kernel<Tr, Q, B16, 4, 1, false>);
-  else
-    up(decode_up_kernel<Tr, Q, B16, 4, 4, false>);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
   const dim3 tiles(a.d / decode_down_cols(a.T, a.d), a.parts);
   const auto down = [&](auto kernel) { hipLaunchKernelGGL(kernel, tiles, dim3(64 * kDownWaves), 0, stream, a); };
-  if constexpr (EB == 2) {
-    if (a.T > 8) {
-      if (decode_down_cols(a.T, a.d) == 16)
-        down(decode_down_kernel<Tr, Q, B16, 1, true>);
-      else
-        down(decode_down_kernel<Tr, Q, B16, 4, true>);
-      return hipGetLastError();
+  const auto down_of = [&](auto lines) {
+    constexpr bool L = decltype(lines)::value;
+    const bool narrow = decode_down_cols(a.T, a.d) == 16;
+    if constexpr (EB == 2) {
+      if (a.T > 8 && narrow) return down(decode_down_kernel<Tr, Q, B16, L, 1, true>);
+      if (a.T > 8) return down(decode_down_kernel<Tr, Q, B16, L, 4, true>);
     }
-  }
-  if (decode_down_cols(a.T, a.d) == 16)
-    down(decode_down_kernel<Tr, Q, B16, 1, false>);
-  else
-    down(decode_down_kernel<Tr, Q, B16, 4, false>);
+    if (narrow) return down(decode_down_kernel<Tr, Q, B16, L, 1, false>);
+    down(decode_down_kernel<Tr, Q, B16, L, 4, false>);
+  };
+  // row-major rows in whole lines: all but E4M3 rows of an odd number of 64 bytes
+  const auto by_width = [&](int row, auto&& of) {
+    if constexpr (B16)
+      of(std::false_type{});
+    else if constexpr (!Q)
+      of(std::true_type{});
+    else if (row % 128 == 0)
+      of(std::true_type{});
+    else
+      of(std::false_type{});
+  };
+  by_width(a.d, up_of);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  by_width(a.F, down_of);
   return hipGetLastError();
 }
 

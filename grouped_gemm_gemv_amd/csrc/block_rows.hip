@@ -86,7 +86,7 @@ __device__ __forceinline__ float element(const void* p, size_t i) {
 
 // The sum, and a norm behind it, one row at a time: NT threads of a row, V 16-byte chunks
 // each.  Bound by memory: 4096 x 4096 bf16 with both norms, a gate a token and dropout takes
-// 26.4 us for 134 MB, 5.1 TB/s with its ramp; a norm alone 11.4 in a loop of calls, 5.9 TB/s.
+// 25 to 26 us for 134 MB, 5.1 to 5.5 TB/s with its ramp; a norm alone 11.4 in a loop of calls, 5.9 TB/s.
 template <class Tr, int NT, int V>
 __global__ __launch_bounds__(block_of(NT)) void residual_kernel(ResidualArgs a) {
   constexpr int EPC = Tr::EPC, G = block_of(NT) / NT;

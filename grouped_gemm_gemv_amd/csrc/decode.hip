@@ -8,9 +8,10 @@
 // no dispatch arrays, the matrix cores have the room (16 rows x 64 bytes of weights
 // per instruction: at the rate of HBM one in 90 cycles of a compute unit), and the
 // work is a single stream over the active experts' weights, which is what bounds
-// it.  Mixtral shape, one token, blocked bf16: 77 us and 38 us of the two kernels for
-// 470 and 235 MB, 6.1 and 6.2 TB/s; 8 tokens with E4M3 weights: 130 and 71 us for 0.85 and
-// 0.42 GB, 6.5 and 6.0 TB/s (a streaming read alone reaches 7.0).
+// it.  Mixtral shape, one token, blocked bf16: 77 us and 37 us of the two kernels for
+// 470 and 235 MB, 6.1 and 6.3 TB/s; 8 tokens with E4M3 weights: 133 and 70 us for 0.85 and
+// 0.42 GB, 6.4 and 6.1 TB/s (a streaming read alone reaches 7.0); 64 experts of 2048 with
+// row-major weights, 4 tokens: 47 and 23 us, of which 6 pass before the first weights.
 //
 //   decode_up_kernel    every workgroup norms the tokens into LDS, routes them
 //                       (all of them, each workgroup for itself: E d weights

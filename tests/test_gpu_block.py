@@ -351,6 +351,25 @@ def test_in_place_results_are_the_same():
     assert np.array_equal(bits(dout), bits(g["dres"])) and np.array_equal(bits(dy), bits(g["dy"]))
 
 
+@pytest.mark.parametrize("gate", ["token", "full"])
+def test_arrays_at_their_least_alignment(gate):
+    def shifted(t, by):
+        b = torch.zeros(t.numel() * t.element_size() + by + 64, dtype=torch.uint8, device="cuda")
+        return b[by:by + t.numel() * t.element_size()].view(t.dtype).view(t.shape).copy_(t)
+
+    c = Case(9, 448, gate=gate, p=0.3, seed=17)
+    out, n = c.forward()
+    g = c.backward(out)
+    for name in ("res", "y", "post", "next", "dout", "dn"):
+        setattr(c, name, shifted(getattr(c, name), 16))
+    c.gate, c.rng = shifted(c.gate, 2 if gate == "token" else 16), shifted(c.rng, 8)
+    out2, n2 = c.forward()
+    g2 = c.backward(shifted(out2, 16))
+    assert np.array_equal(bits(out), bits(out2)) and np.array_equal(bits(n), bits(n2))
+    for name in g:
+        assert np.array_equal(bits(g[name]), bits(g2[name])), name
+
+
 def test_rows_behind_the_last_stay_as_they_were():
     import grouped_gemm_gemv_amd as M
     T, d = 5, 192

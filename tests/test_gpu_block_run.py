@@ -236,3 +236,45 @@ def test_dealt_units_give_the_same_bits(T, d, E, k, F, dtype, fp8, layout):
     err = (first.double() - (x + y)).norm(dim=1)
     half = K.U["bf16"] if dtype == "bf16" else 64 * K.U32
     assert (err <= 3 * half * y.norm(dim=1) + half * (x + y).norm(dim=1)).all(), err.max()
+
+
+def test_captured_graphs_may_share_a_workspace():
+    """Replays in turn on one stream, with eager calls on the same workspaces between them: none leaves anything that
+    the next one needs or minds."""
+    import grouped_gemm_gemv_amd as M
+    bf = torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(9)
+
+    def rand(*shape, std=1.0):
+        return (torch.randn(*shape, generator=gen, device="cuda") * std).to(bf)
+
+    shapes = [M.Shape(T, 256, E, 2, 192, 0, bf) for T, E in ((3, 4), (14, 20))]
+    ws = M.workspace(max(M.decode_workspace_size(s) for s in shapes))
+    gws = M.workspace(max(M.residual_workspace_size(s) for s in shapes))
+    runs = []
+    for s in shapes:
+        T, d, E, F = s.T, s.d, s.E, s.F
+        x, norm, wr = rand(T, d), rand(d), rand(E, d, std=0.1)
+        w = [rand(E, F, d, std=d**-0.5), rand(E, F, d, std=d**-0.5), rand(E, d, F, std=F**-0.5)]
+        out, dn, dx, dw = torch.empty_like(x), rand(T, d), torch.empty_like(x), torch.empty_like(norm)
+
+        def call(s=s, x=x, norm=norm, wr=wr, w=w, out=out, dn=dn, dx=dx, dw=dw):
+            M.moe_decode(s, x, norm, wr, None, None, None, *w, x, out, ws)
+            M.moe_norm_backward(s, out, norm, dn, None, dx, dw, gws)
+
+        call()
+        torch.cuda.synchronize()
+        want = [v.clone() for v in (out, dx, dw)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        runs.append((graph, call, (out, dx, dw), want))
+    for i in (0, 1, 0, 0, 1, 1, 0):
+        graph, call, got, want = runs[i]
+        for v in got:
+            v.fill_(float("nan"))
+        graph.replay()
+        runs[1 - i][1]()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), i

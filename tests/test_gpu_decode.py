@@ -296,6 +296,59 @@ def test_padded_batch_gives_the_same_rows():
     assert np.linalg.norm(a - b) <= 4 * K.U["bf16"] * np.linalg.norm(b)  # two results, each within two half steps
 
 
+def _shifted(t, by):
+    """The same values `by` bytes into an allocation."""
+    b = torch.zeros(t.numel() * t.element_size() + by + 64, dtype=torch.uint8, device="cuda")
+    v = b[by:by + t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+    return v.copy_(t)
+
+
+@pytest.mark.parametrize("dtype,fp8", [("bf16", False), ("f32", False), ("bf16", True)])
+@pytest.mark.parametrize("layout", [0, 1])
+def test_arrays_at_their_least_alignment(dtype, fp8, layout):
+    c = Case(5, 320, 6, 2, 192, dtype=dtype, fp8=fp8, layout=layout, bias=True, seed=16)
+    ids, w = torch.empty(5, 2, dtype=torch.int32, device="cuda"), torch.empty(5, 2, device="cuda")
+    want = c.run(ids, w)
+    weights = [_shifted(v, 16) for v in c.stored()]
+    c.x, c.norm, c.wr, c.res = (_shifted(v, 16) for v in (c.x, c.norm, c.wr, c.res))
+    c.bias = _shifted(c.bias, 4)
+    if fp8:
+        c.scales = [_shifted(v, 16) for v in c.scales]
+    ids2, w2, out = _shifted(ids, 4), _shifted(w, 4), _shifted(torch.zeros_like(want), 16)
+    ids2.zero_(), w2.zero_()
+    got = c.run(ids2, w2, out, weights=weights)
+    assert np.array_equal(bits(got), bits(want)) and torch.equal(ids, ids2) and torch.equal(w, w2)
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+def test_weights_past_2_31_elements(layout):
+    """The last two of 40 experts of 58.7 M elements, against a layer of those two."""
+    import grouped_gemm_gemv_amd as M
+    E, d, F = 40, 4096, 14336
+    print(f"\n[gpu] decode E={E} d={d} F={F} layout={layout}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+
+    def rand(*shape, std):
+        return (torch.randn(*shape, generator=gen, device="cuda") * std).bfloat16()
+
+    two = [rand(2, F, d, std=d**-0.5), rand(2, F, d, std=d**-0.5), rand(2, d, F, std=F**-0.5)]
+    if layout:
+        two = [M.moe_pack_blocked16(w) for w in two]
+    x, norm, w = rand(1, d, std=1.0), rand(d, std=1.0), torch.tensor([[0.75, -0.5]], device="cuda")
+    outs = []
+    for n in (2, E):
+        shape = M.Shape(1, d, n, 2, F, 0, torch.bfloat16, 0, layout)
+        big = two if n == 2 else [torch.empty((E,) + tuple(v.shape[1:]), dtype=v.dtype, device="cuda") for v in two]
+        if n == E:
+            for b, v in zip(big, two):
+                b[-2:] = v
+        ids = torch.tensor([[n - 1, n - 2]], dtype=torch.int32, device="cuda")
+        out = torch.full_like(x, float("nan"))
+        M.moe_decode(shape, x, norm, None, None, ids, w, *big, None, out, M.workspace(M.decode_workspace_size(shape)))
+        outs.append(out)
+    assert torch.isfinite(outs[0].float()).all() and np.array_equal(bits(outs[0]), bits(outs[1]))
+
+
 @pytest.mark.parametrize("name,over", [("mixtral_decode_t8", dict(d=512, F=640)), ("tiny_f32", dict(T=16)),
                                        ("mixtral_decode_t8_fp8", dict(d=512, F=640))])
 def test_agrees_with_the_layers_forward_pass(name, over):

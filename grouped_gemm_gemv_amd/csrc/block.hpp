@@ -78,7 +78,7 @@ struct DecodeTable {
 // Columns of d that a workgroup of the second kernel takes.  Up to four tokens 16, the
 // most workgroups; past them 64 where tiles and parts still fill the compute units,
 // because every tile of columns reads all of h, from L2: at the Mixtral shape one token
-// takes 118 us with 16 and 122 with 64, 8 tokens with E4M3 weights 249 and 213.
+// takes 118 us with 16 and 121 with 64, 8 tokens with E4M3 weights 215 and 205.
 constexpr int kDownWaves = 8, kDownMaxParts = 16;
 inline int decode_down_cols(int T, int d) { return T <= 4 || d < 256 / kDownMaxParts * 64 ? 16 : 64; }
 // How many workgroups share a tile's K: enough tiles and parts to fill the compute
@@ -92,10 +92,10 @@ inline int decode_parts(int64_t chunks, int d, int T) {
 // The router as a kernel of its own from this many bytes of its weights on (a quarter of it
 // for bf16 batches whose second terms have no room in LDS and are made beside the
 // products), and the 64-byte blocks of K of one workgroup of it.  Measured, apart against
-// in the first kernel: 64 experts of 2048 and one token 36.0 vs 39.5 us, of 3584 and 16
-// tokens 467 vs 479; 8 experts of 4096 and one token 118.7 vs 118.7, 16 tokens 449 vs 452.
-// And from this many bytes of the experts that may be active on, for the deal of units that
-// it makes possible (see the first kernel's main loop).
+// in the first kernel: 64 experts of 2048 and one token 35.5 vs 37.6 us, of 3584 and 16
+// tokens 467 vs 479.  And from this many bytes of the experts that may be active on, for the
+// deal of units that it makes possible (see the first kernel's main loop): 8 tokens of the
+// Mixtral shape 375 vs 385 us, with E4M3 weights 206 vs 209, one token 118.1 vs 117.6.
 constexpr int kRouteApart = 128 * 1024, kRouteBlocks = 32;
 constexpr size_t kDealApart = size_t(256) << 20;
 

@@ -205,7 +205,7 @@ __global__ __launch_bounds__(block_of(NT)) void residual_backward_kernel(Residua
   using Elt = typename Tr::T;
   constexpr int EPC = Tr::EPC, B = block_of(NT), G = B / NT;
   extern __shared__ float sums[];  // [G > 1 ? G : 0][d]
-  __shared__ float part1[2][3 * (NT / 64)], part2[NT / 64];
+  __shared__ float part1[2][3 * (NT / 64)], part2[2][NT / 64];
   const int tid = threadIdx.x % NT, group = __builtin_amdgcn_readfirstlane(threadIdx.x / NT), chunks = a.d / EPC;
   float gp[V][EPC], gn[V][EPC];  // columns' sums of dpost_w and dnext_w
 #pragma unroll
@@ -246,9 +246,10 @@ __global__ __launch_bounds__(block_of(NT)) void residual_backward_kernel(Residua
     load_row(first, xc, dnc, doc);
     load_y(first, yc);
   }
-  // (groups of one wavefront meet no barrier in the loop; larger ones are the whole workgroup;
-  // a row's first sums go to the place that the row before did not use, since a norm alone
-  // has no second barrier behind their reading)
+  // (groups of one wavefront meet no barrier in the loop; larger ones are the whole workgroup.
+  // A row may have one barrier only: the first sums' for a norm alone, the second's for a gate a
+  // token without norms.  So both go to the place that the row before did not use: a wavefront
+  // writes there again only two rows on, behind a barrier that all have reached after reading)
   int place = 0;
   for (size_t t = first; t < (size_t)a.T; t += ahead, place ^= 1) {
     const auto at = [&](const void* p) { return static_cast<const char*>(p) + t * width; };
@@ -351,7 +352,7 @@ __global__ __launch_bounds__(block_of(NT)) void residual_backward_kernel(Residua
         D[i][j] *= w[j];
       }
     }
-    if (a.post_w != nullptr || (a.gate != nullptr && !a.gate_full)) row_sum<NT>(cy, part2);
+    if (a.post_w != nullptr || (a.gate != nullptr && !a.gate_full)) row_sum<NT>(cy, part2[place]);
     if (a.gate != nullptr && !a.gate_full && a.dgate != nullptr && tid == 0) {
       const float g = slope * r2 * m * cy[0];
       if constexpr (sizeof(Elt) == 2)

@@ -356,8 +356,9 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
 
   const bool first = blockIdx.x == 0;
   if (route) {
-    // Top-k: k times the largest logit, at the lowest index that has it; a NaN ranks
-    // lowest.  What is taken becomes a NaN, which no maximum sees.
+    // Top-k: k times the largest logit, at the lowest index that has it.  What is taken
+    // becomes a NaN, which no maximum sees; so a NaN logit is not seen either, and ranks below
+    // every other, those of -inf among them: where the maximum is a NaN only such are left.
     for (int t = wave; t < T; t += kWaves) {
       float v[NQ], key[NQ];
       int slot[NQ];
@@ -365,7 +366,7 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
       for (int q = 0; q < NQ; ++q) {
         const int e = lane + 64 * q;
         v[q] = e < E ? logit[t * E + e] : 0.f;
-        key[q] = e < E ? fmaxf(v[q], -INFINITY) : NAN;
+        key[q] = e < E ? v[q] : NAN;
         slot[q] = -1;
       }
       float top = 0.f;
@@ -378,7 +379,7 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
         bool found = false;
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
-          const uint64_t at = __ballot(key[q] == m);
+          const uint64_t at = __ballot(m == m ? key[q] == m : slot[q] < 0 && lane + 64 * q < E);
           if (!found && at != 0) {
             found = true;
             if (lane == __ffsll((unsigned long long)at) - 1) {

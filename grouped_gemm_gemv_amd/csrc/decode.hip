@@ -197,6 +197,13 @@ __device__ __forceinline__ void two_terms(const uint4& x, const uint4& norm_w, u
   lo = low_terms<Tr>(v, hi);
 }
 
+// A logit and its expert's bias: one of -inf masks the expert, whatever its router row holds
+// (a NaN, or +inf, and -inf would be a NaN).
+__device__ __forceinline__ float biased(float s, const float* bias, int e) {
+  const float b = bias != nullptr ? bias[e] : 0.f;
+  return b == -INFINITY ? b : s + b;
+}
+
 // Q: E4M3 weights.  B16: the blocked order.  NE: 16-expert tiles of the router at a time; NQ: experts of a lane in
 // the choice.  RAW: x is in LDS as it is, both terms of p are made for each chunk of weights, and a unit is two
 // tiles, 16 gate rows and 16 up rows.
@@ -338,7 +345,7 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) s += red[((wave >> 2) * kWaves + w) * 64 + lane][quarter];
         const int e = e0 + i * 16 + piece * 4 + quarter;
-        if (e < E && tok < T) logit[tok * E + e] = s * inv + (a.bias != nullptr ? a.bias[e] : 0.f);
+        if (e < E && tok < T) logit[tok * E + e] = biased(s * inv, a.bias, e);
       }
       __syncthreads();
     }
@@ -349,7 +356,7 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
       float s = 0.f;
 #pragma unroll 4
       for (int r = 0; r < a.ranges; ++r) s += a.logits[(size_t)r * a.e16 * kDecodeTokens + i];
-      if (tok < T) logit[tok * E + i / kDecodeTokens] = s * inv + (a.bias != nullptr ? a.bias[i / kDecodeTokens] : 0.f);
+      if (tok < T) logit[tok * E + i / kDecodeTokens] = biased(s * inv, a.bias, i / kDecodeTokens);
     }
     __syncthreads();
   }
@@ -390,17 +397,22 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
         }
       }
       float ex[NQ], sum = 0.f;
+      bool nan = false;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         ex[q] = slot[q] >= 0 && v[q] != -INFINITY ? expf(v[q] - top) : 0.f;
         sum += ex[q];
+        nan |= v[q] != v[q];
       }
       sum = wave_fold(sum, [](float x, float y) { return x + y; });
+      // no expert with a number above -inf: none at all where every one is masked, but what has
+      // a NaN (that of x, for one) is not to be taken for that
+      const float none = __ballot(nan) != 0 ? NAN : 0.f;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         if (slot[q] < 0) continue;
         const int e = lane + 64 * q;
-        const float w = sum == 0.f ? 0.f : ex[q] / sum;  // (every expert masked by a bias of -inf)
+        const float w = sum == 0.f ? none : ex[q] / sum;
         wt[e * T + t] = w;
         if (w != 0.f) chosen[e] = 1;
         if (first && a.ids != nullptr) a.ids[t * a.k + slot[q]] = e;

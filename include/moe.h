@@ -543,9 +543,10 @@ moe_status_t moe_dropout(const void* x, int64_t n, int dtype, float p, const uin
  *    141312 bytes (16 tokens of 4096 bf16 with up to 80 experts, 8 of 7168 with
  *    256); else MOE_ERR_UNSUPPORTED, and moe_forward takes the batch.
  *  - With w_router, topk_ids and topk_w [T,k] receive the routing, or are NULL.
- *    Equal logits: the lower index.  A NaN logit ranks below every other, -inf too, and
- *    where slots are left for one the token's weights are NaN; an expert
- *    with a bias of -inf is left out, and a token that has no other gets no expert.
+ *    Equal logits: the lower index.  An expert with a bias of -inf has that as its logit,
+ *    whatever its router row holds, and weight 0; where all are, the token gets no
+ *    expert.  A NaN logit ranks below every other, -inf too; where slots are left for one,
+ *    or no other logit is above -inf, the token's weights are NaN.
  *  - Without w_router they are read.  Ids outside [0, E) have no expert; an expert
  *    given twice counts twice.  Experts that no token has a weight other than 0 of
  *    are not read, and a token takes nothing from an expert that it has weight 0 of,

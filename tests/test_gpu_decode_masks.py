@@ -63,3 +63,43 @@ def test_a_nan_has_the_slots_that_are_left(T, d, E, F):
     c.wr[:] = NAN
     out, ids, w = _routing(c)
     assert (ids == np.arange(6)).all() and np.isnan(w).all() and torch.isnan(out.float()).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,E,F", ROUTERS)
+def test_a_masked_experts_router_row_may_hold_anything(T, d, E, F, dtype):
+    """A bias of -inf masks an expert whatever its logit would have been: NaN and +inf plus -inf are NaN, and with fewer
+    experts left than slots that would be chosen."""
+    if dtype == "f32" and T * d * 4 > 131072:
+        T = 131072 // 4 // d
+    print(f"\n[gpu] decode masked rows T={T} d={d} E={E} {dtype}", flush=True)
+    c = Case(T, d, E, 3, F, dtype=dtype, bias=True, seed=E)
+    masked = [e for e in range(E) if e not in (2, E - 1)]
+    c.bias[masked] = -INF
+    want, wids, ww = _routing(c)
+    assert (ww[:, 2] == 0).all() and (wids[:, 2] == 0).all() and torch.isfinite(want.float()).all()
+    for bad in (NAN, INF, -INF):
+        c.wr[masked] = bad
+        out, ids, w = _routing(c)
+        assert np.array_equal(ids, wids) and np.array_equal(w, ww), bad
+        assert np.array_equal(bits(out), bits(want)), bad
+    c.wr[masked[0]] = c.wr[2]
+    c.wr[masked[0], 0], c.x[:, 0] = INF, 1.0  # a logit of +inf
+    c.bias[:] = -INF
+    out, ids, w = _routing(c)
+    assert (w == 0).all() and np.array_equal(bits(out), bits(c.res))
+
+
+@pytest.mark.parametrize("T,d,E,F", ROUTERS)
+def test_a_nan_in_x_shows_beside_masked_experts(T, d, E, F):
+    """The experts that are not masked have a NaN for that token: masked ones fill its slots, but its row is a NaN."""
+    print(f"\n[gpu] decode NaN in x and masked T={T} d={d} E={E}", flush=True)
+    c = Case(T, d, E, 2, F, bias=True, seed=E)
+    c.bias[:] = -INF
+    c.bias[[1, E - 1]] = 0.5
+    want = c.run()
+    c.x[T - 1, 7] = NAN
+    out, ids, w = _routing(c)
+    assert torch.isnan(out[T - 1].float()).all() and np.isnan(w[T - 1]).all()
+    assert ids.min() >= 0 and ids.max() < E
+    assert np.array_equal(bits(out)[:T - 1], bits(want)[:T - 1]) and torch.isfinite(want.float()).all()

@@ -2,9 +2,10 @@
 what a kernel's fp32 arithmetic and one rounding of each output may be off by.
 
 Inputs are float64 arrays that hold the device's values.  A function returns (value, bound) for each output.  Bounds:
-`S` fp32 operations lie on any path from an input to a sum over a row (up to 32 elements of a thread, 6 exchanges of a
-wavefront, 8 wavefronts, and the square root, division, exponential and products around them, each at most 2^-24, the
-exponential at most 4 of those), so each term of such a sum is off by at most S 2^-24 of its magnitude.
+`S` fp32 operations lie on any path from an input to a sum over a row (up to 16 elements of a thread, 6 exchanges of a
+wavefront, up to 16 wavefronts one after another, which is 38, and twice as many for the square root, division,
+exponential and products around them, each at most 2^-24, the exponential at most 4 of those), so each term of such a sum
+is off by at most S 2^-24 of its magnitude.
 """
 from __future__ import annotations
 
@@ -135,17 +136,20 @@ def residual_backward(x, y, post_w, gate, mask, next_w, dout, dn, eps, scale, dt
     return outs
 
 
-def decode(x, norm_w, eps, ids, w, wg, wu, wd, res, scale, dtype, e_w=0.0):
+def decode(x, norm_w, eps, ids, w, wg, wu, wd, res, scale, dtype, e_w=0.0, terms=1):
     """out and its bound for a routing (ids [T, k] and weights [T, k], each off by at most e_w of itself); weights
-    [E, F, d], [E, F, d], [E, d, F].  m and h are rounded to the type once (at most half a step each)."""
+    [E, F, d], [E, F, d], [E, d, F].  m and h are kept in `terms` numbers of the type, each of which takes what rounding
+    left of the one before (half a step of it at most): 1 is the bound of a layer that rounds both, 2 of one that does not."""
     T, d = x.shape
     F = wg.shape[1]
     u = U[dtype]
+    u_in = u ** terms
     m = x * rms(x, eps) * norm_w if norm_w is not None else x
-    e_m = (u + S) * np.abs(m) if norm_w is not None else np.zeros_like(m)
+    e_m = (u_in + S) * np.abs(m) if norm_w is not None else np.zeros_like(m)
     out = np.zeros((T, d))
     bound = np.zeros((T, d))
-    k_up, k_down = (d + 64) * U32, (F * ids.shape[1] + 64) * U32  # products added one after another
+    # products added one after another; those of second terms are as many again, and 2^-8 of the first ones'
+    k_up, k_down = [(n + (terms - 1) * (1 + 2 * u) * n + 64) * U32 for n in (d, F * ids.shape[1])]
     for t in range(T):
         for j, expert in enumerate(ids[t]):
             if not 0 <= expert < wg.shape[0] or w[t, j] == 0:
@@ -157,7 +161,7 @@ def decode(x, norm_w, eps, ids, w, wg, wu, wd, res, scale, dtype, e_w=0.0):
             sg = sigmoid(g)
             h = g * sg * up
             # |silu'| is at most 1.1
-            e_h = 1.1 * e_g * (np.abs(up) + e_u) + np.abs(g * sg) * e_u + (u + EXP) * np.abs(h)
+            e_h = 1.1 * e_g * (np.abs(up) + e_u) + np.abs(g * sg) * e_u + (u_in + EXP) * np.abs(h)
             y = wd[expert] @ h
             e_y = ad @ (e_h + k_down * np.abs(h))
             out[t] += w[t, j] * y

@@ -365,7 +365,7 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
   if (route) {
     // Top-k: k times the largest logit, at the lowest index that has it.  What is taken
     // becomes a NaN, which no maximum sees; so a NaN logit is not seen either, and ranks below
-    // every other, those of -inf among them: where the maximum is a NaN only such are left.
+    // every other, those of -inf among them: where no key is the maximum only such are left.
     for (int t = wave; t < T; t += kWaves) {
       float v[NQ], key[NQ];
       int slot[NQ];
@@ -384,9 +384,8 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
         m = wave_fold(m, [](float x, float y) { return fmaxf(x, y); });
         if (j == 0) top = m;
         bool found = false;
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          const uint64_t at = __ballot(m == m ? key[q] == m : slot[q] < 0 && lane + 64 * q < E);
+        const auto take = [&](int q, bool candidate) {  // the first lane that has one
+          const uint64_t at = __ballot(candidate);
           if (!found && at != 0) {
             found = true;
             if (lane == __ffsll((unsigned long long)at) - 1) {
@@ -394,7 +393,12 @@ __global__ __launch_bounds__(64 * kWaves) void decode_up_kernel(DecodeArgs a) {
               key[q] = NAN;
             }
           }
-        }
+        };
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) take(q, key[q] == m);
+        if (found) continue;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) take(q, slot[q] < 0 && lane + 64 * q < E);
       }
       float ex[NQ], sum = 0.f;
       bool nan = false;

@@ -601,7 +601,8 @@ def moe_decode(shape: Shape, x, norm_w, w_router, bias, topk_ids, topk_w, w_gate
                eps: float = 1e-6, scale: float = 1.0, stream=None):
     """The layer for up to 16 tokens, with the norm before it (norm_w) and the residual behind it (res; out may be
     res): out = res + scale layer(x / rms(x) norm_w).  norm_w, bias and res may be None.  With w_router the routing is
-    computed, and written to topk_ids and topk_w [T, k] where they are given; without it they are read."""
+    computed, and written to topk_ids and topk_w [T, k] where they are given; without it they are read.  9 to 16 wide
+    tokens and few, large experts are faster with moe_norm and moe_forward."""
     weights = _weights(shape, "w", w_gate, w_up, w_down, x.device)
     _decode("moe_decode", shape, x, norm_w, w_router, bias, topk_ids, topk_w, weights, res, out, ws, eps, scale, stream)
 

@@ -77,8 +77,11 @@ struct DecodeTable {
 };
 // Columns of d that a workgroup of the second kernel takes.  Up to four tokens 16, the
 // most workgroups; past them 64 where tiles and parts still fill the compute units,
-// because every tile of columns reads all of h, from L2: at the Mixtral shape one token
-// takes 118 us with 16 and 121 with 64, 8 tokens with E4M3 weights 215 and 205.
+// because every tile of columns reads all of h, from L2.  With 16 and with 64, Mixtral shape:
+// one token 117 and 120 us, 5 tokens 272 and 275, 8 379 and 378, 16 465 and 450, with E4M3
+// weights 1 token 69.6 and 70.4, 4 153 and 150, 8 216 and 207, 16 300 and 269; 64 experts of 2048,
+// 4 tokens 70.0 and 71.2, 8 112 and 115, 16 155.6 and 155.0; of 1024, 8 tokens 62.5 and 65.4, 16
+// 100 and 102 (16 columns would do there); of 512, 16 tokens 59.5 and 65.7.
 constexpr int kDownWaves = 8, kDownMaxParts = 16;
 inline int decode_down_cols(int T, int d) { return T <= 4 || d < 256 / kDownMaxParts * 64 ? 16 : 64; }
 // How many workgroups share a tile's K: enough tiles and parts to fill the compute

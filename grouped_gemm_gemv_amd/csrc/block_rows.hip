@@ -1,7 +1,9 @@
 // The operators around the layer: the norm before a block, the norm, gate,
 // dropout and residual scale behind it, and their gradients.  All of them move
 // whole rows once and are bound by that; a row stays in the registers of the
-// threads that work on it, and every sum is fp32 in a fixed order.
+// threads that work on it, and every sum is fp32 in a fixed order.  (Gradients of wide rows
+// need more registers than 1024 threads have: past 8192 elements of bf16 64 of them spill, in
+// fp32 12 past 4096 and 90 past 8192.)
 #include <algorithm>
 
 #include "block.hpp"
@@ -199,7 +201,8 @@ __global__ __launch_bounds__(block_of(NT)) void residual_kernel(ResidualArgs a) 
 // The sums over tokens: each thread keeps its columns' over the rows that its
 // workgroup works, rows in ascending order.  4096 x 4096 bf16 with both norms, a gate a token
 // and dropout: 201 MB and 17 of partial sums in 47 to 51 us, 4.5 TB/s; the generator is 2.5 us of
-// that and the sums over a row most of the rest of what memory does not take.
+// that and the sums over a row most of the rest of what memory does not take.  With what spills it
+// is slower by far (both kernels, 201 to 203 MB: 2048 x 8192 45 us, 2048 x 8256 173, 1024 x 16384 120).
 template <class Tr, int NT, int V>
 __global__ __launch_bounds__(block_of(NT)) void residual_backward_kernel(ResidualBackwardArgs a) {
   using Elt = typename Tr::T;
@@ -557,9 +560,10 @@ int residual_backward_groups(int T, int d) {
   int threads = 64;                  // of a workgroup, as MOE_ROW_SHAPES has them
   while (threads < 1024 && d > threads * 8) threads *= 2;
   threads = block_of(threads);
-  // sixteen wavefronts for each compute unit, all that their registers allow: half or twice
-  // as many take 58 and 64 us for 16384 rows of 1024 bf16 against 54, and 62 and 65 against
-  // 53 for 4096 of 4096
+  // sixteen wavefronts for each compute unit, all that their registers allow (fp32 rows of 2112
+  // to 4096 take 149 of them, so that eight are resident and the workgroups come in two rounds):
+  // half or twice as many take 58 and 64 us for 16384 rows of 1024 bf16 against 54, and 62 and 65
+  // against 53 for 4096 of 4096
   return std::min((T - 1) / per + 1, 256 * 1024 / threads);
 }
 
